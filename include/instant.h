@@ -384,6 +384,116 @@ instant_status instant_reconstruction_error(const void* t, const void* Q, const 
                                            double* err2_out, double* energy_out,
                                            void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Operators of an MLP block trained with activations kept in 8 bits: a
+ * root-mean-square norm, linear layers with their bias, activation and
+ * residual, and the gradients that read the 8-bit checkpoints.  The notes page
+ * has no counterpart; they stand next to the low-rank path for the layers
+ * around its linears.
+ *
+ * Checkpoint of t [rows, C]: groups of 128 channels of a row (the last may be
+ * shorter), each with a power-of-two scale 2^k, the smallest with
+ * max|t| / 2^k <= 127 (k in -120..121), and codes q = round(t / 2^k), ties to
+ * even, from t in fp32.
+ *   q  [rows, ldq]            int8, ldq = C rounded up to a multiple of 16
+ *                             (the padding codes may be written, are never read)
+ *   s  [ceil(C / 128), rows]  uint8, k + 127; 255 marks a group that holds an
+ *                             infinity or a NaN: all of it reads back as NaN
+ * q 2^k is exact in bf16.  q must be 16-byte aligned, s need not be.
+ *
+ * Sums and statistics are fp32; every output is rounded once.  bf16: widths
+ * are multiples of 8; f32: any width.  Tensors of dtype dt unless stated.
+ * ------------------------------------------------------------------------ */
+
+/* Activations: gelu is z Phi(z) (the erf form), silu is z / (1 + exp(-z)). */
+typedef enum {
+  INSTANT_ACT_NONE = 0,
+  INSTANT_ACT_RELU = 1,
+  INSTANT_ACT_GELU = 2,
+  INSTANT_ACT_SILU = 3
+} instant_act;
+
+/*
+ * Checkpoint of a tensor, and the values a checkpoint stands for.
+ *   x [rows, C] dtype dt (read by pack, written by unpack)
+ */
+instant_status instant_ckpt_pack(const void* x, void* q, void* s, int rows, int C,
+                                 instant_dtype dt, void* stream);
+instant_status instant_ckpt_unpack(const void* q, const void* s, void* x, int rows, int C,
+                                   instant_dtype dt, void* stream);
+
+#define INSTANT_RMS_NORM_MAX_C 32768
+
+/*
+ * Root-mean-square norm with the residual's addition:
+ *   h = x + residual,  r = (mean_j h_j^2 + eps)^(-1/2),  u = h r,  y = u gamma
+ * The norm is taken of the unrounded h.
+ *   x, residual (may be NULL: h = x), h (may be NULL), y (may be NULL when q is
+ *   given)  [rows, C];  gamma [C]
+ *   q, s   checkpoint of u, or both NULL
+ *   r      [rows] fp32, or NULL (the backward needs q, s and r)
+ * h may be x or residual.  Limits: C <= INSTANT_RMS_NORM_MAX_C, eps >= 0.
+ */
+instant_status instant_rms_norm(const void* x, const void* residual, const void* gamma, void* h,
+                                void* y, void* q, void* s, float* r, int rows, int C, float eps,
+                                instant_dtype dt, void* stream);
+
+/*
+ * Its gradient, from the checkpoint of u alone:
+ *   d = gy gamma,  c = mean_j(d_j u_j),  gx = r (d - u c) + residual,
+ *   ggamma (+)= sum over rows of gy u
+ *   gy, gx, residual (may be NULL; the gradient that bypassed the norm) [rows, C]
+ *   ggamma [C] fp32 (written, or added to when accumulate != 0)
+ *   ws     device scratch of instant_rms_norm_backward_workspace_bytes(rows, C)
+ *          bytes, 16-byte aligned; contents are overwritten
+ * gx may be gy or residual.  The sums over rows are taken in a fixed order.
+ */
+instant_status instant_rms_norm_backward(const void* gy, const void* q, const void* s, const float* r,
+                                         const void* gamma, const void* residual, void* gx,
+                                         float* ggamma, int accumulate, void* ws, size_t ws_bytes,
+                                         int rows, int C, instant_dtype dt, void* stream);
+size_t instant_rms_norm_backward_workspace_bytes(int rows, int C);
+
+/*
+ * Linear layer with its epilogue:
+ *   z = x w^T + bias,  y = act(z) + residual
+ *   x [rows, Cx], w [Cy, Cx], bias [Cy] or NULL, residual [rows, Cy] or NULL
+ *   y [rows, Cy], or NULL when yq is given
+ *   zq, zs  checkpoint of z, yq, ys  checkpoint of y (either may be NULL, in pairs)
+ * y may be residual.  One launch; from a single token (generation) to training batches.
+ */
+instant_status instant_linear_act(const void* x, const void* w, const void* bias, const void* residual,
+                                  void* y, void* zq, void* zs, void* yq, void* ys, int rows, int Cx,
+                                  int Cy, instant_act act, instant_dtype dt, void* stream);
+
+/*
+ * Gradient through a linear layer and the activation before it:
+ *   gx = (gy w) act'(z) + residual
+ *   gy [rows, Cy], w [Cy, Cx], gx and residual (may be NULL) [rows, Cx]
+ *   zq, zs  checkpoint of the activation's input z [rows, Cx] (NULL only for
+ *           INSTANT_ACT_NONE)
+ * relu'(0) is 0.  gx may be residual.
+ */
+instant_status instant_linear_act_grad(const void* gy, const void* w, const void* zq, const void* zs,
+                                       const void* residual, void* gx, int rows, int Cx, int Cy,
+                                       instant_act act, instant_dtype dt, void* stream);
+
+/*
+ * Weight and bias gradient of a linear layer from the checkpoint of its input:
+ *   gw (+)= (gy^T v) diag(col_scale),  gb (+)= sum over rows of gy
+ * with v the checkpoint's values.  col_scale lets a norm's checkpoint of u
+ * serve a layer whose input was u gamma.
+ *   gy [rows, Cy];  q, s checkpoint of [rows, Cx];  col_scale [Cx] or NULL
+ *   gw [Cy, Cx] fp32, gb [Cy] fp32 or NULL (written, or added to)
+ *   ws  device scratch of instant_ckpt_grad_w_workspace_bytes(rows, Cx, Cy)
+ *       bytes, 16-byte aligned (may be NULL without gb); contents are overwritten
+ * The sums over rows are taken in a fixed order.
+ */
+instant_status instant_ckpt_grad_w(const void* gy, const void* q, const void* s, const void* col_scale,
+                                   float* gw, float* gb, int accumulate, void* ws, size_t ws_bytes,
+                                   int rows, int Cx, int Cy, instant_dtype dt, void* stream);
+size_t instant_ckpt_grad_w_workspace_bytes(int rows, int Cx, int Cy);
+
 /* Reads (and clears when clear != 0) the sticky device status word after
  * synchronising `stream`; INSTANT_OK when no device-side wait ran out. */
 instant_status instant_device_status(int clear, void* stream);

@@ -15,6 +15,9 @@ LIB_PATH = os.path.join(_HERE, "libinstant.so")
 INSTANT_F32 = 0
 INSTANT_BF16 = 1
 
+# instant_act
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
+
 # size of the library's fixed g_hat_x array (INSTANT_GRAD_X_STATIC_SCRATCH_BYTES)
 GRAD_X_STATIC_SCRATCH_BYTES = 8 << 20
 
@@ -108,6 +111,16 @@ _PROTOS = {
     "instant_reconstruction_error": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i,
                                           ctypes.POINTER(ctypes.c_double),
                                           ctypes.POINTER(ctypes.c_double), _vp, _sz, _vp]),
+    "instant_ckpt_pack": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp]),
+    "instant_ckpt_unpack": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp]),
+    "instant_rms_norm": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, ctypes.c_float, _i, _vp]),
+    "instant_rms_norm_backward": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _sz, _i, _i, _i,
+                                       _vp]),
+    "instant_rms_norm_backward_workspace_bytes": (_sz, [_i, _i]),
+    "instant_linear_act": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp]),
+    "instant_linear_act_grad": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp]),
+    "instant_ckpt_grad_w": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _sz, _i, _i, _i, _i, _vp]),
+    "instant_ckpt_grad_w_workspace_bytes": (_sz, [_i, _i, _i]),
     "instant_device_status": (_i, [_i, _vp]),
     "instant_status_string": (ctypes.c_char_p, [_i]),
     "instant_version": (_i, []),

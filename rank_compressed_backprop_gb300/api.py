@@ -12,7 +12,7 @@ import dataclasses
 
 import torch
 
-from ._lib import (GRAD_X_STATIC_SCRATCH_BYTES, INSTANT_BF16, INSTANT_F32, AccumulateItem,
+from ._lib import (ACTIVATIONS, GRAD_X_STATIC_SCRATCH_BYTES, INSTANT_BF16, INSTANT_F32, AccumulateItem,
                    CalibParams, CalibProblem, check, lib)
 
 __all__ = [
@@ -38,6 +38,16 @@ __all__ = [
     "CalibBatch",
     "calib_workspace_bytes",
     "calib_batch_workspace_bytes",
+    "ckpt_buffers",
+    "ckpt_pack",
+    "ckpt_unpack",
+    "rms_norm",
+    "rms_norm_backward",
+    "rms_norm_backward_workspace",
+    "linear_act",
+    "linear_act_grad",
+    "ckpt_grad_w",
+    "ckpt_grad_w_workspace",
     "device_status",
     "reconstruction_error",
     "CalibResult",
@@ -475,6 +485,186 @@ def reconstruction_error(t: torch.Tensor, Q: torch.Tensor, S: torch.Tensor, ws: 
                                              ws.numel() * ws.element_size(), _stream(stream)),
           "instant_reconstruction_error")
     return e2.value, n2.value
+
+
+# --------------------------------------------------------------------------
+# operators of an MLP block: norm, products with epilogues, 8-bit checkpoints
+# --------------------------------------------------------------------------
+def _opt(t, name: str):
+    return None if t is None else _dev(t, name)
+
+
+def _rows(where: str, C: int, dt, rows: int, **tensors) -> None:
+    """Every tensor given is ``[rows, C]`` of dtype ``dt``."""
+    for name, t in tensors.items():
+        if t is not None:
+            if t.shape != (rows, C):
+                raise ValueError(f"{where}: {name} must be [{rows}, {C}], got {list(t.shape)}")
+            _same_dtype(dt, (name, t))
+
+
+def _vec(where: str, C: int, dt, **tensors) -> None:
+    """Every tensor given is ``[C]`` of dtype ``dt``."""
+    for name, t in tensors.items():
+        if t is not None:
+            if t.shape != (C,):
+                raise ValueError(f"{where}: {name} must be [{C}], got {list(t.shape)}")
+            _same_dtype(dt, (name, t))
+
+
+def _ckpt(where: str, rows: int, C: int, q, s, names=("q", "s")):
+    """Device pointers of a checkpoint of ``[rows, C]`` (both arrays or neither)."""
+    if (q is None) != (s is None):
+        raise ValueError(f"{where}: {names[0]} and {names[1]} come together")
+    if q is None:
+        return None, None
+    if q.shape != (rows, -(-C // 16) * 16) or s.shape != (-(-C // 128), rows):
+        raise ValueError(f"{where}: a checkpoint of [{rows}, {C}] has {names[0]} "
+                         f"[{rows}, {-(-C // 16) * 16}] and {names[1]} [{-(-C // 128)}, {rows}]")
+    if q.dtype != torch.int8 or s.dtype != torch.uint8:
+        raise TypeError(f"{where}: {names[0]} must be int8 and {names[1]} uint8")
+    return _dev(q, names[0]), _dev(s, names[1])
+
+
+def _act(act: str) -> int:
+    if act not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {act!r}: use one of {sorted(ACTIVATIONS)}")
+    return ACTIVATIONS[act]
+
+
+def ckpt_buffers(rows: int, C: int, device):
+    """Empty code and scale arrays of an 8-bit checkpoint of ``[rows, C]``:
+    ``q`` int8 ``[rows, C rounded up to 16]``, ``s`` uint8 ``[ceil(C / 128), rows]``."""
+    return (torch.empty(rows, -(-C // 16) * 16, dtype=torch.int8, device=device),
+            torch.empty(-(-C // 128), rows, dtype=torch.uint8, device=device))
+
+
+def ckpt_pack(x: torch.Tensor, q: torch.Tensor, s: torch.Tensor, stream=None):
+    """The 8-bit checkpoint of x ``[rows, C]``; q, s from :func:`ckpt_buffers`."""
+    rows, C = x.shape
+    pq, ps = _ckpt("ckpt_pack", rows, C, q, s)
+    check(lib().instant_ckpt_pack(_dev(x, "x"), pq, ps, rows, C, dtype_code(x.dtype), _stream(stream)),
+          "instant_ckpt_pack")
+    return q, s
+
+
+def ckpt_unpack(q: torch.Tensor, s: torch.Tensor, x: torch.Tensor, stream=None) -> torch.Tensor:
+    """The values a checkpoint stands for, into x ``[rows, C]`` (exact in bf16)."""
+    rows, C = x.shape
+    pq, ps = _ckpt("ckpt_unpack", rows, C, q, s)
+    check(lib().instant_ckpt_unpack(pq, ps, _dev(x, "x"), rows, C, dtype_code(x.dtype),
+                                    _stream(stream)), "instant_ckpt_unpack")
+    return x
+
+
+def rms_norm(x: torch.Tensor, gamma: torch.Tensor, y: torch.Tensor | None, *,
+             residual: torch.Tensor | None = None, h: torch.Tensor | None = None,
+             q: torch.Tensor | None = None, s: torch.Tensor | None = None,
+             r: torch.Tensor | None = None, eps: float = 1e-5, stream=None):
+    """``h = x + residual``, ``r = rsqrt(mean(h^2) + eps)``, ``u = h r``,
+    ``y = u gamma``; q, s take the 8-bit checkpoint of u and r ``[rows]`` fp32
+    the factor (both for :func:`rms_norm_backward`).  Returns y."""
+    rows, C = x.shape
+    _rows("rms_norm", C, x.dtype, rows, residual=residual, h=h, y=y)
+    _vec("rms_norm", C, x.dtype, gamma=gamma)
+    _vec("rms_norm", rows, torch.float32, r=r)
+    pq, ps = _ckpt("rms_norm", rows, C, q, s)
+    check(lib().instant_rms_norm(_dev(x, "x"), _opt(residual, "residual"), _dev(gamma, "gamma"),
+                                 _opt(h, "h"), _opt(y, "y"), pq, ps, _opt(r, "r"), rows, C, eps,
+                                 dtype_code(x.dtype), _stream(stream)), "instant_rms_norm")
+    return y
+
+
+def rms_norm_backward_workspace(rows: int, C: int, device) -> torch.Tensor:
+    n = int(lib().instant_rms_norm_backward_workspace_bytes(rows, C))
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def rms_norm_backward(g_y: torch.Tensor, q: torch.Tensor, s: torch.Tensor, r: torch.Tensor,
+                      gamma: torch.Tensor, gx: torch.Tensor, ggamma: torch.Tensor,
+                      ws: torch.Tensor, *, residual: torch.Tensor | None = None,
+                      accumulate: bool = False, stream=None):
+    """Gradient of :func:`rms_norm` from the checkpoint of u: ``gx`` (with the
+    gradient ``residual`` that bypassed the norm added) and ``ggamma`` ``[C]``
+    fp32 (added to with ``accumulate``).  Returns ``(gx, ggamma)``."""
+    rows, C = g_y.shape
+    _rows("rms_norm_backward", C, g_y.dtype, rows, gx=gx, residual=residual)
+    _vec("rms_norm_backward", C, g_y.dtype, gamma=gamma)
+    _vec("rms_norm_backward", rows, torch.float32, r=r)
+    _vec("rms_norm_backward", C, torch.float32, ggamma=ggamma)
+    pq, ps = _ckpt("rms_norm_backward", rows, C, q, s)
+    check(lib().instant_rms_norm_backward(
+        _dev(g_y, "g_y"), pq, ps, _dev(r, "r"), _dev(gamma, "gamma"), _opt(residual, "residual"),
+        _dev(gx, "gx"), _dev(ggamma, "ggamma"), int(bool(accumulate)), _dev(ws, "ws"),
+        ws.numel() * ws.element_size(), rows, C, dtype_code(g_y.dtype), _stream(stream)),
+        "instant_rms_norm_backward")
+    return gx, ggamma
+
+
+def linear_act(x: torch.Tensor, w: torch.Tensor, y: torch.Tensor | None, *,
+               bias: torch.Tensor | None = None, act: str = "none",
+               residual: torch.Tensor | None = None, zq: torch.Tensor | None = None,
+               zs: torch.Tensor | None = None, yq: torch.Tensor | None = None,
+               ys: torch.Tensor | None = None, stream=None):
+    """``z = x w^T + bias``, ``y = act(z) + residual``: x ``[rows, Cx]``, w ``[Cy, Cx]``,
+    y ``[rows, Cy]``; zq, zs take the 8-bit checkpoint of z, yq, ys that of y.
+    act: "none", "relu", "gelu" (erf form) or "silu".  Returns y."""
+    rows, Cx = x.shape
+    Cy = w.shape[0]
+    _rows("linear_act", Cx, x.dtype, Cy, w=w)
+    _rows("linear_act", Cy, x.dtype, rows, y=y, residual=residual)
+    _vec("linear_act", Cy, x.dtype, bias=bias)
+    pzq, pzs = _ckpt("linear_act", rows, Cy, zq, zs, ("zq", "zs"))
+    pyq, pys = _ckpt("linear_act", rows, Cy, yq, ys, ("yq", "ys"))
+    check(lib().instant_linear_act(_dev(x, "x"), _dev(w, "w"), _opt(bias, "bias"),
+                                   _opt(residual, "residual"), _opt(y, "y"), pzq, pzs, pyq, pys, rows,
+                                   Cx, Cy, _act(act), dtype_code(x.dtype), _stream(stream)),
+          "instant_linear_act")
+    return y
+
+
+def linear_act_grad(g_y: torch.Tensor, w: torch.Tensor, gx: torch.Tensor, *, act: str = "none",
+                    zq: torch.Tensor | None = None, zs: torch.Tensor | None = None,
+                    residual: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """``gx = (g_y w) act'(z) + residual``: g_y ``[rows, Cy]``, w ``[Cy, Cx]``, gx
+    ``[rows, Cx]``; zq, zs is the checkpoint of the activation's input z."""
+    rows, Cy = g_y.shape
+    Cx = w.shape[1] if w.dim() == 2 else -1
+    _rows("linear_act_grad", Cx, g_y.dtype, Cy, w=w)
+    _rows("linear_act_grad", Cx, g_y.dtype, rows, gx=gx, residual=residual)
+    pq, ps = _ckpt("linear_act_grad", rows, Cx, zq, zs, ("zq", "zs"))
+    check(lib().instant_linear_act_grad(_dev(g_y, "g_y"), _dev(w, "w"), pq, ps,
+                                        _opt(residual, "residual"), _dev(gx, "gx"), rows, Cx, Cy,
+                                        _act(act), dtype_code(g_y.dtype), _stream(stream)),
+          "instant_linear_act_grad")
+    return gx
+
+
+def ckpt_grad_w_workspace(rows: int, Cx: int, Cy: int, device) -> torch.Tensor:
+    n = int(lib().instant_ckpt_grad_w_workspace_bytes(rows, Cx, Cy))
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def ckpt_grad_w(g_y: torch.Tensor, q: torch.Tensor, s: torch.Tensor, gw: torch.Tensor,
+                ws: torch.Tensor | None = None, *, gb: torch.Tensor | None = None,
+                col_scale: torch.Tensor | None = None, accumulate: bool = False, stream=None):
+    """``gw (+)= (g_y^T v) diag(col_scale)`` and ``gb (+)= sum over rows of g_y``, v the
+    values of the checkpoint q, s of the layer's input: g_y ``[rows, Cy]``, gw
+    ``[Cy, Cx]`` fp32, gb ``[Cy]`` fp32 (needs ws).  Returns ``(gw, gb)``."""
+    rows, Cy = g_y.shape
+    Cx = gw.shape[1] if gw.dim() == 2 else -1
+    _rows("ckpt_grad_w", Cx, torch.float32, Cy, gw=gw)
+    _vec("ckpt_grad_w", Cx, g_y.dtype, col_scale=col_scale)
+    _vec("ckpt_grad_w", Cy, torch.float32, gb=gb)
+    if gb is not None and ws is None:
+        raise ValueError("ckpt_grad_w: gb needs a workspace")
+    pq, ps = _ckpt("ckpt_grad_w", rows, Cx, q, s)
+    check(lib().instant_ckpt_grad_w(_dev(g_y, "g_y"), pq, ps, _opt(col_scale, "col_scale"),
+                                    _dev(gw, "gw"), _opt(gb, "gb"), int(bool(accumulate)),
+                                    _opt(ws, "ws"),
+                                    0 if ws is None else ws.numel() * ws.element_size(), rows, Cx, Cy,
+                                    dtype_code(g_y.dtype), _stream(stream)), "instant_ckpt_grad_w")
+    return gw, gb
 
 
 def device_status(clear: bool = True, stream=None) -> int:

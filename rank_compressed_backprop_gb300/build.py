@@ -21,7 +21,7 @@ LIB = os.path.join(PKG, "libinstant.so")
 
 SOURCES = ["capi.cu", "project.cu", "gemm.cu", "expand.cu", "gradx_fused.cu", "syrk.cu", "eig.cu",
            "static_scratch.cu", "recon.cu", "gradw_stream.cu",
-           "forward.cu"]
+           "forward.cu", "ckpt.cu", "rmsnorm.cu", "linear_simt.cu", "block_capi.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-I", INCLUDE, "-I", CSRC]
@@ -36,7 +36,7 @@ def nvcc() -> str:
 
 def _deps():
     return [os.path.join(CSRC, s) for s in SOURCES] + [
-        os.path.join(CSRC, "kernels.h"), os.path.join(CSRC, "tc.cuh"),
+        os.path.join(CSRC, "kernels.h"), os.path.join(CSRC, "tc.cuh"), os.path.join(CSRC, "ckpt.cuh"),
         os.path.join(INCLUDE, "instant.h"), os.path.abspath(__file__)]
 
 

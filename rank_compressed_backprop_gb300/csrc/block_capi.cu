@@ -1,0 +1,210 @@
+// block_capi.cu -- the extern "C" boundary of the MLP-block operators declared
+// in include/instant.h (norm, products with epilogues, 8-bit checkpoints):
+// argument validation and launch planning.  No device memory is allocated here.
+#include <algorithm>
+#include <cstdint>
+
+#include "instant.h"
+#include "kernels.h"
+
+using namespace instant;
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+int cdiv(int a, int b) { return (a + b - 1) / b; }
+bool dtype_ok(instant_dtype dt) { return dt == INSTANT_F32 || dt == INSTANT_BF16; }
+bool act_ok(int act) { return act >= INSTANT_ACT_NONE && act <= INSTANT_ACT_SILU; }
+instant_status from_cuda(cudaError_t e) { return e == cudaSuccess ? INSTANT_OK : INSTANT_ERR_CUDA; }
+
+// largest extents: a row index and a padded row stay within an int
+bool extent_ok(int rows, int C) { return rows >= 1 && C >= 1 && C <= (1 << 24); }
+
+// a checkpoint's two arrays come together
+bool pair_ok(const void* q, const void* s) { return (q == nullptr) == (s == nullptr); }
+
+CkptRef ref(const void* q, const void* s) {
+  CkptRef r;
+  r.q = static_cast<int8_t*>(const_cast<void*>(q));
+  r.s = static_cast<uint8_t*>(const_cast<void*>(s));
+  return r;
+}
+
+// bf16 rows are read and written 16 bytes at a time; fp32 rows may be any width
+// and take wide accesses where C is a multiple of 4
+bool align_ok(instant_dtype dt, int C) { return dt == INSTANT_F32 || C % 8 == 0; }
+bool vec_ok(instant_dtype dt, int C) { return C % (dt == INSTANT_F32 ? 4 : 8) == 0; }
+
+}  // namespace
+
+extern "C" {
+
+instant_status instant_ckpt_pack(const void* x, void* q, void* s, int rows, int C, instant_dtype dt,
+                                 void* stream) {
+  if (!dtype_ok(dt)) return INSTANT_ERR_DTYPE;
+  if (!x || !q || !s) return INSTANT_ERR_ARG;
+  if (!extent_ok(rows, C)) return INSTANT_ERR_SHAPE;
+  if (!aligned16(x) || !aligned16(q) || !align_ok(dt, C)) return INSTANT_ERR_ALIGN;
+  return from_cuda(launch_ckpt_pack(x, ref(q, s), rows, C, dt == INSTANT_BF16, vec_ok(dt, C),
+                                    static_cast<cudaStream_t>(stream)));
+}
+
+instant_status instant_ckpt_unpack(const void* q, const void* s, void* x, int rows, int C,
+                                   instant_dtype dt, void* stream) {
+  if (!dtype_ok(dt)) return INSTANT_ERR_DTYPE;
+  if (!x || !q || !s) return INSTANT_ERR_ARG;
+  if (!extent_ok(rows, C)) return INSTANT_ERR_SHAPE;
+  if (!aligned16(x) || !aligned16(q) || !align_ok(dt, C)) return INSTANT_ERR_ALIGN;
+  return from_cuda(launch_ckpt_unpack(ref(q, s), x, rows, C, dt == INSTANT_BF16, vec_ok(dt, C),
+                                      static_cast<cudaStream_t>(stream)));
+}
+
+instant_status instant_rms_norm(const void* x, const void* residual, const void* gamma, void* h,
+                                void* y, void* q, void* s, float* r, int rows, int C, float eps,
+                                instant_dtype dt, void* stream) {
+  if (!dtype_ok(dt)) return INSTANT_ERR_DTYPE;
+  if (!x || !gamma || !(y || q) || !pair_ok(q, s) || !(eps >= 0.f)) return INSTANT_ERR_ARG;
+  if (!extent_ok(rows, C) || C > INSTANT_RMS_NORM_MAX_C) return INSTANT_ERR_SHAPE;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(gamma) || !aligned16(h) || !aligned16(y) ||
+      !aligned16(q) || !align_ok(dt, C))
+    return INSTANT_ERR_ALIGN;
+  NormArgs a;
+  a.x = x;
+  a.res = residual;
+  a.gamma = gamma;
+  a.h = h;
+  a.y = y;
+  a.k = ref(q, s);
+  a.r = r;
+  a.rows = rows;
+  a.C = C;
+  a.ld = ckpt_ld(C);
+  a.vec = vec_ok(dt, C);
+  a.eps = eps;
+  return from_cuda(launch_rms_norm(a, dt == INSTANT_BF16, static_cast<cudaStream_t>(stream)));
+}
+
+size_t instant_rms_norm_backward_workspace_bytes(int rows, int C) {
+  if (!extent_ok(rows, C) || C > INSTANT_RMS_NORM_MAX_C) return 0;
+  return static_cast<size_t>(norm_back_parts(rows, C)) * C * sizeof(float);
+}
+
+instant_status instant_rms_norm_backward(const void* gy, const void* q, const void* s, const float* r,
+                                         const void* gamma, const void* residual, void* gx,
+                                         float* ggamma, int accumulate, void* ws, size_t ws_bytes,
+                                         int rows, int C, instant_dtype dt, void* stream) {
+  if (!dtype_ok(dt)) return INSTANT_ERR_DTYPE;
+  if (!gy || !q || !s || !r || !gamma || !gx || !ggamma) return INSTANT_ERR_ARG;
+  if (!extent_ok(rows, C) || C > INSTANT_RMS_NORM_MAX_C) return INSTANT_ERR_SHAPE;
+  if (!ws || ws_bytes < instant_rms_norm_backward_workspace_bytes(rows, C)) return INSTANT_ERR_WORKSPACE;
+  if (!aligned16(gy) || !aligned16(q) || !aligned16(gamma) || !aligned16(residual) || !aligned16(gx) ||
+      !aligned16(ggamma) || !aligned16(ws) || !align_ok(dt, C))
+    return INSTANT_ERR_ALIGN;
+  NormBackArgs a;
+  a.gy = gy;
+  a.gamma = gamma;
+  a.res = residual;
+  a.gx = gx;
+  a.k = ref(q, s);
+  a.r = r;
+  a.part = static_cast<float*>(ws);
+  a.ggamma = ggamma;
+  a.rows = rows;
+  a.C = C;
+  a.ld = ckpt_ld(C);
+  a.vec = vec_ok(dt, C);
+  a.accumulate = accumulate != 0;
+  return from_cuda(launch_rms_norm_back(a, dt == INSTANT_BF16, static_cast<cudaStream_t>(stream)));
+}
+
+instant_status instant_linear_act(const void* x, const void* w, const void* bias, const void* residual,
+                                  void* y, void* zq, void* zs, void* yq, void* ys, int rows, int Cx,
+                                  int Cy, instant_act act, instant_dtype dt, void* stream) {
+  if (!dtype_ok(dt)) return INSTANT_ERR_DTYPE;
+  if (!x || !w || !(y || yq) || !pair_ok(zq, zs) || !pair_ok(yq, ys) || !act_ok(act))
+    return INSTANT_ERR_ARG;
+  if (!extent_ok(rows, Cx) || !extent_ok(rows, Cy)) return INSTANT_ERR_SHAPE;
+  if (!aligned16(x) || !aligned16(w) || !aligned16(bias) || !aligned16(residual) || !aligned16(y) ||
+      !aligned16(zq) || !aligned16(yq) || !align_ok(dt, Cx) || !align_ok(dt, Cy))
+    return INSTANT_ERR_ALIGN;
+  LinearArgs a{};
+  a.kind = 0;
+  a.M = rows;
+  a.N = Cy;
+  a.K = Cx;
+  a.a = x;
+  a.b = w;
+  a.bias = bias;
+  a.res = residual;
+  a.out = y;
+  a.zk = ref(zq, zs);
+  a.yk = ref(yq, ys);
+  a.ld = ckpt_ld(Cy);
+  a.act = act;
+  a.vec = vec_ok(dt, Cy);
+  return from_cuda(launch_linear_simt(a, dt == INSTANT_BF16, static_cast<cudaStream_t>(stream)));
+}
+
+instant_status instant_linear_act_grad(const void* gy, const void* w, const void* zq, const void* zs,
+                                       const void* residual, void* gx, int rows, int Cx, int Cy,
+                                       instant_act act, instant_dtype dt, void* stream) {
+  if (!dtype_ok(dt)) return INSTANT_ERR_DTYPE;
+  if (!gy || !w || !gx || !pair_ok(zq, zs) || !act_ok(act) || (act != INSTANT_ACT_NONE && !zq))
+    return INSTANT_ERR_ARG;
+  if (!extent_ok(rows, Cx) || !extent_ok(rows, Cy)) return INSTANT_ERR_SHAPE;
+  if (!aligned16(gy) || !aligned16(w) || !aligned16(zq) || !aligned16(residual) || !aligned16(gx) ||
+      !align_ok(dt, Cx) || !align_ok(dt, Cy))
+    return INSTANT_ERR_ALIGN;
+  LinearArgs a{};
+  a.kind = 1;
+  a.M = rows;
+  a.N = Cx;
+  a.K = Cy;
+  a.a = gy;
+  a.b = w;
+  a.res = residual;
+  a.out = gx;
+  a.ck = ref(zq, zs);
+  a.ld = ckpt_ld(Cx);
+  a.act = act;
+  a.vec = vec_ok(dt, Cx);
+  return from_cuda(launch_linear_simt(a, dt == INSTANT_BF16, static_cast<cudaStream_t>(stream)));
+}
+
+size_t instant_ckpt_grad_w_workspace_bytes(int rows, int Cx, int Cy) {
+  if (!extent_ok(rows, Cx) || !extent_ok(rows, Cy)) return 0;
+  return static_cast<size_t>(col_sum_parts(rows, Cy)) * Cy * sizeof(float);
+}
+
+instant_status instant_ckpt_grad_w(const void* gy, const void* q, const void* s, const void* col_scale,
+                                   float* gw, float* gb, int accumulate, void* ws, size_t ws_bytes,
+                                   int rows, int Cx, int Cy, instant_dtype dt, void* stream) {
+  if (!dtype_ok(dt)) return INSTANT_ERR_DTYPE;
+  if (!gy || !q || !s || !gw) return INSTANT_ERR_ARG;
+  if (!extent_ok(rows, Cx) || !extent_ok(rows, Cy)) return INSTANT_ERR_SHAPE;
+  if (gb && (!ws || ws_bytes < instant_ckpt_grad_w_workspace_bytes(rows, Cx, Cy)))
+    return INSTANT_ERR_WORKSPACE;
+  if (!aligned16(gy) || !aligned16(q) || !aligned16(col_scale) || !aligned16(gw) || !aligned16(gb) ||
+      (gb && !aligned16(ws)) || !align_ok(dt, Cx) || !align_ok(dt, Cy))
+    return INSTANT_ERR_ALIGN;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool bf16 = dt == INSTANT_BF16;
+  LinearArgs a{};
+  a.kind = 2;
+  a.M = Cy;
+  a.N = Cx;
+  a.K = rows;
+  a.a = gy;
+  a.bias = col_scale;
+  a.out = gw;
+  a.ck = ref(q, s);
+  a.ld = ckpt_ld(Cx);
+  a.accumulate = accumulate != 0;
+  a.vec = vec_ok(dt, Cx);
+  cudaError_t e = launch_linear_simt(a, bf16, st);
+  if (e == cudaSuccess && gb)
+    e = launch_col_sum(gy, gb, static_cast<float*>(ws), rows, Cy, accumulate != 0, bf16, vec_ok(dt, Cy), st);
+  return from_cuda(e);
+}
+
+}  // extern "C"

@@ -1,0 +1,188 @@
+// ckpt.cuh -- 8-bit activation checkpoints and activation functions, shared by
+// the kernels of an MLP block.
+//
+// A checkpoint of t [rows, C] cuts each row into groups of 128 channels (the
+// last one may be shorter).  A group with largest magnitude amax holds
+//   2^k   the smallest power of two with amax / 2^k <= 127, k in [-120, 121]
+//   q     = round(t / 2^k), ties to even, within [-127, 127]
+// stored as int8 codes q [rows, ld] (ld = C rounded up to 16) and one byte
+// s [groups, rows] = k + 127 per group, 255 when the group holds an infinity or
+// a NaN (it then reads back as NaN).  The scale is a power of two so that
+// q 2^k, at most seven significant bits, is exact in bf16: a gradient that reads
+// a checkpoint feeds it to the tensor cores without a second rounding, and
+// t / 2^k is exact, so the only rounding is that to the codes.  The lower clamp
+// keeps q 2^k a normal number (what is below 2^-121 reads back as 0), the upper
+// one keeps 127 * 2^k finite.
+#pragma once
+
+#include "kernels.h"
+#include "tc.cuh"
+
+namespace instant {
+
+constexpr int kCkptGroup = 128;
+constexpr uint32_t kCkptNaN = 255;
+
+// magnitude bits: NaN > inf > every finite value, so an integer maximum keeps
+// the non-finite ones (fmaxf would drop a NaN)
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// scale byte of a group from the bits of its largest magnitude: with amax =
+// 1.f * 2^E, k = E - 6, one more when the significand 1.f is above 127 / 64
+__device__ __forceinline__ uint32_t ckpt_scale_code(uint32_t amax) {
+  if (amax >= 0x7f800000u) return kCkptNaN;
+  int c = static_cast<int>(amax >> 23) - 6 + ((amax & 0x7fffffu) > 0x7e0000u ? 1 : 0);
+  return static_cast<uint32_t>(min(max(c, 7), 248));
+}
+
+__device__ __forceinline__ float ckpt_scale(uint32_t code) {  // 2^k (NaN for 255)
+  return code == kCkptNaN ? __uint_as_float(0x7fc00000u) : __uint_as_float(code << 23);
+}
+
+__device__ __forceinline__ float ckpt_inv_scale(uint32_t code) {  // 2^-k
+  return code == kCkptNaN ? 0.f : __uint_as_float((254u - code) << 23);
+}
+
+// The code of v as the low byte of an integer.  Adding 1.5 * 2^23 rounds to an
+// integer, ties to even, and leaves it in two's complement in the low bits of
+// the sum; |v inv| <= 127 by the choice of the scale except at its upper
+// clamp, where the minimum matters.
+__device__ __forceinline__ uint32_t ckpt_code(float v, float inv) {
+  const float t = fminf(fmaxf(v * inv, -127.f), 127.f);
+  return __float_as_uint(t + 12582912.f);
+}
+
+__device__ __forceinline__ uint32_t ckpt_code4(float a, float b, float c, float d, float inv) {
+  const uint32_t ab = __byte_perm(ckpt_code(a, inv), ckpt_code(b, inv), 0x0040);
+  const uint32_t cd = __byte_perm(ckpt_code(c, inv), ckpt_code(d, inv), 0x0040);
+  return __byte_perm(ab, cd, 0x5410);
+}
+
+// byte i of w as a float times the scale
+template <int I>
+__device__ __forceinline__ float ckpt_value(uint32_t w, float scale) {
+  // q + 128 in the low mantissa bits of 2^23: one byte permute and a subtract
+  const uint32_t m = __byte_perm(w ^ 0x80808080u, 0x4b000000u, 0x7440 | I);
+  return (__uint_as_float(m) - 8388736.f) * scale;
+}
+
+__device__ __forceinline__ void ckpt_values4(uint32_t w, float scale, float* v) {
+  v[0] = ckpt_value<0>(w, scale);
+  v[1] = ckpt_value<1>(w, scale);
+  v[2] = ckpt_value<2>(w, scale);
+  v[3] = ckpt_value<3>(w, scale);
+}
+
+// maximum over the 16 lanes of a half warp
+__device__ __forceinline__ uint32_t half_warp_max(uint32_t v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// ---------------------------------------------------------------------------
+// element access: bf16 (as its 16 bits) and fp32
+// ---------------------------------------------------------------------------
+template <typename T>
+__device__ __forceinline__ float elem_to_f(T v);
+template <>
+__device__ __forceinline__ float elem_to_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float elem_to_f<uint16_t>(uint16_t v) { return bf16_to_f32(v); }
+
+template <typename T>
+__device__ __forceinline__ T f_to_elem(float v);
+template <>
+__device__ __forceinline__ float f_to_elem<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ uint16_t f_to_elem<uint16_t>(float v) { return bf16_bits(v); }
+
+// N consecutive elements (N = 4 or 8) from an address aligned to the access
+template <int N>
+__device__ __forceinline__ void load_vec(const uint16_t* p, float* v) {
+  uint32_t w[N / 2];
+  if (N == 8) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    w[0] = u.x; w[1] = u.y; w[N / 2 - 2] = u.z; w[N / 2 - 1] = u.w;
+  } else {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    w[0] = u.x; w[1] = u.y;
+  }
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+template <int N>
+__device__ __forceinline__ void load_vec(const float* p, float* v) {
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) {
+    const float4 u = *reinterpret_cast<const float4*>(p + 4 * i);
+    v[4 * i] = u.x; v[4 * i + 1] = u.y; v[4 * i + 2] = u.z; v[4 * i + 3] = u.w;
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_vec(uint16_t* p, const float* v) {
+  if (N == 8)
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                              pack_bf16x2(v[N - 4], v[N - 3]), pack_bf16x2(v[N - 2], v[N - 1]));
+  else
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+}
+template <int N>
+__device__ __forceinline__ void store_vec(float* p, const float* v) {
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i)
+    *reinterpret_cast<float4*>(p + 4 * i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+}
+
+// the same with `n` valid elements of N (the rest read as 0, are not written);
+// vec: the address is aligned and, where all N are valid, may be used at once
+template <int N, typename T>
+__device__ __forceinline__ void load_part(const T* p, int n, bool vec, float* v) {
+  if (vec && n >= N) {
+    load_vec<N>(p, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = i < n ? elem_to_f<T>(p[i]) : 0.f;
+  }
+}
+template <int N, typename T>
+__device__ __forceinline__ void store_part(T* p, int n, bool vec, const float* v) {
+  if (vec && n >= N) {
+    store_vec<N>(p, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < n) p[i] = f_to_elem<T>(v[i]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// activations in fp32 with CUDA's own functions (the fp32 path; gelu in its erf
+// form through erfc, which keeps its relative accuracy in the negative tail)
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float act_f32(float z, int act) {
+  switch (act) {
+    case INSTANT_ACT_RELU: return z < 0.f ? 0.f : z;  // keeps a NaN
+    case INSTANT_ACT_GELU: return 0.5f * z * erfcf(-0.70710678f * z);
+    case INSTANT_ACT_SILU: return z / (1.f + expf(-z));
+    default: return z;
+  }
+}
+
+__device__ __forceinline__ float act_slope_f32(float z, int act) {
+  switch (act) {
+    case INSTANT_ACT_RELU: return z > 0.f ? 1.f : (z <= 0.f ? 0.f : z);  // keeps a NaN
+    case INSTANT_ACT_GELU:
+      return 0.5f * erfcf(-0.70710678f * z) + z * 0.39894228f * expf(-0.5f * z * z);
+    case INSTANT_ACT_SILU: {
+      const float s = 1.f / (1.f + expf(-z));
+      return s * (1.f + z * (1.f - s));
+    }
+    default: return 1.f;
+  }
+}
+
+}  // namespace instant

@@ -304,6 +304,69 @@ cudaError_t launch_cluster_solve_batch(ClusterSolveBatch& b, int count, cudaStre
 cudaError_t launch_recon(const void* t, const void* Q, const void* S, int B, int L, int C, int R,
                          int bf16, double* totals, cudaStream_t st);
 
+// ---------------------------------------------------------------------------
+// operators of an MLP block (norm, products with epilogues, 8-bit checkpoints)
+// ---------------------------------------------------------------------------
+struct CkptRef {       // a checkpoint of [rows, C] (ckpt.cuh); q null: none
+  int8_t* q;           // [rows, ckpt_ld(C)] codes
+  uint8_t* s;          // [ceil(C / 128), rows] scale bytes
+};
+__host__ __device__ inline int ckpt_ld(int C) { return (C + 15) / 16 * 16; }
+
+struct NormArgs {
+  const void *x, *res, *gamma;  // [rows, C], [rows, C] or null, [C]
+  void *h, *y;                  // [rows, C] or null
+  CkptRef k;                    // of u
+  float* r;                     // [rows] or null
+  int rows, C, ld;
+  int vec;                      // rows start on 16-byte boundaries
+  float eps;
+};
+struct NormBackArgs {
+  const void *gy, *gamma, *res; // [rows, C], [C], [rows, C] or null
+  void* gx;                     // [rows, C]
+  CkptRef k;                    // of u
+  const float* r;               // [rows]
+  float* part;                  // [norm_back_parts][C] shares of ggamma
+  float* ggamma;                // [C]
+  int rows, C, ld, vec, accumulate;
+};
+
+// one of three products D[m, n] = sum_k A[m, k] B[k, n] with its epilogue
+//   kind 0  a = x [M, K], b = w [N, K]: y = act(D + bias) + res, checkpoints zk, yk
+//   kind 1  a = gy [M, K], b = w [K, N]: gx = D * act'(ck) + res
+//   kind 2  a = gy [K, M], B = values of ck [K, N]: gw (+)= D * bias (per column)
+struct LinearArgs {
+  int kind;
+  int M, N, K;
+  const void *a, *b;
+  const void* bias;    // [N] or null
+  const void* res;     // [M, N] or null
+  void* out;           // [M, N]; kinds 0, 1 in the operands' type, kind 2 fp32
+  CkptRef zk, yk, ck;
+  int ld;              // code pitch of the checkpoints
+  int act;             // instant_act
+  int accumulate;      // kind 2
+  int vec;             // rows of N elements start on 16-byte boundaries
+};
+
+// shares of a column reduction are counted from the SMs of the one device this
+// library is built for, so that workspace sizes need no device
+constexpr int kColSumSMs = 152;
+int col_sum_parts(int rows, int C);
+int norm_back_parts(int rows, int C);
+cudaError_t launch_ckpt_pack(const void* x, const CkptRef& k, int rows, int C, bool bf16, bool vec,
+                             cudaStream_t st);
+cudaError_t launch_ckpt_unpack(const CkptRef& k, void* x, int rows, int C, bool bf16, bool vec,
+                               cudaStream_t st);
+cudaError_t launch_part_sum(const float* part, float* out, int parts, int C, int accumulate,
+                            cudaStream_t st);
+cudaError_t launch_col_sum(const void* x, float* out, float* part, int rows, int C, int accumulate,
+                           bool bf16, bool vec, cudaStream_t st);
+cudaError_t launch_rms_norm(const NormArgs& a, bool bf16, cudaStream_t st);
+cudaError_t launch_rms_norm_back(const NormBackArgs& a, bool bf16, cudaStream_t st);
+cudaError_t launch_linear_simt(const LinearArgs& a, bool bf16, cudaStream_t st);
+
 // host-side count of kernel launches issued by the library
 void count_launches(unsigned int n);
 
