@@ -35,6 +35,11 @@ CkptRef ref(const void* q, const void* s) {
 bool align_ok(instant_dtype dt, int C) { return dt == INSTANT_F32 || C % 8 == 0; }
 bool vec_ok(instant_dtype dt, int C) { return C % (dt == INSTANT_F32 ? 4 : 8) == 0; }
 
+// bf16 products run on the tensor cores, fp32 ones on FFMA
+cudaError_t launch_linear(const LinearArgs& a, bool bf16, cudaStream_t st) {
+  return bf16 ? launch_linear_tc(a, st) : launch_linear_simt(a, false, st);
+}
+
 }  // namespace
 
 extern "C" {
@@ -142,7 +147,7 @@ instant_status instant_linear_act(const void* x, const void* w, const void* bias
   a.ld = ckpt_ld(Cy);
   a.act = act;
   a.vec = vec_ok(dt, Cy);
-  return from_cuda(launch_linear_simt(a, dt == INSTANT_BF16, static_cast<cudaStream_t>(stream)));
+  return from_cuda(launch_linear(a, dt == INSTANT_BF16, static_cast<cudaStream_t>(stream)));
 }
 
 instant_status instant_linear_act_grad(const void* gy, const void* w, const void* zq, const void* zs,
@@ -168,7 +173,7 @@ instant_status instant_linear_act_grad(const void* gy, const void* w, const void
   a.ld = ckpt_ld(Cx);
   a.act = act;
   a.vec = vec_ok(dt, Cx);
-  return from_cuda(launch_linear_simt(a, dt == INSTANT_BF16, static_cast<cudaStream_t>(stream)));
+  return from_cuda(launch_linear(a, dt == INSTANT_BF16, static_cast<cudaStream_t>(stream)));
 }
 
 size_t instant_ckpt_grad_w_workspace_bytes(int rows, int Cx, int Cy) {
@@ -201,7 +206,7 @@ instant_status instant_ckpt_grad_w(const void* gy, const void* q, const void* s,
   a.ld = ckpt_ld(Cx);
   a.accumulate = accumulate != 0;
   a.vec = vec_ok(dt, Cx);
-  cudaError_t e = launch_linear_simt(a, bf16, st);
+  cudaError_t e = launch_linear(a, bf16, st);
   if (e == cudaSuccess && gb)
     e = launch_col_sum(gy, gb, static_cast<float*>(ws), rows, Cy, accumulate != 0, bf16, vec_ok(dt, Cy), st);
   return from_cuda(e);

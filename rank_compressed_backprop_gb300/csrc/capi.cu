@@ -115,11 +115,12 @@ EncodeTiledFn encoder() {
   return fn;
 }
 
+}  // namespace
+
 // tiled map with the 128-byte swizzle (bf16 unless stated); dims/strides
 // innermost first
-bool make_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
-              const uint64_t* strides_bytes, const uint32_t* box,
-              CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) {
+bool instant::make_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
+                       const uint64_t* strides_bytes, const uint32_t* box, CUtensorMapDataType type) {
   EncodeTiledFn f = encoder();
   if (!f) return false;
   cuuint64_t d[5], s[5];
@@ -134,6 +135,8 @@ bool make_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 int round_up(int x, int m) { return (x + m - 1) / m * m; }
@@ -1525,6 +1528,8 @@ instant_status instant_device_status(int clear, void* stream) {
   if (read_fault_gradw(&v, clear) != cudaSuccess) return INSTANT_ERR_CUDA;
   total |= v;
   if (read_fault_forward(&v, clear) != cudaSuccess) return INSTANT_ERR_CUDA;
+  total |= v;
+  if (read_fault_linear(&v, clear) != cudaSuccess) return INSTANT_ERR_CUDA;
   total |= v;
   return total ? INSTANT_ERR_DEVICE : INSTANT_OK;
 }

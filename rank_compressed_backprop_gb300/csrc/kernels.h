@@ -367,6 +367,30 @@ cudaError_t launch_rms_norm(const NormArgs& a, bool bf16, cudaStream_t st);
 cudaError_t launch_rms_norm_back(const NormBackArgs& a, bool bf16, cudaStream_t st);
 cudaError_t launch_linear_simt(const LinearArgs& a, bool bf16, cudaStream_t st);
 
+// the same products on the tensor cores, bf16 (linear_tc.cu)
+struct TcArgs {
+  int M, N, K;
+  int mt, nt, nk;      // 256 x 256 tiles, 64-deep chunks
+  int group;           // m tiles per rasterization group
+  const void* bias;    // [N] bf16 or null (grad_w: column scale)
+  const void* res;     // [M, N] bf16 or null
+  const void* out;     // null: no y
+  uint8_t *zs, *ys;    // scale bytes of the checkpoints written (null: none)
+  const int8_t* cq;    // checkpoint read
+  const uint8_t* cs;
+  int ld;              // code pitch
+  int accumulate;
+};
+struct TcMaps {
+  CUtensorMap a, b, y, z, k;
+};
+cudaError_t launch_linear_tc(const LinearArgs& a, cudaStream_t st);
+
+// tiled tensor map with the 128-byte swizzle; dims/strides innermost first
+bool make_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
+              const uint64_t* strides_bytes, const uint32_t* box,
+              CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
+
 // host-side count of kernel launches issued by the library
 void count_launches(unsigned int n);
 
@@ -443,5 +467,6 @@ cudaError_t read_fault_eig(unsigned int* out, int clear);
 cudaError_t read_fault_fused(unsigned int* out, int clear);
 cudaError_t read_fault_gradw(unsigned int* out, int clear);
 cudaError_t read_fault_forward(unsigned int* out, int clear);
+cudaError_t read_fault_linear(unsigned int* out, int clear);
 
 }  // namespace instant

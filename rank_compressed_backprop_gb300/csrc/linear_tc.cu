@@ -1,0 +1,773 @@
+// linear_tc.cu -- the three products of an MLP block's linear layers on the
+// tensor cores (bf16 operands, fp32 accumulation), each with its epilogue:
+//   forward   z = x w^T + bias, y = act(z) + res, checkpoints of z and y
+//   back      gx = (gy w) * act'(z) + res, z from its checkpoint
+//   grad_w    gw (+)= (gy^T v) * col_scale, v the values of a checkpoint
+//
+// A persistent kernel of CTA pairs: the two CTAs of a cluster share one
+// 256 x 256 output tile (tcgen05.mma cta_group::2, M = 256, N = 256, K = 16).
+// Each holds 128 of the tile's rows as its A operand and 128 of its columns as
+// its half of B, so an operand byte staged in shared memory feeds twice the
+// products of a single CTA's 128 x 128 tile; the fp32 accumulator is 128 lanes x
+// 256 columns of each CTA's TMEM, two of them, so that the epilogue of one tile
+// runs under the products of the next.
+//   warp 0     TMA producer: 64-deep chunks of this CTA's A and B halves into a
+//              ring; the arrivals of both CTAs are counted on the leader's
+//              barrier (the leader issues the products of both)
+//   warp 1     MMA issuer (the leader's only); commits free the stage in both CTAs
+//   warps 4-7, 8-11  epilogue: columns 0-127 and 128-255 of the accumulator, a
+//              thread a row, so that a thread sees a whole checkpoint group and
+//              finds its largest magnitude without talking to another
+//   grad_w: warps 8-11 turn the codes of the B half into bf16 instead, from the
+//              TMA-staged codes to the swizzled operand tile, and warps 4-7 do
+//              the whole epilogue.  q 2^k is exact in bf16, so this rounds nothing.
+// Operands contracted over their rows (w in back, gy and the codes in grad_w)
+// are MN-major operands read from their natural layout.  Outputs leave through
+// 128-byte-swizzled staging boxes and TMA stores, which also clip ragged edges;
+// accumulation into gw is the TMA's own add (each element is added to once).
+#include "ckpt.cuh"
+
+namespace instant {
+
+namespace {
+
+constexpr int BM = 256, BN = 256, BK = 64;   // tile of a CTA pair; each CTA: 128 rows of A, 128 of B
+constexpr uint32_t A_BYTES = 128 * BK * 2;   // 16 KB
+constexpr uint32_t B_BYTES = 128 * BK * 2;   // 16 KB
+constexpr uint32_t Q_BYTES = BK * 128;       // codes of the B half: 64 tokens x 128 channels
+constexpr uint32_t BOX = 128 * 128;          // staging box: 128 rows x 128 bytes
+constexpr int kThreads = 384;
+enum { FORWARD = 0, BACK = 1, GRAD_W = 2 };
+
+template <int KIND>
+struct Lay {
+  static constexpr uint32_t stage = A_BYTES + B_BYTES + (KIND == GRAD_W ? Q_BYTES : 0);
+  static constexpr int ns = KIND == GRAD_W ? 4 : 5;
+  static constexpr uint32_t box = ns * stage;
+  static constexpr int boxes = KIND == GRAD_W ? 2 : 4;
+  static constexpr uint32_t bar = box + boxes * BOX;
+  static constexpr uint32_t total = bar + 256;
+};
+
+// ---- cluster-scope barriers and pair-wide tensor-core operations ----------
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// waits for arrivals of both CTAs; gives up like mbar_wait
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  uint32_t n = 0;
+  while (!mbar_try_wait_cluster(bar, parity)) {
+    if (((++n) & 255u) == 0 && global_timer_ns() - t0 > kWaitLimitNs) return false;
+  }
+  return true;
+}
+
+// one answer for a whole warp, so that its lanes give up together
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
+}
+
+// one answer for the 128 threads of an epilogue group, which meet at barriers
+template <int ID>
+__device__ __forceinline__ bool mbar_wait_group(uint64_t* bar, uint32_t parity) {
+  const uint32_t mine = mbar_wait_cluster(bar, parity) ? 1u : 0u;
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, %2, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"(mine), "n"(ID)
+      : "memory");
+  return all != 0;
+}
+
+__device__ __forceinline__ void mbar_arrive_at(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
+
+// TMA load into this CTA, completion counted on a barrier of either CTA of the pair
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t bar, int c0,
+                                                 int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(smem_u32(src)), "r"(c0), "r"(c1)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_add_2d(const CUtensorMap* map, const void* src, int c0, int c1) {
+  asm volatile(
+      "cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(smem_u32(src)), "r"(c0), "r"(c1)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   smem_u32(dst_smem)),
+               "r"(ncols)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish_pair() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
+               : "memory");
+}
+
+__device__ __forceinline__ void umma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                               uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// arrives on the barrier at this offset in both CTAs once every product issued
+// so far by this thread has completed
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+// output tile t of the grouped order -> (m, n): groups of tiles share columns
+// of the B operand in L2
+__device__ __forceinline__ void tile_at(const TcArgs& a, int t, int& m, int& n) {
+  const int per_group = a.group * a.nt;
+  const int gid = t / per_group;
+  const int first = gid * a.group;
+  const int gsz = min(a.mt - first, a.group);
+  const int r = t - gid * per_group;
+  m = first + r % gsz;
+  n = r / gsz;
+}
+
+// two bf16 of codes (bytes 0 and 1 of the halves of w2) times a power of two.
+// A two's complement byte is low7 - 128 sign, and bf16 counts in ones from 128
+// to 256, so 0x4300 | low7 is 128 + low7 and 0x4300 | sign bit is 128 or 256;
+// their difference is the code, exactly.
+__device__ __forceinline__ uint32_t code_pair_bf16(uint32_t w2, uint32_t scale2) {
+  const uint32_t v = (w2 & 0x007f007fu) | 0x43004300u;
+  const uint32_t c = (w2 & 0x00800080u) | 0xc300c300u;
+  uint32_t r;
+  asm("{\n\t.reg .b32 t;\n\tadd.rn.bf16x2 t, %1, %2;\n\tmul.rn.bf16x2 %0, t, %3;\n\t}"
+      : "=r"(r)
+      : "r"(v), "r"(c), "r"(scale2));
+  return r;
+}
+
+// 32 columns of this warp's 32 lanes, no wait
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32"
+      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, "
+      "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_wait() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// N columns from taddr into v (N a multiple of 32), loads in flight together
+template <int N>
+__device__ __forceinline__ void tmem_read(uint32_t taddr, float* v) {
+  uint32_t r[N];
+#pragma unroll
+  for (int i = 0; i < N / 32; ++i) tmem_ld32_async(taddr + 32 * i, r + 32 * i);
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// eight elements of a row vector shared by all lanes (bias, column scale), 0 past the end
+__device__ __forceinline__ void load_row8(const uint16_t* p, int n, float* v) {
+  if (n >= 8) {
+    load_vec<8>(p, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.f;
+  }
+}
+
+struct Boxes {  // the staging boxes of one epilogue group of 128 threads
+  uint8_t* base;
+  int used;
+  int lead;     // the thread that issues the stores
+  // a box whose previous store has been read out; every thread of the group calls it
+  template <int BARRIER>
+  __device__ __forceinline__ uint8_t* next() {
+    if (lead && used >= 2) tma_store_wait_read<1>();
+    named_barrier<BARRIER>(128);
+    uint8_t* b = base + (used & 1) * BOX;
+    ++used;
+    return b;
+  }
+};
+
+// ---------------------------------------------------------------------------
+// epilogues: one 128-column group of the tile, a row a thread
+// ---------------------------------------------------------------------------
+template <int BARRIER>
+__device__ __forceinline__ void put_box_bf16(const TcArgs& a, const CUtensorMap* map, Boxes& bx, int r,
+                                             const float* v, int col, int row0) {
+  uint8_t* row = bx.next<BARRIER>() + r * 128;
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    *reinterpret_cast<uint4*>(row + ((c ^ (r & 7)) << 4)) =
+        make_uint4(pack_bf16x2(v[8 * c], v[8 * c + 1]), pack_bf16x2(v[8 * c + 2], v[8 * c + 3]),
+                   pack_bf16x2(v[8 * c + 4], v[8 * c + 5]), pack_bf16x2(v[8 * c + 6], v[8 * c + 7]));
+  fence_proxy_async_smem();
+  named_barrier<BARRIER>(128);
+  if (bx.lead) {
+    if (col < a.N && row0 < a.M) tma_store_2d(map, row - r * 128, col, row0);
+    tma_store_commit();
+  }
+}
+
+template <int BARRIER>
+__device__ __forceinline__ void put_codes(const TcArgs& a, const CUtensorMap* map, uint8_t* s, Boxes& bx,
+                                          int r, const float* v, int col, int row0) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 128; ++j) m = max(m, abs_bits(v[j]));
+  const uint32_t code = ckpt_scale_code(m);
+  const float inv = ckpt_inv_scale(code);
+  uint8_t* row = bx.next<BARRIER>() + r * 128;
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    *reinterpret_cast<uint4*>(row + ((c ^ (r & 7)) << 4)) =
+        make_uint4(ckpt_code4(v[16 * c], v[16 * c + 1], v[16 * c + 2], v[16 * c + 3], inv),
+                   ckpt_code4(v[16 * c + 4], v[16 * c + 5], v[16 * c + 6], v[16 * c + 7], inv),
+                   ckpt_code4(v[16 * c + 8], v[16 * c + 9], v[16 * c + 10], v[16 * c + 11], inv),
+                   ckpt_code4(v[16 * c + 12], v[16 * c + 13], v[16 * c + 14], v[16 * c + 15], inv));
+  if (col < a.N && row0 + r < a.M)
+    s[static_cast<size_t>(col / kCkptGroup) * a.M + row0 + r] = static_cast<uint8_t>(code);
+  fence_proxy_async_smem();
+  named_barrier<BARRIER>(128);
+  if (bx.lead) {
+    if (col < a.N && row0 < a.M) tma_store_2d(map, row - r * 128, col, row0);
+    tma_store_commit();
+  }
+}
+
+// forward with checkpoints: the group's 128 values stay in registers from the
+// accumulator to the last output
+template <int ACT, int BARRIER>
+__device__ __forceinline__ void epi_forward_keep(const TcArgs& a, const CUtensorMap* my,
+                                                 const CUtensorMap* mz, const CUtensorMap* mk, Boxes& bx,
+                                                 float* v, int r, int col, int row0) {
+  const bool on = row0 + r < a.M;
+  if (a.bias) {
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      float b[8];
+      load_row8(static_cast<const uint16_t*>(a.bias) + col + 8 * c, a.N - col - 8 * c, b);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[8 * c + e] += b[e];
+    }
+  }
+  if (a.zs) put_codes<BARRIER>(a, mz, a.zs, bx, r, v, col, row0);
+#pragma unroll
+  for (int j = 0; j < 128; ++j) v[j] = act_fast<ACT>(v[j]);
+  if (a.res) {
+    const uint16_t* res = static_cast<const uint16_t*>(a.res) + static_cast<size_t>(on ? row0 + r : 0) * a.N + col;
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      float o[8];
+      load_row8(res + 8 * c, on ? a.N - col - 8 * c : 0, o);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[8 * c + e] += o[e];
+    }
+  }
+  if (a.ys) put_codes<BARRIER>(a, mk, a.ys, bx, r, v, col, row0);
+  if (a.out) {
+    put_box_bf16<BARRIER>(a, my, bx, r, v, col, row0);
+    put_box_bf16<BARRIER>(a, my, bx, r, v + 64, col + 64, row0);
+  }
+}
+
+// forward without checkpoints, and back: 64 columns at a time
+template <int KIND, int ACT, int BARRIER>
+__device__ __forceinline__ void epi_half(const TcArgs& a, const CUtensorMap* my, Boxes& bx, float* v,
+                                         const uint4* codes, float scale, int r, int col, int row0) {
+  const bool on = row0 + r < a.M;
+  if (KIND == FORWARD) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      if (a.bias) {
+        float b[8];
+        load_row8(static_cast<const uint16_t*>(a.bias) + col + 8 * c, a.N - col - 8 * c, b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[8 * c + e] += b[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[8 * c + e] = act_fast<ACT>(v[8 * c + e]);
+    }
+  } else if (ACT != INSTANT_ACT_NONE) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint32_t w[4] = {codes[c].x, codes[c].y, codes[c].z, codes[c].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float z[4];
+        ckpt_values4(w[k], scale, z);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[16 * c + 4 * k + e] *= act_slope_fast<ACT>(z[e]);
+      }
+    }
+  }
+  if (a.res) {
+    const uint16_t* res = static_cast<const uint16_t*>(a.res) + static_cast<size_t>(on ? row0 + r : 0) * a.N + col;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      float o[8];
+      load_row8(res + 8 * c, on ? a.N - col - 8 * c : 0, o);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[8 * c + e] += o[e];
+    }
+  }
+  put_box_bf16<BARRIER>(a, my, bx, r, v, col, row0);
+}
+
+template <int KIND, int ACT, bool KEEP, int BARRIER>
+__device__ __forceinline__ void epilogue(const TcArgs& a, const CUtensorMap* my, const CUtensorMap* mz,
+                                         const CUtensorMap* mk, uint8_t* boxes, uint32_t tmem,
+                                         uint64_t* t_full, uint32_t t_empty_leader, uint32_t rank,
+                                         int pair, int pairs, int half) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quarter = warp & 3;
+  const int r = quarter * 32 + lane;
+  Boxes bx{boxes, 0, (threadIdx.x & 127) == 0};
+  const int tiles = a.mt * a.nt;
+  int q = 0;
+  for (int t = pair; t < tiles; t += pairs, ++q) {
+    int m, n;
+    tile_at(a, t, m, n);
+    const int acc = q & 1;
+    const int row0 = m * BM + static_cast<int>(rank) * 128;
+    const int col = n * BN + (KIND == GRAD_W ? 0 : half * 128);
+    const bool on = row0 + r < a.M;
+    uint4 codes[8];
+    float scale = 0.f;
+    if (KIND == BACK && ACT != INSTANT_ACT_NONE) {
+      // this row's codes of the group, asked for before the products are done
+      const int8_t* p = a.cq + static_cast<size_t>(on ? row0 + r : 0) * a.ld + col;
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        codes[c] = on && col + 16 * c < a.N ? *reinterpret_cast<const uint4*>(p + 16 * c)
+                                            : make_uint4(0u, 0u, 0u, 0u);
+      if (on && col < a.N) scale = ckpt_scale(a.cs[static_cast<size_t>(col / kCkptGroup) * a.M + row0 + r]);
+    }
+    if (!mbar_wait_group<BARRIER>(&t_full[acc], (q >> 1) & 1)) {
+      raise_fault(FAULT_WAIT_DONE);
+      break;
+    }
+    tc_fence_after();
+    const uint32_t taddr = tmem + acc * BN + half * 128 + (static_cast<uint32_t>(quarter * 32) << 16);
+    auto release = [&]() {  // the accumulator may be overwritten
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_at(t_empty_leader + 8 * acc);
+    };
+    if (KIND == GRAD_W) {
+      for (int h = 0; h < BN / 32; ++h) {
+        float v[32];
+        tmem_read<32>(taddr + 32 * h, v);
+        if (h == BN / 32 - 1) release();
+        const int c0 = col + 32 * h;
+        if (a.bias) {  // column scale
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float b[8];
+            load_row8(static_cast<const uint16_t*>(a.bias) + c0 + 8 * c, a.N - c0 - 8 * c, b);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[8 * c + e] *= b[e];
+          }
+        }
+        uint8_t* row = bx.next<BARRIER>() + r * 128;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<float4*>(row + ((c ^ (r & 7)) << 4)) =
+              make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+        fence_proxy_async_smem();
+        named_barrier<BARRIER>(128);
+        if (bx.lead) {
+          if (c0 < a.N && row0 < a.M) {
+            if (a.accumulate) tma_add_2d(my, row - r * 128, c0, row0);
+            else tma_store_2d(my, row - r * 128, c0, row0);
+          }
+          tma_store_commit();
+        }
+      }
+    } else if (KEEP) {
+      float v[128];
+      tmem_read<128>(taddr, v);
+      release();
+      epi_forward_keep<ACT, BARRIER>(a, my, mz, mk, bx, v, r, col, row0);
+    } else {
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        float v[64];
+        tmem_read<64>(taddr + 64 * h, v);
+        if (h == 1) release();
+        uint4 cc[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) cc[c] = h ? codes[4 + c] : codes[c];
+        epi_half<KIND, ACT, BARRIER>(a, my, bx, v, cc, scale, r, col + 64 * h, row0);
+      }
+    }
+  }
+  if (bx.lead) tma_store_wait_all();
+}
+
+// ---------------------------------------------------------------------------
+template <int KIND, int ACT, bool KEEP>
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+    k_linear_tc(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                const __grid_constant__ CUtensorMap map_y, const __grid_constant__ CUtensorMap map_z,
+                const __grid_constant__ CUtensorMap map_k, TcArgs a) {
+  using L = Lay<KIND>;
+  constexpr int NS = L::ns;
+  constexpr bool A_MN = KIND == GRAD_W, B_MN = KIND != FORWARD;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::bar);  // leader's: both CTAs' TMA bytes
+  uint64_t* empty = full + NS;                                  // each CTA's: products of a stage done
+  uint64_t* b_full = empty + NS;                                // leader's: codes turned (grad_w)
+  uint64_t* q_full = b_full + NS;                               // each CTA's: codes arrived (grad_w)
+  uint64_t* t_full = q_full + NS;                               // [2] each CTA's: accumulator done
+  uint64_t* t_empty = t_full + 2;                               // [2] leader's: accumulator read
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(t_empty + 2);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int tiles = a.mt * a.nt;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+      mbar_init(&b_full[s], 8);  // four dequantising warps of each CTA
+      mbar_init(&q_full[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&t_full[i], 1);
+      mbar_init(&t_empty[i], KIND == GRAD_W ? 8 : 16);  // epilogue warps of both CTAs
+    }
+    fence_barrier_init();
+    prefetch_tmap(&map_a);
+    prefetch_tmap(&map_b);
+    prefetch_tmap(&map_y);
+  }
+  if (warp == 0) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  if (warp == 0) {
+    // ---------------- producer ----------------
+    if (lane == 0) {
+      const uint32_t full_leader = dsmem_addr(full, 0);
+      constexpr uint32_t kPairBytes = 2 * (A_BYTES + (KIND == GRAD_W ? 0 : B_BYTES));
+      int s = 0, par = 0, issued = 0;
+      bool ok = true;
+      for (int t = pair; ok && t < tiles; t += pairs) {
+        int m, n;
+        tile_at(a, t, m, n);
+        const int m0 = m * BM + static_cast<int>(rank) * 128;
+        const int n0 = n * BN + static_cast<int>(rank) * 128;
+        for (int kc = 0; kc < a.nk; ++kc) {
+          if (issued >= NS && !mbar_wait_cluster(&empty[s], par ^ 1)) {
+            raise_fault(FAULT_WAIT_EMPTY);
+            ok = false;
+            break;
+          }
+          uint8_t* sa = smem + s * L::stage;
+          uint8_t* sb = sa + A_BYTES;
+          const uint32_t bar = full_leader + 8 * s;
+          const int k0 = kc * BK;
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], kPairBytes);
+          if (A_MN) {  // stored [K, M]: two boxes of 64 M x 64 K rows
+            tma_load_2d_pair(sa, &map_a, bar, m0, k0);
+            tma_load_2d_pair(sa + A_BYTES / 2, &map_a, bar, m0 + 64, k0);
+          } else {
+            tma_load_2d_pair(sa, &map_a, bar, k0, m0);
+          }
+          if (KIND == GRAD_W) {
+            mbar_arrive_expect_tx(&q_full[s], Q_BYTES);
+            tma_load_2d(sb + B_BYTES, &map_b, &q_full[s], n0, k0);
+          } else if (B_MN) {
+            tma_load_2d_pair(sb, &map_b, bar, n0, k0);
+            tma_load_2d_pair(sb + B_BYTES / 2, &map_b, bar, n0 + 64, k0);
+          } else {
+            tma_load_2d_pair(sb, &map_b, bar, k0, n0);
+          }
+          ++issued;
+          if (++s == NS) {
+            s = 0;
+            par ^= 1;
+          }
+        }
+      }
+      // the last loads have landed before the CTA goes (the leader counts both CTAs')
+      for (int k = 0; k < NS && k < issued; ++k) {
+        if (--s < 0) {
+          s = NS - 1;
+          par ^= 1;
+        }
+        if (rank == 0 && !mbar_wait_cluster(&full[s], par)) raise_fault(FAULT_WAIT_FULL);
+        if (KIND == GRAD_W && !mbar_wait(&q_full[s], par)) raise_fault(FAULT_WAIT_FULL);
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issuer of the pair ----------------
+    if (rank == 0 && lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(BM, BN, A_MN, B_MN);
+      int s = 0, par = 0, q = 0;
+      bool ok = true;
+      for (int t = pair; ok && t < tiles; t += pairs, ++q) {
+        const int acc = q & 1;
+        if (q >= 2 && !mbar_wait_cluster(&t_empty[acc], ((q >> 1) - 1) & 1)) {
+          raise_fault(FAULT_WAIT_EMPTY);
+          break;
+        }
+        tc_fence_after();
+        for (int kc = 0; kc < a.nk; ++kc) {
+          if (!mbar_wait_cluster(&full[s], par) ||
+              (KIND == GRAD_W && !mbar_wait_cluster(&b_full[s], par))) {
+            raise_fault(FAULT_WAIT_FULL);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a_base = smem_u32(smem + s * L::stage);
+          const uint32_t b_base = a_base + A_BYTES;
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk) {
+            const uint64_t ad = A_MN ? sdesc_sw128(a_base + kk * 2048, A_BYTES / 2, 1024)
+                                     : sdesc_sw128(a_base + kk * 32, 16, 1024);
+            const uint64_t bd = B_MN ? sdesc_sw128(b_base + kk * 2048, B_BYTES / 2, 1024)
+                                     : sdesc_sw128(b_base + kk * 32, 16, 1024);
+            umma_bf16_pair(tmem + acc * BN, ad, bd, idesc, (kc | kk) != 0);
+          }
+          umma_commit_pair(&empty[s]);
+          if (++s == NS) {
+            s = 0;
+            par ^= 1;
+          }
+        }
+        if (ok) umma_commit_pair(&t_full[acc]);
+      }
+    }
+  } else if (warp >= 4 && warp < 8) {
+    epilogue<KIND, ACT, KEEP, 1>(a, &map_y, &map_z, &map_k, smem + L::box, tmem, t_full,
+                                 dsmem_addr(t_empty, 0), rank, pair, pairs, 0);
+  } else if (warp >= 8 && KIND != GRAD_W) {
+    epilogue<KIND, ACT, KEEP, 2>(a, &map_y, &map_z, &map_k, smem + L::box + 2 * BOX, tmem, t_full,
+                                 dsmem_addr(t_empty, 0), rank, pair, pairs, 1);
+  } else if (warp >= 8) {
+    // ---------------- codes -> bf16 operand ----------------
+    const int tid = threadIdx.x - 256;       // 0..127
+    const int ch = tid & 7;                  // 16-channel chunk of the row
+    const int tok = tid >> 3;                // first of four tokens, 16 apart
+    const uint32_t b_full_leader = dsmem_addr(b_full, 0);
+    int s = 0, par = 0;
+    bool ok = true;
+    for (int t = pair; ok && t < tiles; t += pairs) {
+      int m, n;
+      tile_at(a, t, m, n);
+      const int n0 = n * BN + static_cast<int>(rank) * 128;
+      const uint8_t* sc = a.cs + static_cast<size_t>(n0 / kCkptGroup) * a.K;
+      const bool live = n0 < a.N;
+      // scale bytes of the chunk's tokens, fetched two chunks ahead
+      uint32_t sb[2][4];
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int k = p * BK + tok + 16 * i;
+          sb[p][i] = live && k < a.K ? sc[k] : 0u;
+        }
+      for (int kc = 0; kc < a.nk; ++kc) {
+        uint32_t now[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          now[i] = sb[0][i];
+          sb[0][i] = sb[1][i];
+          const int k = (kc + 2) * BK + tok + 16 * i;
+          sb[1][i] = live && k < a.K ? sc[k] : 0u;
+        }
+        if (!mbar_wait_warp(&q_full[s], par)) {
+          raise_fault(FAULT_WAIT_FULL);
+          ok = false;
+          break;
+        }
+        uint8_t* b = smem + s * L::stage + A_BYTES;
+        const uint8_t* codes = b + B_BYTES;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int k = tok + 16 * i;
+          const uint4 w = *reinterpret_cast<const uint4*>(codes + k * 128 + ((ch ^ (k & 7)) << 4));
+          const uint32_t half = now[i] == kCkptNaN ? 0x7fc0u : now[i] << 7;
+          const uint32_t sc2 = half | (half << 16);
+          uint4 o[2];
+          o[0].x = code_pair_bf16(__byte_perm(w.x, 0u, 0x4140), sc2);
+          o[0].y = code_pair_bf16(__byte_perm(w.x, 0u, 0x4342), sc2);
+          o[0].z = code_pair_bf16(__byte_perm(w.y, 0u, 0x4140), sc2);
+          o[0].w = code_pair_bf16(__byte_perm(w.y, 0u, 0x4342), sc2);
+          o[1].x = code_pair_bf16(__byte_perm(w.z, 0u, 0x4140), sc2);
+          o[1].y = code_pair_bf16(__byte_perm(w.z, 0u, 0x4342), sc2);
+          o[1].z = code_pair_bf16(__byte_perm(w.w, 0u, 0x4140), sc2);
+          o[1].w = code_pair_bf16(__byte_perm(w.w, 0u, 0x4342), sc2);
+          // channels 16 ch .. 16 ch + 15 of token k: 64-channel block ch / 4, two
+          // 16-byte pieces; lanes 4-7 store theirs in the other order, so that
+          // eight lanes cover all banks at each store
+          uint8_t* dst = b + (ch >> 2) * (B_BYTES / 2) + k * 128;
+          const int c0 = 2 * (ch & 3), sw = k & 7, odd = ch >> 2;
+          *reinterpret_cast<uint4*>(dst + (((c0 + odd) ^ sw) << 4)) = odd ? o[1] : o[0];
+          *reinterpret_cast<uint4*>(dst + (((c0 + 1 - odd) ^ sw) << 4)) = odd ? o[0] : o[1];
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_at(b_full_leader + 8 * s);
+        if (++s == NS) {
+          s = 0;
+          par ^= 1;
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();  // the peer's barriers, operands and accumulator stay until both are done
+  if (warp == 0) tmem_dealloc_pair(tmem, 512);
+}
+
+template <int KIND, int ACT, bool KEEP>
+cudaError_t go(const TcMaps& m, const TcArgs& a, cudaStream_t st) {
+  constexpr size_t bytes = Lay<KIND>::total + 1024;
+  auto k = k_linear_tc<KIND, ACT, KEEP>;
+  const cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(k), bytes);
+  if (e != cudaSuccess) return e;
+  const long long tiles = static_cast<long long>(a.mt) * a.nt;
+  const int pairs = static_cast<int>(tiles < sm_count() / 2 ? tiles : sm_count() / 2);
+  return launch_ex(k, dim3(2 * pairs), dim3(kThreads), bytes, st, 1, pdl_enabled(), m.a, m.b, m.y, m.z,
+                   m.k, a);
+}
+
+template <int KIND, bool KEEP>
+cudaError_t go_act(int act, const TcMaps& m, const TcArgs& a, cudaStream_t st) {
+  switch (act) {
+    case INSTANT_ACT_RELU: return go<KIND, INSTANT_ACT_RELU, KEEP>(m, a, st);
+    case INSTANT_ACT_GELU: return go<KIND, INSTANT_ACT_GELU, KEEP>(m, a, st);
+    case INSTANT_ACT_SILU: return go<KIND, INSTANT_ACT_SILU, KEEP>(m, a, st);
+    default: return go<KIND, INSTANT_ACT_NONE, KEEP>(m, a, st);
+  }
+}
+
+bool map2(CUtensorMap* m, const void* p, long long inner, long long outer, long long pitch_bytes,
+          int box_inner, int box_outer, CUtensorMapDataType type) {
+  const uint64_t d[2] = {static_cast<uint64_t>(inner), static_cast<uint64_t>(outer)};
+  const uint64_t s[1] = {static_cast<uint64_t>(pitch_bytes)};
+  const uint32_t b[2] = {static_cast<uint32_t>(box_inner), static_cast<uint32_t>(box_outer)};
+  return make_map(m, p, 2, d, s, b, type);
+}
+
+}  // namespace
+
+// Every tensor map is encoded before the launch; the caller has checked extents
+// and alignment.
+cudaError_t launch_linear_tc(const LinearArgs& l, cudaStream_t st) {
+  constexpr CUtensorMapDataType kBf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  constexpr CUtensorMapDataType kU8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  TcArgs a{};
+  a.M = l.M;
+  a.N = l.N;
+  a.K = l.K;
+  a.mt = (l.M + BM - 1) / BM;
+  a.nt = (l.N + BN - 1) / BN;
+  a.nk = (l.K + BK - 1) / BK;
+  a.group = 8;
+  if (static_cast<long long>(a.mt) * a.nt > 0x7fffffffll - 4096) return cudaErrorInvalidValue;
+  a.bias = l.bias;
+  a.res = l.res;
+  a.out = l.out;
+  a.zs = l.zk.s;
+  a.ys = l.yk.s;
+  a.cq = l.ck.q;
+  a.cs = l.ck.s;
+  a.ld = l.ld;
+  a.accumulate = l.accumulate;
+  TcMaps m{};
+  bool ok;
+  if (l.kind == FORWARD) {
+    ok = map2(&m.a, l.a, l.K, l.M, 2ll * l.K, BK, 128, kBf) && map2(&m.b, l.b, l.K, l.N, 2ll * l.K, BK, 128, kBf);
+  } else if (l.kind == BACK) {
+    ok = map2(&m.a, l.a, l.K, l.M, 2ll * l.K, BK, 128, kBf) && map2(&m.b, l.b, l.N, l.K, 2ll * l.N, 64, BK, kBf);
+  } else {
+    ok = map2(&m.a, l.a, l.M, l.K, 2ll * l.M, 64, BK, kBf) && map2(&m.b, l.ck.q, l.N, l.K, l.ld, 128, BK, kU8);
+  }
+  if (l.kind == GRAD_W)
+    ok = ok && map2(&m.y, l.out, l.N, l.M, 4ll * l.N, 32, 128, CU_TENSOR_MAP_DATA_TYPE_FLOAT32);
+  else if (l.out)
+    ok = ok && map2(&m.y, l.out, l.N, l.M, 2ll * l.N, 64, 128, kBf);
+  if (l.zk.q) ok = ok && map2(&m.z, l.zk.q, l.N, l.M, l.ld, 128, 128, kU8);
+  if (l.yk.q) ok = ok && map2(&m.k, l.yk.q, l.N, l.M, l.ld, 128, 128, kU8);
+  if (!ok) return cudaErrorInvalidValue;
+  if (l.kind == GRAD_W) return go<GRAD_W, INSTANT_ACT_NONE, false>(m, a, st);
+  if (l.kind == BACK) return go_act<BACK, false>(l.act, m, a, st);
+  return l.zk.q || l.yk.q ? go_act<FORWARD, true>(l.act, m, a, st) : go_act<FORWARD, false>(l.act, m, a, st);
+}
+
+INSTANT_FAULT_READER(read_fault_linear)
+
+}  // namespace instant
