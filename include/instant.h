@@ -486,7 +486,8 @@ instant_status instant_linear_act_grad(const void* gy, const void* w, const void
  *   gy [rows, Cy];  q, s checkpoint of [rows, Cx];  col_scale [Cx] or NULL
  *   gw [Cy, Cx] fp32, gb [Cy] fp32 or NULL (written, or added to)
  *   ws  device scratch of instant_ckpt_grad_w_workspace_bytes(rows, Cx, Cy)
- *       bytes, 16-byte aligned (may be NULL without gb); contents are overwritten
+ *       bytes, 16-byte aligned (f32: may be NULL without gb); contents are
+ *       overwritten.  Its larger part holds v in bf16 during the call
  * The sums over rows are taken in a fixed order.
  */
 instant_status instant_ckpt_grad_w(const void* gy, const void* q, const void* s, const void* col_scale,

@@ -650,7 +650,9 @@ def ckpt_grad_w(g_y: torch.Tensor, q: torch.Tensor, s: torch.Tensor, gw: torch.T
                 col_scale: torch.Tensor | None = None, accumulate: bool = False, stream=None):
     """``gw (+)= (g_y^T v) diag(col_scale)`` and ``gb (+)= sum over rows of g_y``, v the
     values of the checkpoint q, s of the layer's input: g_y ``[rows, Cy]``, gw
-    ``[Cy, Cx]`` fp32, gb ``[Cy]`` fp32 (needs ws).  Returns ``(gw, gb)``."""
+    ``[Cy, Cx]`` fp32, gb ``[Cy]`` fp32 (needs ws).  ws from
+    :func:`ckpt_grad_w_workspace`; without gb it may be left out, and bf16 calls
+    then allocate it.  Returns ``(gw, gb)``."""
     rows, Cy = g_y.shape
     Cx = gw.shape[1] if gw.dim() == 2 else -1
     _rows("ckpt_grad_w", Cx, torch.float32, Cy, gw=gw)
@@ -659,6 +661,11 @@ def ckpt_grad_w(g_y: torch.Tensor, q: torch.Tensor, s: torch.Tensor, gw: torch.T
     if gb is not None and ws is None:
         raise ValueError("ckpt_grad_w: gb needs a workspace")
     pq, ps = _ckpt("ckpt_grad_w", rows, Cx, q, s)
+    if ws is None and g_y.dtype == torch.bfloat16:
+        ws = ckpt_grad_w_workspace(rows, Cx, Cy, g_y.device)
+        if stream is not None:
+            ws.record_stream(stream if isinstance(stream, torch.cuda.Stream)
+                             else torch.cuda.ExternalStream(int(stream)))
     check(lib().instant_ckpt_grad_w(_dev(g_y, "g_y"), pq, ps, _opt(col_scale, "col_scale"),
                                     _dev(gw, "gw"), _opt(gb, "gb"), int(bool(accumulate)),
                                     _opt(ws, "ws"),

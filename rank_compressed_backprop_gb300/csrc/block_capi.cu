@@ -176,9 +176,14 @@ instant_status instant_linear_act_grad(const void* gy, const void* w, const void
   return from_cuda(launch_linear(a, dt == INSTANT_BF16, static_cast<cudaStream_t>(stream)));
 }
 
+// the checkpoint's values in bf16, then the row shares of gb
+static size_t values_bytes(int rows, int Cx) {
+  return (static_cast<size_t>(rows) * Cx * 2 + 255) & ~static_cast<size_t>(255);
+}
+
 size_t instant_ckpt_grad_w_workspace_bytes(int rows, int Cx, int Cy) {
   if (!extent_ok(rows, Cx) || !extent_ok(rows, Cy)) return 0;
-  return static_cast<size_t>(col_sum_parts(rows, Cy)) * Cy * sizeof(float);
+  return values_bytes(rows, Cx) + static_cast<size_t>(col_sum_parts(rows, Cy)) * Cy * sizeof(float);
 }
 
 instant_status instant_ckpt_grad_w(const void* gy, const void* q, const void* s, const void* col_scale,
@@ -187,10 +192,10 @@ instant_status instant_ckpt_grad_w(const void* gy, const void* q, const void* s,
   if (!dtype_ok(dt)) return INSTANT_ERR_DTYPE;
   if (!gy || !q || !s || !gw) return INSTANT_ERR_ARG;
   if (!extent_ok(rows, Cx) || !extent_ok(rows, Cy)) return INSTANT_ERR_SHAPE;
-  if (gb && (!ws || ws_bytes < instant_ckpt_grad_w_workspace_bytes(rows, Cx, Cy)))
+  if ((gb || dt == INSTANT_BF16) && (!ws || ws_bytes < instant_ckpt_grad_w_workspace_bytes(rows, Cx, Cy)))
     return INSTANT_ERR_WORKSPACE;
   if (!aligned16(gy) || !aligned16(q) || !aligned16(col_scale) || !aligned16(gw) || !aligned16(gb) ||
-      (gb && !aligned16(ws)) || !align_ok(dt, Cx) || !align_ok(dt, Cy))
+      !aligned16(ws) || !align_ok(dt, Cx) || !align_ok(dt, Cy))
     return INSTANT_ERR_ALIGN;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf16 = dt == INSTANT_BF16;
@@ -206,9 +211,16 @@ instant_status instant_ckpt_grad_w(const void* gy, const void* q, const void* s,
   a.ld = ckpt_ld(Cx);
   a.accumulate = accumulate != 0;
   a.vec = vec_ok(dt, Cx);
-  cudaError_t e = launch_linear(a, bf16, st);
+  cudaError_t e = cudaSuccess;
+  if (bf16) {
+    // the values are exact in bf16 and every row tile of gw reads them: made once
+    a.b = ws;
+    e = launch_ckpt_unpack(a.ck, ws, rows, Cx, true, true, st);
+  }
+  if (e == cudaSuccess) e = launch_linear(a, bf16, st);
   if (e == cudaSuccess && gb)
-    e = launch_col_sum(gy, gb, static_cast<float*>(ws), rows, Cy, accumulate != 0, bf16, vec_ok(dt, Cy), st);
+    e = launch_col_sum(gy, gb, reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + values_bytes(rows, Cx)),
+                       rows, Cy, accumulate != 0, bf16, vec_ok(dt, Cy), st);
   return from_cuda(e);
 }
 

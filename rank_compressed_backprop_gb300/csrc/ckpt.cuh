@@ -186,13 +186,16 @@ __device__ __forceinline__ float act_slope_f32(float z, int act) {
 }
 
 // ---------------------------------------------------------------------------
-// The same for outputs in bf16, a third of the instructions: the epilogues of
-// the tensor-core products spend theirs on them.
-//   Phi(-t) = exp(-t^2 / 2) M(t), t >= 0, with M(t) = erfcx(t / sqrt 2) / 2, which
-// falls smoothly from 1/2 like 1 / t; M is a degree-7 polynomial in
-// 1 / (1 + 0.265 t) without constant term, fitted by weighted least squares on
-// [0, 16] to 8e-7 relative, so the negative tail keeps its relative accuracy.
-// Error with the approximate exponential and reciprocal: below 2^-17 relative.
+// The same for outputs in bf16, two values at a time: the epilogues of the
+// tensor-core products spend most of their instructions here, and the packed
+// fp32 operations halve those that are sums and products.
+//   gelu(z) = max(z, 0) - |z| Phi(-|z|),  Phi(-t) = exp(-t^2 / 2) M(t), t >= 0
+// with M(t) = erfcx(t / sqrt 2) / 2, which falls smoothly from 1/2 like 1 / t; M is
+// a degree-7 polynomial in 1 / (1 + 0.265 t) without constant term, fitted by
+// weighted least squares on [0, 16] to 8e-7 relative, so the negative tail keeps
+// its relative accuracy.  t is cut at 40, where Phi(-t) is 0 in fp32, so that an
+// infinite z meets no 0 * inf.  Error with the approximate exponential and
+// reciprocal: below 2^-17 relative.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float rcp_approx(float x) {
   float r;
@@ -205,45 +208,100 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return r;
 }
 
-// Phi(z), and *e = exp(-z^2 / 2)
-__device__ __forceinline__ float normal_cdf(float z, float* e) {
-  const float t = fabsf(z);
-  const float s = rcp_approx(fmaf(0.265f, t, 1.f));
-  float m = fmaf(-0.06719099f, s, 0.19320227f);
-  m = fmaf(m, s, -0.06348484f);
-  m = fmaf(m, s, 0.14045395f);
-  m = fmaf(m, s, 0.08372033f);
-  m = fmaf(m, s, 0.10768833f);
-  m = fmaf(m, s, 0.10561106f);
-  *e = ex2_approx(z * z * -0.72134752f);  // -log2(e) / 2
-  const float tail = *e * (m * s);
-  return z < 0.f ? tail : 1.f - tail;
+__device__ __forceinline__ uint64_t f2_bits(float2 v) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
+  return r;
+}
+__device__ __forceinline__ float2 f2_of(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)), "l"(f2_bits(c)));
+  return f2_of(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)));
+  return f2_of(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)));
+  return f2_of(r);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// t = min(|z|, 40), e = exp(-z^2 / 2), Phi(-t)
+__device__ __forceinline__ float2 normal_tail(float2 z, float2& t, float2& e) {
+  t = make_float2(fminf(fabsf(z.x), 40.f), fminf(fabsf(z.y), 40.f));
+  const float2 s = make_float2(rcp_approx(fmaf(0.265f, t.x, 1.f)), rcp_approx(fmaf(0.265f, t.y, 1.f)));
+  float2 m = fma2(both(-0.06719099f), s, both(0.19320227f));
+  m = fma2(m, s, both(-0.06348484f));
+  m = fma2(m, s, both(0.14045395f));
+  m = fma2(m, s, both(0.08372033f));
+  m = fma2(m, s, both(0.10768833f));
+  m = fma2(m, s, both(0.10561106f));
+  const float2 x = mul2(mul2(z, z), both(-0.72134752f));  // -log2(e) / 2
+  e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+  return mul2(e, mul2(m, s));
 }
 
 template <int ACT>
-__device__ __forceinline__ float act_fast(float z) {
-  if (ACT == INSTANT_ACT_RELU) return z < 0.f ? 0.f : z;
+__device__ __forceinline__ float2 act_fast(float2 z) {
+  if (ACT == INSTANT_ACT_RELU) return make_float2(z.x < 0.f ? 0.f : z.x, z.y < 0.f ? 0.f : z.y);
   if (ACT == INSTANT_ACT_GELU) {
-    float e;
-    return z * normal_cdf(z, &e);
+    float2 t, e;
+    const float2 p = normal_tail(z, t, e);
+    return make_float2(fmaf(-t.x, p.x, fmaxf(z.x, 0.f)), fmaf(-t.y, p.y, fmaxf(z.y, 0.f)));
   }
-  if (ACT == INSTANT_ACT_SILU) return z * rcp_approx(1.f + ex2_approx(z * -1.44269504f));
+  if (ACT == INSTANT_ACT_SILU) {
+    const float2 x = mul2(z, both(-1.44269504f));
+    const float2 d = add2(make_float2(ex2_approx(x.x), ex2_approx(x.y)), both(1.f));
+    return mul2(z, make_float2(rcp_approx(d.x), rcp_approx(d.y)));
+  }
   return z;
 }
 
 template <int ACT>
-__device__ __forceinline__ float act_slope_fast(float z) {
-  if (ACT == INSTANT_ACT_RELU) return z > 0.f ? 1.f : (z <= 0.f ? 0.f : z);
+__device__ __forceinline__ float2 act_slope_fast(float2 z) {
+  if (ACT == INSTANT_ACT_RELU)
+    return make_float2(z.x > 0.f ? 1.f : (z.x <= 0.f ? 0.f : z.x), z.y > 0.f ? 1.f : (z.y <= 0.f ? 0.f : z.y));
   if (ACT == INSTANT_ACT_GELU) {
-    float e;
-    const float c = normal_cdf(z, &e);
-    return fmaf(z * 0.39894228f, e, c);
+    // Phi(z) = 1/2 + sign(z) (1/2 - Phi(-|z|)), and z times the density
+    float2 t, e;
+    const float2 p = normal_tail(z, t, e);
+    const float2 h = fma2(p, both(-1.f), both(0.5f));
+    const float2 c = add2(make_float2(copysignf(h.x, z.x), copysignf(h.y, z.y)), both(0.5f));
+    return fma2(mul2(z, both(0.39894228f)), e, c);
   }
   if (ACT == INSTANT_ACT_SILU) {
-    const float s = rcp_approx(1.f + ex2_approx(z * -1.44269504f));
-    return s * fmaf(z, 1.f - s, 1.f);
+    const float2 x = mul2(z, both(-1.44269504f));
+    const float2 d = add2(make_float2(ex2_approx(x.x), ex2_approx(x.y)), both(1.f));
+    const float2 s = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+    return mul2(s, fma2(z, fma2(s, both(-1.f), both(1.f)), both(1.f)));
   }
-  return 1.f;
+  return both(1.f);
+}
+
+// the larger magnitude of three values, NaN if one of them is
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Codes of four values whose scale is not at its upper clamp: no value is above
+// 127 steps then (of a NaN group the codes do not matter).
+__device__ __forceinline__ uint32_t ckpt_code4_in_range(float2 ab, float2 cd, float inv) {
+  const float2 p = fma2(ab, both(inv), both(12582912.f));
+  const float2 q = fma2(cd, both(inv), both(12582912.f));
+  const uint32_t lo = __byte_perm(__float_as_uint(p.x), __float_as_uint(p.y), 0x0040);
+  const uint32_t hi = __byte_perm(__float_as_uint(q.x), __float_as_uint(q.y), 0x0040);
+  return __byte_perm(lo, hi, 0x5410);
 }
 
 }  // namespace instant

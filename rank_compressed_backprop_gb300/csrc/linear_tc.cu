@@ -2,7 +2,7 @@
 // tensor cores (bf16 operands, fp32 accumulation), each with its epilogue:
 //   forward   z = x w^T + bias, y = act(z) + res, checkpoints of z and y
 //   back      gx = (gy w) * act'(z) + res, z from its checkpoint
-//   grad_w    gw (+)= (gy^T v) * col_scale, v the values of a checkpoint
+//   grad_w    gw (+)= (gy^T v) * col_scale, v a checkpoint's values in bf16 (exact)
 //
 // A persistent kernel of CTA pairs: the two CTAs of a cluster share one
 // 256 x 256 output tile (tcgen05.mma cta_group::2, M = 256, N = 256, K = 16).
@@ -18,10 +18,12 @@
 //   warps 4-7, 8-11  epilogue: columns 0-127 and 128-255 of the accumulator, a
 //              thread a row, so that a thread sees a whole checkpoint group and
 //              finds its largest magnitude without talking to another
-//   grad_w: warps 8-11 turn the codes of the B half into bf16 instead, from the
-//              TMA-staged codes to the swizzled operand tile, and warps 4-7 do
-//              the whole epilogue.  q 2^k is exact in bf16, so this rounds nothing.
-// Operands contracted over their rows (w in back, gy and the codes in grad_w)
+// The tensor cores' fp32 accumulation cuts low bits at every step, which adds
+// up over a long contraction (6e-6 of a 8192-token weight gradient).  Where the
+// output shows it (fp32 gradients, and checkpoints, whose codes flip) the
+// accumulator holds `seg` chunks at a time and the epilogue threads add the
+// segments into registers in ordinary fp32, under the products of the next.
+// Operands contracted over their rows (w in back, gy and v in grad_w)
 // are MN-major operands read from their natural layout.  Outputs leave through
 // 128-byte-swizzled staging boxes and TMA stores, which also clip ragged edges;
 // accumulation into gw is the TMA's own add (each element is added to once).
@@ -34,20 +36,15 @@ namespace {
 constexpr int BM = 256, BN = 256, BK = 64;   // tile of a CTA pair; each CTA: 128 rows of A, 128 of B
 constexpr uint32_t A_BYTES = 128 * BK * 2;   // 16 KB
 constexpr uint32_t B_BYTES = 128 * BK * 2;   // 16 KB
-constexpr uint32_t Q_BYTES = BK * 128;       // codes of the B half: 64 tokens x 128 channels
-constexpr uint32_t BOX = 128 * 128;          // staging box: 128 rows x 128 bytes
-constexpr int kThreads = 384;
 enum { FORWARD = 0, BACK = 1, GRAD_W = 2 };
-
-template <int KIND>
-struct Lay {
-  static constexpr uint32_t stage = A_BYTES + B_BYTES + (KIND == GRAD_W ? Q_BYTES : 0);
-  static constexpr int ns = KIND == GRAD_W ? 4 : 5;
-  static constexpr uint32_t box = ns * stage;
-  static constexpr int boxes = KIND == GRAD_W ? 2 : 4;
-  static constexpr uint32_t bar = box + boxes * BOX;
-  static constexpr uint32_t total = bar + 256;
-};
+constexpr uint32_t STAGE = A_BYTES + B_BYTES;
+constexpr int NS = 5;                        // ring depth
+constexpr uint32_t BOX = 128 * 128;          // staging box: 128 rows x 128 bytes
+constexpr uint32_t BOX_OFF = NS * STAGE;     // two boxes for each epilogue group
+constexpr uint32_t VEC_OFF = BOX_OFF + 4 * BOX;  // 2 x 128 floats: the tile's bias or column scale
+constexpr uint32_t BAR_OFF = VEC_OFF + 1024;
+constexpr uint32_t SMEM = BAR_OFF + 128;
+constexpr int kThreads = 384;
 
 // ---- cluster-scope barriers and pair-wide tensor-core operations ----------
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
@@ -73,11 +70,6 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
   return true;
 }
 
-// one answer for a whole warp, so that its lanes give up together
-__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
-}
-
 // one answer for the 128 threads of an epilogue group, which meet at barriers
 template <int ID>
 __device__ __forceinline__ bool mbar_wait_group(uint64_t* bar, uint32_t parity) {
@@ -94,8 +86,12 @@ __device__ __forceinline__ bool mbar_wait_group(uint64_t* bar, uint32_t parity) 
   return all != 0;
 }
 
+// Arrival on a barrier of either CTA.  It announces that a slot of TMEM has been
+// read, which tcgen05.fence orders; no memory is handed over, so a release at
+// CTA scope is enough (one at cluster scope waits for all that its thread has
+// under way and took 0.9 us).
 __device__ __forceinline__ void mbar_arrive_at(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
 }
 
@@ -177,20 +173,6 @@ __device__ __forceinline__ void tile_at(const TcArgs& a, int t, int& m, int& n) 
   n = r / gsz;
 }
 
-// two bf16 of codes (bytes 0 and 1 of the halves of w2) times a power of two.
-// A two's complement byte is low7 - 128 sign, and bf16 counts in ones from 128
-// to 256, so 0x4300 | low7 is 128 + low7 and 0x4300 | sign bit is 128 or 256;
-// their difference is the code, exactly.
-__device__ __forceinline__ uint32_t code_pair_bf16(uint32_t w2, uint32_t scale2) {
-  const uint32_t v = (w2 & 0x007f007fu) | 0x43004300u;
-  const uint32_t c = (w2 & 0x00800080u) | 0xc300c300u;
-  uint32_t r;
-  asm("{\n\t.reg .b32 t;\n\tadd.rn.bf16x2 t, %1, %2;\n\tmul.rn.bf16x2 %0, t, %3;\n\t}"
-      : "=r"(r)
-      : "r"(v), "r"(c), "r"(scale2));
-  return r;
-}
-
 // 32 columns of this warp's 32 lanes, no wait
 __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t* r) {
   asm volatile(
@@ -210,16 +192,16 @@ __device__ __forceinline__ void tmem_ld_wait() {
 
 // N columns from taddr into v (N a multiple of 32), loads in flight together
 template <int N>
-__device__ __forceinline__ void tmem_read(uint32_t taddr, float* v) {
+__device__ __forceinline__ void tmem_read(uint32_t taddr, float2* v) {
   uint32_t r[N];
 #pragma unroll
   for (int i = 0; i < N / 32; ++i) tmem_ld32_async(taddr + 32 * i, r + 32 * i);
   tmem_ld_wait();
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < N / 2; ++i) v[i] = make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
 }
 
-// eight elements of a row vector shared by all lanes (bias, column scale), 0 past the end
+// eight elements of a row, 0 past its end
 __device__ __forceinline__ void load_row8(const uint16_t* p, int n, float* v) {
   if (n >= 8) {
     load_vec<8>(p, v);
@@ -236,7 +218,7 @@ struct Boxes {  // the staging boxes of one epilogue group of 128 threads
   // a box whose previous store has been read out; every thread of the group calls it
   template <int BARRIER>
   __device__ __forceinline__ uint8_t* next() {
-    if (lead && used >= 2) tma_store_wait_read<1>();
+    if (lead) tma_store_wait_read<1>();
     named_barrier<BARRIER>(128);
     uint8_t* b = base + (used & 1) * BOX;
     ++used;
@@ -245,17 +227,43 @@ struct Boxes {  // the staging boxes of one epilogue group of 128 threads
 };
 
 // ---------------------------------------------------------------------------
-// epilogues: one 128-column group of the tile, a row a thread
+// epilogues: one 128-column group of the tile, a row a thread, values in pairs
 // ---------------------------------------------------------------------------
+// `n` pairs of a row vector of the tile (bias or column scale, fp32 in shared
+// memory: one address for the whole warp) starting at column c
+template <int N, bool MUL>
+__device__ __forceinline__ void with_row_vector(const float* vec, int c, float2* v) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const float4 b = *reinterpret_cast<const float4*>(vec + c + 2 * i);
+    const float2 lo = make_float2(b.x, b.y), hi = make_float2(b.z, b.w);
+    v[i] = MUL ? mul2(v[i], lo) : add2(v[i], lo);
+    v[i + 1] = MUL ? mul2(v[i + 1], hi) : add2(v[i + 1], hi);
+  }
+}
+
+// adds 2 N columns of this thread's row of `p` (n of them exist)
+template <int N>
+__device__ __forceinline__ void add_row(const uint16_t* p, int n, float2* v) {
+#pragma unroll
+  for (int c = 0; c < N / 4; ++c) {
+    float o[8];
+    load_row8(p + 8 * c, n - 8 * c, o);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[4 * c + e] = add2(v[4 * c + e], make_float2(o[2 * e], o[2 * e + 1]));
+  }
+}
+
+// 64 columns in bf16
 template <int BARRIER>
 __device__ __forceinline__ void put_box_bf16(const TcArgs& a, const CUtensorMap* map, Boxes& bx, int r,
-                                             const float* v, int col, int row0) {
+                                             const float2* v, int col, int row0) {
   uint8_t* row = bx.next<BARRIER>() + r * 128;
 #pragma unroll
   for (int c = 0; c < 8; ++c)
     *reinterpret_cast<uint4*>(row + ((c ^ (r & 7)) << 4)) =
-        make_uint4(pack_bf16x2(v[8 * c], v[8 * c + 1]), pack_bf16x2(v[8 * c + 2], v[8 * c + 3]),
-                   pack_bf16x2(v[8 * c + 4], v[8 * c + 5]), pack_bf16x2(v[8 * c + 6], v[8 * c + 7]));
+        make_uint4(pack_bf16x2(v[4 * c].x, v[4 * c].y), pack_bf16x2(v[4 * c + 1].x, v[4 * c + 1].y),
+                   pack_bf16x2(v[4 * c + 2].x, v[4 * c + 2].y), pack_bf16x2(v[4 * c + 3].x, v[4 * c + 3].y));
   fence_proxy_async_smem();
   named_barrier<BARRIER>(128);
   if (bx.lead) {
@@ -264,22 +272,33 @@ __device__ __forceinline__ void put_box_bf16(const TcArgs& a, const CUtensorMap*
   }
 }
 
+// the checkpoint of 128 columns; columns past the tensor's end hold zeros
 template <int BARRIER>
 __device__ __forceinline__ void put_codes(const TcArgs& a, const CUtensorMap* map, uint8_t* s, Boxes& bx,
-                                          int r, const float* v, int col, int row0) {
-  uint32_t m = 0;
+                                          int r, const float2* v, int col, int row0) {
+  float m[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int j = 0; j < 128; ++j) m = max(m, abs_bits(v[j]));
-  const uint32_t code = ckpt_scale_code(m);
+  for (int j = 0; j < 64; ++j) m[j & 3] = max_abs3(m[j & 3], v[j].x, v[j].y);
+  const uint32_t code = ckpt_scale_code(__float_as_uint(max_abs3(max_abs3(m[0], m[1], m[2]), m[3], 0.f)));
   const float inv = ckpt_inv_scale(code);
   uint8_t* row = bx.next<BARRIER>() + r * 128;
+  if (code != 248u) {
 #pragma unroll
-  for (int c = 0; c < 8; ++c)
-    *reinterpret_cast<uint4*>(row + ((c ^ (r & 7)) << 4)) =
-        make_uint4(ckpt_code4(v[16 * c], v[16 * c + 1], v[16 * c + 2], v[16 * c + 3], inv),
-                   ckpt_code4(v[16 * c + 4], v[16 * c + 5], v[16 * c + 6], v[16 * c + 7], inv),
-                   ckpt_code4(v[16 * c + 8], v[16 * c + 9], v[16 * c + 10], v[16 * c + 11], inv),
-                   ckpt_code4(v[16 * c + 12], v[16 * c + 13], v[16 * c + 14], v[16 * c + 15], inv));
+    for (int c = 0; c < 8; ++c) {
+      const float2* w = v + 8 * c;
+      *reinterpret_cast<uint4*>(row + ((c ^ (r & 7)) << 4)) =
+          make_uint4(ckpt_code4_in_range(w[0], w[1], inv), ckpt_code4_in_range(w[2], w[3], inv),
+                     ckpt_code4_in_range(w[4], w[5], inv), ckpt_code4_in_range(w[6], w[7], inv));
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const float2* w = v + 8 * c;
+      *reinterpret_cast<uint4*>(row + ((c ^ (r & 7)) << 4)) =
+          make_uint4(ckpt_code4(w[0].x, w[0].y, w[1].x, w[1].y, inv), ckpt_code4(w[2].x, w[2].y, w[3].x, w[3].y, inv),
+                     ckpt_code4(w[4].x, w[4].y, w[5].x, w[5].y, inv), ckpt_code4(w[6].x, w[6].y, w[7].x, w[7].y, inv));
+    }
+  }
   if (col < a.N && row0 + r < a.M)
     s[static_cast<size_t>(col / kCkptGroup) * a.M + row0 + r] = static_cast<uint8_t>(code);
   fence_proxy_async_smem();
@@ -295,54 +314,32 @@ __device__ __forceinline__ void put_codes(const TcArgs& a, const CUtensorMap* ma
 template <int ACT, int BARRIER>
 __device__ __forceinline__ void epi_forward_keep(const TcArgs& a, const CUtensorMap* my,
                                                  const CUtensorMap* mz, const CUtensorMap* mk, Boxes& bx,
-                                                 float* v, int r, int col, int row0) {
+                                                 const float* vec, float2* v, int r, int col, int row0) {
   const bool on = row0 + r < a.M;
-  if (a.bias) {
-#pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      float b[8];
-      load_row8(static_cast<const uint16_t*>(a.bias) + col + 8 * c, a.N - col - 8 * c, b);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[8 * c + e] += b[e];
-    }
-  }
+  if (a.bias) with_row_vector<64, false>(vec, 0, v);
   if (a.zs) put_codes<BARRIER>(a, mz, a.zs, bx, r, v, col, row0);
 #pragma unroll
-  for (int j = 0; j < 128; ++j) v[j] = act_fast<ACT>(v[j]);
-  if (a.res) {
-    const uint16_t* res = static_cast<const uint16_t*>(a.res) + static_cast<size_t>(on ? row0 + r : 0) * a.N + col;
-#pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      float o[8];
-      load_row8(res + 8 * c, on ? a.N - col - 8 * c : 0, o);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[8 * c + e] += o[e];
-    }
-  }
+  for (int j = 0; j < 64; ++j) v[j] = act_fast<ACT>(v[j]);
+  if (a.res)
+    add_row<64>(static_cast<const uint16_t*>(a.res) + static_cast<size_t>(on ? row0 + r : 0) * a.N + col,
+                on ? a.N - col : 0, v);
   if (a.ys) put_codes<BARRIER>(a, mk, a.ys, bx, r, v, col, row0);
   if (a.out) {
     put_box_bf16<BARRIER>(a, my, bx, r, v, col, row0);
-    put_box_bf16<BARRIER>(a, my, bx, r, v + 64, col + 64, row0);
+    put_box_bf16<BARRIER>(a, my, bx, r, v + 32, col + 64, row0);
   }
 }
 
-// forward without checkpoints, and back: 64 columns at a time
+// forward without checkpoints, and back: 64 columns at a time, c0 of the group
 template <int KIND, int ACT, int BARRIER>
-__device__ __forceinline__ void epi_half(const TcArgs& a, const CUtensorMap* my, Boxes& bx, float* v,
-                                         const uint4* codes, float scale, int r, int col, int row0) {
+__device__ __forceinline__ void epi_half(const TcArgs& a, const CUtensorMap* my, Boxes& bx, const float* vec,
+                                         float2* v, const uint4* codes, float scale, int r, int c0, int col,
+                                         int row0) {
   const bool on = row0 + r < a.M;
   if (KIND == FORWARD) {
+    if (a.bias) with_row_vector<32, false>(vec, c0, v);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      if (a.bias) {
-        float b[8];
-        load_row8(static_cast<const uint16_t*>(a.bias) + col + 8 * c, a.N - col - 8 * c, b);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[8 * c + e] += b[e];
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[8 * c + e] = act_fast<ACT>(v[8 * c + e]);
-    }
+    for (int j = 0; j < 32; ++j) v[j] = act_fast<ACT>(v[j]);
   } else if (ACT != INSTANT_ACT_NONE) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
@@ -351,27 +348,47 @@ __device__ __forceinline__ void epi_half(const TcArgs& a, const CUtensorMap* my,
       for (int k = 0; k < 4; ++k) {
         float z[4];
         ckpt_values4(w[k], scale, z);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[16 * c + 4 * k + e] *= act_slope_fast<ACT>(z[e]);
+        float2* p = v + 8 * c + 2 * k;
+        p[0] = mul2(p[0], act_slope_fast<ACT>(make_float2(z[0], z[1])));
+        p[1] = mul2(p[1], act_slope_fast<ACT>(make_float2(z[2], z[3])));
       }
     }
   }
-  if (a.res) {
-    const uint16_t* res = static_cast<const uint16_t*>(a.res) + static_cast<size_t>(on ? row0 + r : 0) * a.N + col;
+  if (a.res)
+    add_row<32>(static_cast<const uint16_t*>(a.res) + static_cast<size_t>(on ? row0 + r : 0) * a.N + col + c0,
+                on ? a.N - col - c0 : 0, v);
+  put_box_bf16<BARRIER>(a, my, bx, r, v, col + c0, row0);
+}
+
+// grad_w: column scale, then four boxes of 32 fp32 columns
+template <int BARRIER>
+__device__ __forceinline__ void epi_grad_w(const TcArgs& a, const CUtensorMap* my, Boxes& bx, const float* vec,
+                                           float2* v, int r, int col, int row0) {
+  if (a.bias) with_row_vector<64, true>(vec, 0, v);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      float o[8];
-      load_row8(res + 8 * c, on ? a.N - col - 8 * c : 0, o);
+  for (int h = 0; h < 4; ++h) {
+    const int c0 = col + 32 * h;
+    const float2* w = v + 16 * h;
+    uint8_t* row = bx.next<BARRIER>() + r * 128;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[8 * c + e] += o[e];
+    for (int c = 0; c < 8; ++c)
+      *reinterpret_cast<float4*>(row + ((c ^ (r & 7)) << 4)) =
+          make_float4(w[2 * c].x, w[2 * c].y, w[2 * c + 1].x, w[2 * c + 1].y);
+    fence_proxy_async_smem();
+    named_barrier<BARRIER>(128);
+    if (bx.lead) {
+      if (c0 < a.N && row0 < a.M) {
+        if (a.accumulate) tma_add_2d(my, row - r * 128, c0, row0);
+        else tma_store_2d(my, row - r * 128, c0, row0);
+      }
+      tma_store_commit();
     }
   }
-  put_box_bf16<BARRIER>(a, my, bx, r, v, col, row0);
 }
 
 template <int KIND, int ACT, bool KEEP, int BARRIER>
 __device__ __forceinline__ void epilogue(const TcArgs& a, const CUtensorMap* my, const CUtensorMap* mz,
-                                         const CUtensorMap* mk, uint8_t* boxes, uint32_t tmem,
+                                         const CUtensorMap* mk, uint8_t* boxes, float* vec, uint32_t tmem,
                                          uint64_t* t_full, uint32_t t_empty_leader, uint32_t rank,
                                          int pair, int pairs, int half) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -379,82 +396,82 @@ __device__ __forceinline__ void epilogue(const TcArgs& a, const CUtensorMap* my,
   const int r = quarter * 32 + lane;
   Boxes bx{boxes, 0, (threadIdx.x & 127) == 0};
   const int tiles = a.mt * a.nt;
-  int q = 0;
-  for (int t = pair; t < tiles; t += pairs, ++q) {
+  const uint32_t tbase = tmem + half * 128 + (static_cast<uint32_t>(quarter * 32) << 16);
+  int q = 0;  // accumulators read so far
+  auto release = [&](int acc) {  // the accumulator may be overwritten
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_at(t_empty_leader + 8 * acc);
+  };
+  for (int t = pair; t < tiles; t += pairs) {
     int m, n;
     tile_at(a, t, m, n);
-    const int acc = q & 1;
     const int row0 = m * BM + static_cast<int>(rank) * 128;
-    const int col = n * BN + (KIND == GRAD_W ? 0 : half * 128);
-    const bool on = row0 + r < a.M;
-    uint4 codes[8];
-    float scale = 0.f;
-    if (KIND == BACK && ACT != INSTANT_ACT_NONE) {
-      // this row's codes of the group, asked for before the products are done
-      const int8_t* p = a.cq + static_cast<size_t>(on ? row0 + r : 0) * a.ld + col;
+    const int col = n * BN + half * 128;
+    // the columns' bias or scale, for the whole group: read by all of it before
+    // its last box of the tile before, and written before the wait below
+    if (a.bias && KIND != BACK)
+      vec[r] = col + r < a.N ? bf16_to_f32(static_cast<const uint16_t*>(a.bias)[col + r]) : 0.f;
+    if (KEEP || KIND == GRAD_W) {
+      float2 v[64];
+      bool ok = true;
+      for (int k0 = 0; k0 < a.nk; k0 += a.seg, ++q) {
+        const int acc = q & 1;
+        ok = mbar_wait_group<BARRIER>(&t_full[acc], (q >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (k0 == 0) {
+          tmem_read<64>(tbase + acc * BN, v);
+          tmem_read<64>(tbase + acc * BN + 64, v + 32);
+        } else {
 #pragma unroll
-      for (int c = 0; c < 8; ++c)
-        codes[c] = on && col + 16 * c < a.N ? *reinterpret_cast<const uint4*>(p + 16 * c)
-                                            : make_uint4(0u, 0u, 0u, 0u);
-      if (on && col < a.N) scale = ckpt_scale(a.cs[static_cast<size_t>(col / kCkptGroup) * a.M + row0 + r]);
-    }
-    if (!mbar_wait_group<BARRIER>(&t_full[acc], (q >> 1) & 1)) {
-      raise_fault(FAULT_WAIT_DONE);
-      break;
-    }
-    tc_fence_after();
-    const uint32_t taddr = tmem + acc * BN + half * 128 + (static_cast<uint32_t>(quarter * 32) << 16);
-    auto release = [&]() {  // the accumulator may be overwritten
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_at(t_empty_leader + 8 * acc);
-    };
-    if (KIND == GRAD_W) {
-      for (int h = 0; h < BN / 32; ++h) {
-        float v[32];
-        tmem_read<32>(taddr + 32 * h, v);
-        if (h == BN / 32 - 1) release();
-        const int c0 = col + 32 * h;
-        if (a.bias) {  // column scale
+          for (int h = 0; h < 8; ++h) {
+            float w[16];
+            tmem_ld16(tbase + acc * BN + 16 * h, w);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float b[8];
-            load_row8(static_cast<const uint16_t*>(a.bias) + c0 + 8 * c, a.N - c0 - 8 * c, b);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[8 * c + e] *= b[e];
+            for (int j = 0; j < 8; ++j)
+              v[8 * h + j] = add2(v[8 * h + j], make_float2(w[2 * j], w[2 * j + 1]));
           }
         }
-        uint8_t* row = bx.next<BARRIER>() + r * 128;
+        release(acc);
+      }
+      if (!ok) {
+        raise_fault(FAULT_WAIT_DONE);
+        break;
+      }
+      if (KIND == GRAD_W) epi_grad_w<BARRIER>(a, my, bx, vec, v, r, col, row0);
+      else epi_forward_keep<ACT, BARRIER>(a, my, mz, mk, bx, vec, v, r, col, row0);
+    } else {
+      const bool on = row0 + r < a.M;
+      uint4 codes[8];
+      float scale = 0.f;
+      if (KIND == BACK && ACT != INSTANT_ACT_NONE) {
+        // this row's codes of the group, asked for before the products are done
+        const int8_t* p = a.cq + static_cast<size_t>(on ? row0 + r : 0) * a.ld + col;
 #pragma unroll
         for (int c = 0; c < 8; ++c)
-          *reinterpret_cast<float4*>(row + ((c ^ (r & 7)) << 4)) =
-              make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-        fence_proxy_async_smem();
-        named_barrier<BARRIER>(128);
-        if (bx.lead) {
-          if (c0 < a.N && row0 < a.M) {
-            if (a.accumulate) tma_add_2d(my, row - r * 128, c0, row0);
-            else tma_store_2d(my, row - r * 128, c0, row0);
-          }
-          tma_store_commit();
-        }
+          codes[c] = on && col + 16 * c < a.N ? *reinterpret_cast<const uint4*>(p + 16 * c)
+                                              : make_uint4(0u, 0u, 0u, 0u);
+        if (on && col < a.N)
+          scale = ckpt_scale(a.cs[static_cast<size_t>(col / kCkptGroup) * a.M + row0 + r]);
       }
-    } else if (KEEP) {
-      float v[128];
-      tmem_read<128>(taddr, v);
-      release();
-      epi_forward_keep<ACT, BARRIER>(a, my, mz, mk, bx, v, r, col, row0);
-    } else {
+      const int acc = q & 1;
+      if (!mbar_wait_group<BARRIER>(&t_full[acc], (q >> 1) & 1)) {
+        raise_fault(FAULT_WAIT_DONE);
+        break;
+      }
+      tc_fence_after();
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
-        float v[64];
-        tmem_read<64>(taddr + 64 * h, v);
-        if (h == 1) release();
+        float2 v[32];
+        tmem_read<64>(tbase + acc * BN + 64 * h, v);
+        if (h == 1) release(acc);
         uint4 cc[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) cc[c] = h ? codes[4 + c] : codes[c];
-        epi_half<KIND, ACT, BARRIER>(a, my, bx, v, cc, scale, r, col + 64 * h, row0);
+        epi_half<KIND, ACT, BARRIER>(a, my, bx, vec, v, cc, scale, r, 64 * h, col, row0);
       }
+      ++q;
     }
   }
   if (bx.lead) tma_store_wait_all();
@@ -466,19 +483,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     k_linear_tc(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                 const __grid_constant__ CUtensorMap map_y, const __grid_constant__ CUtensorMap map_z,
                 const __grid_constant__ CUtensorMap map_k, TcArgs a) {
-  using L = Lay<KIND>;
-  constexpr int NS = L::ns;
   constexpr bool A_MN = KIND == GRAD_W, B_MN = KIND != FORWARD;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::bar);  // leader's: both CTAs' TMA bytes
-  uint64_t* empty = full + NS;                                  // each CTA's: products of a stage done
-  uint64_t* b_full = empty + NS;                                // leader's: codes turned (grad_w)
-  uint64_t* q_full = b_full + NS;                               // each CTA's: codes arrived (grad_w)
-  uint64_t* t_full = q_full + NS;                               // [2] each CTA's: accumulator done
-  uint64_t* t_empty = t_full + 2;                               // [2] leader's: accumulator read
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + BAR_OFF);  // leader's: both CTAs' TMA bytes
+  uint64_t* empty = full + NS;       // each CTA's: products of a chunk done
+  uint64_t* t_full = empty + NS;     // [2] each CTA's: accumulator done
+  uint64_t* t_empty = t_full + 2;    // [2] leader's: accumulator read
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(t_empty + 2);
+
+  float* vec = reinterpret_cast<float*>(smem + VEC_OFF);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -490,12 +505,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     for (int s = 0; s < NS; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
-      mbar_init(&b_full[s], 8);  // four dequantising warps of each CTA
-      mbar_init(&q_full[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&t_full[i], 1);
-      mbar_init(&t_empty[i], KIND == GRAD_W ? 8 : 16);  // epilogue warps of both CTAs
+      mbar_init(&t_empty[i], 16);  // epilogue warps of both CTAs
     }
     fence_barrier_init();
     prefetch_tmap(&map_a);
@@ -517,8 +530,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     // ---------------- producer ----------------
     if (lane == 0) {
       const uint32_t full_leader = dsmem_addr(full, 0);
-      constexpr uint32_t kPairBytes = 2 * (A_BYTES + (KIND == GRAD_W ? 0 : B_BYTES));
-      int s = 0, par = 0, issued = 0;
+      constexpr uint32_t kPairBytes = 2 * STAGE;
+      int s = 0, par = 1, issued = 0;  // slot, and parity of its last release (1: never used)
       bool ok = true;
       for (int t = pair; ok && t < tiles; t += pairs) {
         int m, n;
@@ -526,12 +539,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const int m0 = m * BM + static_cast<int>(rank) * 128;
         const int n0 = n * BN + static_cast<int>(rank) * 128;
         for (int kc = 0; kc < a.nk; ++kc) {
-          if (issued >= NS && !mbar_wait_cluster(&empty[s], par ^ 1)) {
+          if (!mbar_wait_cluster(&empty[s], par)) {
             raise_fault(FAULT_WAIT_EMPTY);
             ok = false;
             break;
           }
-          uint8_t* sa = smem + s * L::stage;
+          uint8_t* sa = smem + s * STAGE;
           uint8_t* sb = sa + A_BYTES;
           const uint32_t bar = full_leader + 8 * s;
           const int k0 = kc * BK;
@@ -542,10 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           } else {
             tma_load_2d_pair(sa, &map_a, bar, k0, m0);
           }
-          if (KIND == GRAD_W) {
-            mbar_arrive_expect_tx(&q_full[s], Q_BYTES);
-            tma_load_2d(sb + B_BYTES, &map_b, &q_full[s], n0, k0);
-          } else if (B_MN) {
+          if (B_MN) {
             tma_load_2d_pair(sb, &map_b, bar, n0, k0);
             tma_load_2d_pair(sb + B_BYTES / 2, &map_b, bar, n0 + 64, k0);
           } else {
@@ -559,13 +569,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         }
       }
       // the last loads have landed before the CTA goes (the leader counts both CTAs')
+      par ^= 1;
       for (int k = 0; k < NS && k < issued; ++k) {
         if (--s < 0) {
           s = NS - 1;
           par ^= 1;
         }
         if (rank == 0 && !mbar_wait_cluster(&full[s], par)) raise_fault(FAULT_WAIT_FULL);
-        if (KIND == GRAD_W && !mbar_wait(&q_full[s], par)) raise_fault(FAULT_WAIT_FULL);
       }
     }
   } else if (warp == 1) {
@@ -574,22 +584,27 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       constexpr uint32_t idesc = idesc_bf16_f32(BM, BN, A_MN, B_MN);
       int s = 0, par = 0, q = 0;
       bool ok = true;
-      for (int t = pair; ok && t < tiles; t += pairs, ++q) {
-        const int acc = q & 1;
-        if (q >= 2 && !mbar_wait_cluster(&t_empty[acc], ((q >> 1) - 1) & 1)) {
-          raise_fault(FAULT_WAIT_EMPTY);
-          break;
-        }
-        tc_fence_after();
+      for (int t = pair; ok && t < tiles; t += pairs) {
+        int left = 0, acc = 0;  // chunks left of the accumulator's segment
         for (int kc = 0; kc < a.nk; ++kc) {
-          if (!mbar_wait_cluster(&full[s], par) ||
-              (KIND == GRAD_W && !mbar_wait_cluster(&b_full[s], par))) {
+          const bool first = left == 0;
+          if (first) {
+            acc = q & 1;
+            left = min(a.seg, a.nk - kc);
+            if (q >= 2 && !mbar_wait_cluster(&t_empty[acc], ((q >> 1) - 1) & 1)) {
+              raise_fault(FAULT_WAIT_EMPTY);
+              ok = false;
+              break;
+            }
+            ++q;
+          }
+          if (!mbar_wait_cluster(&full[s], par)) {
             raise_fault(FAULT_WAIT_FULL);
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a_base = smem_u32(smem + s * L::stage);
+          const uint32_t a_base = smem_u32(smem + s * STAGE);
           const uint32_t b_base = a_base + A_BYTES;
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk) {
@@ -597,94 +612,23 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                                      : sdesc_sw128(a_base + kk * 32, 16, 1024);
             const uint64_t bd = B_MN ? sdesc_sw128(b_base + kk * 2048, B_BYTES / 2, 1024)
                                      : sdesc_sw128(b_base + kk * 32, 16, 1024);
-            umma_bf16_pair(tmem + acc * BN, ad, bd, idesc, (kc | kk) != 0);
+            umma_bf16_pair(tmem + acc * BN, ad, bd, idesc, !(first && kk == 0));
           }
           umma_commit_pair(&empty[s]);
+          if (--left == 0) umma_commit_pair(&t_full[acc]);
           if (++s == NS) {
             s = 0;
             par ^= 1;
           }
         }
-        if (ok) umma_commit_pair(&t_full[acc]);
       }
     }
   } else if (warp >= 4 && warp < 8) {
-    epilogue<KIND, ACT, KEEP, 1>(a, &map_y, &map_z, &map_k, smem + L::box, tmem, t_full,
+    epilogue<KIND, ACT, KEEP, 1>(a, &map_y, &map_z, &map_k, smem + BOX_OFF, vec, tmem, t_full,
                                  dsmem_addr(t_empty, 0), rank, pair, pairs, 0);
-  } else if (warp >= 8 && KIND != GRAD_W) {
-    epilogue<KIND, ACT, KEEP, 2>(a, &map_y, &map_z, &map_k, smem + L::box + 2 * BOX, tmem, t_full,
-                                 dsmem_addr(t_empty, 0), rank, pair, pairs, 1);
   } else if (warp >= 8) {
-    // ---------------- codes -> bf16 operand ----------------
-    const int tid = threadIdx.x - 256;       // 0..127
-    const int ch = tid & 7;                  // 16-channel chunk of the row
-    const int tok = tid >> 3;                // first of four tokens, 16 apart
-    const uint32_t b_full_leader = dsmem_addr(b_full, 0);
-    int s = 0, par = 0;
-    bool ok = true;
-    for (int t = pair; ok && t < tiles; t += pairs) {
-      int m, n;
-      tile_at(a, t, m, n);
-      const int n0 = n * BN + static_cast<int>(rank) * 128;
-      const uint8_t* sc = a.cs + static_cast<size_t>(n0 / kCkptGroup) * a.K;
-      const bool live = n0 < a.N;
-      // scale bytes of the chunk's tokens, fetched two chunks ahead
-      uint32_t sb[2][4];
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int k = p * BK + tok + 16 * i;
-          sb[p][i] = live && k < a.K ? sc[k] : 0u;
-        }
-      for (int kc = 0; kc < a.nk; ++kc) {
-        uint32_t now[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          now[i] = sb[0][i];
-          sb[0][i] = sb[1][i];
-          const int k = (kc + 2) * BK + tok + 16 * i;
-          sb[1][i] = live && k < a.K ? sc[k] : 0u;
-        }
-        if (!mbar_wait_warp(&q_full[s], par)) {
-          raise_fault(FAULT_WAIT_FULL);
-          ok = false;
-          break;
-        }
-        uint8_t* b = smem + s * L::stage + A_BYTES;
-        const uint8_t* codes = b + B_BYTES;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int k = tok + 16 * i;
-          const uint4 w = *reinterpret_cast<const uint4*>(codes + k * 128 + ((ch ^ (k & 7)) << 4));
-          const uint32_t half = now[i] == kCkptNaN ? 0x7fc0u : now[i] << 7;
-          const uint32_t sc2 = half | (half << 16);
-          uint4 o[2];
-          o[0].x = code_pair_bf16(__byte_perm(w.x, 0u, 0x4140), sc2);
-          o[0].y = code_pair_bf16(__byte_perm(w.x, 0u, 0x4342), sc2);
-          o[0].z = code_pair_bf16(__byte_perm(w.y, 0u, 0x4140), sc2);
-          o[0].w = code_pair_bf16(__byte_perm(w.y, 0u, 0x4342), sc2);
-          o[1].x = code_pair_bf16(__byte_perm(w.z, 0u, 0x4140), sc2);
-          o[1].y = code_pair_bf16(__byte_perm(w.z, 0u, 0x4342), sc2);
-          o[1].z = code_pair_bf16(__byte_perm(w.w, 0u, 0x4140), sc2);
-          o[1].w = code_pair_bf16(__byte_perm(w.w, 0u, 0x4342), sc2);
-          // channels 16 ch .. 16 ch + 15 of token k: 64-channel block ch / 4, two
-          // 16-byte pieces; lanes 4-7 store theirs in the other order, so that
-          // eight lanes cover all banks at each store
-          uint8_t* dst = b + (ch >> 2) * (B_BYTES / 2) + k * 128;
-          const int c0 = 2 * (ch & 3), sw = k & 7, odd = ch >> 2;
-          *reinterpret_cast<uint4*>(dst + (((c0 + odd) ^ sw) << 4)) = odd ? o[1] : o[0];
-          *reinterpret_cast<uint4*>(dst + (((c0 + 1 - odd) ^ sw) << 4)) = odd ? o[0] : o[1];
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_at(b_full_leader + 8 * s);
-        if (++s == NS) {
-          s = 0;
-          par ^= 1;
-        }
-      }
-    }
+    epilogue<KIND, ACT, KEEP, 2>(a, &map_y, &map_z, &map_k, smem + BOX_OFF + 2 * BOX, vec + 128, tmem, t_full,
+                                 dsmem_addr(t_empty, 0), rank, pair, pairs, 1);
   }
   __syncwarp();
   tc_fence_before();
@@ -694,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 
 template <int KIND, int ACT, bool KEEP>
 cudaError_t go(const TcMaps& m, const TcArgs& a, cudaStream_t st) {
-  constexpr size_t bytes = Lay<KIND>::total + 1024;
+  constexpr size_t bytes = SMEM + 1024;
   auto k = k_linear_tc<KIND, ACT, KEEP>;
   const cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(k), bytes);
   if (e != cudaSuccess) return e;
@@ -737,6 +681,8 @@ cudaError_t launch_linear_tc(const LinearArgs& l, cudaStream_t st) {
   a.nt = (l.N + BN - 1) / BN;
   a.nk = (l.K + BK - 1) / BK;
   a.group = 8;
+  const bool keep = l.zk.q || l.yk.q;
+  a.seg = l.kind == GRAD_W ? 16 : keep ? 8 : a.nk;
   if (static_cast<long long>(a.mt) * a.nt > 0x7fffffffll - 4096) return cudaErrorInvalidValue;
   a.bias = l.bias;
   a.res = l.res;
@@ -754,7 +700,7 @@ cudaError_t launch_linear_tc(const LinearArgs& l, cudaStream_t st) {
   } else if (l.kind == BACK) {
     ok = map2(&m.a, l.a, l.K, l.M, 2ll * l.K, BK, 128, kBf) && map2(&m.b, l.b, l.N, l.K, 2ll * l.N, 64, BK, kBf);
   } else {
-    ok = map2(&m.a, l.a, l.M, l.K, 2ll * l.M, 64, BK, kBf) && map2(&m.b, l.ck.q, l.N, l.K, l.ld, 128, BK, kU8);
+    ok = map2(&m.a, l.a, l.M, l.K, 2ll * l.M, 64, BK, kBf) && map2(&m.b, l.b, l.N, l.K, 2ll * l.N, 64, BK, kBf);
   }
   if (l.kind == GRAD_W)
     ok = ok && map2(&m.y, l.out, l.N, l.M, 4ll * l.N, 32, 128, CU_TENSOR_MAP_DATA_TYPE_FLOAT32);
@@ -765,7 +711,7 @@ cudaError_t launch_linear_tc(const LinearArgs& l, cudaStream_t st) {
   if (!ok) return cudaErrorInvalidValue;
   if (l.kind == GRAD_W) return go<GRAD_W, INSTANT_ACT_NONE, false>(m, a, st);
   if (l.kind == BACK) return go_act<BACK, false>(l.act, m, a, st);
-  return l.zk.q || l.yk.q ? go_act<FORWARD, true>(l.act, m, a, st) : go_act<FORWARD, false>(l.act, m, a, st);
+  return keep ? go_act<FORWARD, true>(l.act, m, a, st) : go_act<FORWARD, false>(l.act, m, a, st);
 }
 
 INSTANT_FAULT_READER(read_fault_linear)
