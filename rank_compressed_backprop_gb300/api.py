@@ -73,8 +73,15 @@ def _dev(t: torch.Tensor, name: str) -> int:
     return t.data_ptr()
 
 
+# the current stream's handle without building a torch.cuda.Stream around it
+# (0.1 us against 3 us)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -490,40 +497,58 @@ def reconstruction_error(t: torch.Tensor, Q: torch.Tensor, S: torch.Tensor, ws: 
 # --------------------------------------------------------------------------
 # operators of an MLP block: norm, products with epilogues, 8-bit checkpoints
 # --------------------------------------------------------------------------
-def _opt(t, name: str):
-    return None if t is None else _dev(t, name)
+def _ptr(t, shape, dt):
+    """Device pointer of a contiguous CUDA tensor of this shape and dtype, None
+    for None, -1 for anything else (the caller then finds out what is wrong; one
+    token's call takes less time on the GPU than a full report's checks)."""
+    if t is None:
+        return None
+    if t.shape == shape and t.dtype is dt and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    return -1
 
 
-def _rows(where: str, C: int, dt, rows: int, **tensors) -> None:
-    """Every tensor given is ``[rows, C]`` of dtype ``dt``."""
-    for name, t in tensors.items():
+def _refuse(where: str, *wanted, ckpts=()):
+    """Raises for the first of ``(name, tensor, shape, dtype)`` that is not what
+    it should be: shapes and dtypes first, then device and layout."""
+    for name, t, shape, dt in wanted:
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.shape != shape:
+            raise ValueError(f"{where}: {name} must be {list(shape)}, got {list(t.shape)}")
+        _same_dtype(dt, (name, t))
+    for q, s, rows, C, names in ckpts:
+        _ckpt_refuse(where, rows, C, q, s, names)
+    for name, t, _, _ in wanted:
         if t is not None:
-            if t.shape != (rows, C):
-                raise ValueError(f"{where}: {name} must be [{rows}, {C}], got {list(t.shape)}")
-            _same_dtype(dt, (name, t))
+            _dev(t, name)
+    for q, s, _, _, names in ckpts:
+        if q is not None:
+            _dev(q, names[0])
+            _dev(s, names[1])
 
 
-def _vec(where: str, C: int, dt, **tensors) -> None:
-    """Every tensor given is ``[C]`` of dtype ``dt``."""
-    for name, t in tensors.items():
-        if t is not None:
-            if t.shape != (C,):
-                raise ValueError(f"{where}: {name} must be [{C}], got {list(t.shape)}")
-            _same_dtype(dt, (name, t))
-
-
-def _ckpt(where: str, rows: int, C: int, q, s, names=("q", "s")):
-    """Device pointers of a checkpoint of ``[rows, C]`` (both arrays or neither)."""
+def _ckpt_refuse(where: str, rows: int, C: int, q, s, names):
     if (q is None) != (s is None):
         raise ValueError(f"{where}: {names[0]} and {names[1]} come together")
     if q is None:
-        return None, None
+        return
     if q.shape != (rows, -(-C // 16) * 16) or s.shape != (-(-C // 128), rows):
         raise ValueError(f"{where}: a checkpoint of [{rows}, {C}] has {names[0]} "
                          f"[{rows}, {-(-C // 16) * 16}] and {names[1]} [{-(-C // 128)}, {rows}]")
     if q.dtype != torch.int8 or s.dtype != torch.uint8:
         raise TypeError(f"{where}: {names[0]} must be int8 and {names[1]} uint8")
-    return _dev(q, names[0]), _dev(s, names[1])
+
+
+def _ckpt_ptrs(rows: int, C: int, q, s):
+    """Pointers of a checkpoint of ``[rows, C]``: both, (None, None), or a -1."""
+    if q is None and s is None:
+        return None, None
+    if q is None or s is None:
+        return -1, -1
+    return _ptr(q, (rows, -(-C // 16) * 16), torch.int8), _ptr(s, (-(-C // 128), rows), torch.uint8)
 
 
 def _act(act: str) -> int:
@@ -541,19 +566,25 @@ def ckpt_buffers(rows: int, C: int, device):
 
 def ckpt_pack(x: torch.Tensor, q: torch.Tensor, s: torch.Tensor, stream=None):
     """The 8-bit checkpoint of x ``[rows, C]``; q, s from :func:`ckpt_buffers`."""
-    rows, C = x.shape
-    pq, ps = _ckpt("ckpt_pack", rows, C, q, s)
-    check(lib().instant_ckpt_pack(_dev(x, "x"), pq, ps, rows, C, dtype_code(x.dtype), _stream(stream)),
+    rows, C = shape = x.shape
+    px = _ptr(x, shape, x.dtype)
+    pq, ps = _ckpt_ptrs(rows, C, q, s)
+    if -1 in (px, pq, ps):
+        _refuse("ckpt_pack", ("x", x, shape, x.dtype), ckpts=[(q, s, rows, C, ("q", "s"))])
+    check(lib().instant_ckpt_pack(px, pq, ps, rows, C, dtype_code(x.dtype), _stream(stream)),
           "instant_ckpt_pack")
     return q, s
 
 
 def ckpt_unpack(q: torch.Tensor, s: torch.Tensor, x: torch.Tensor, stream=None) -> torch.Tensor:
     """The values a checkpoint stands for, into x ``[rows, C]`` (exact in bf16)."""
-    rows, C = x.shape
-    pq, ps = _ckpt("ckpt_unpack", rows, C, q, s)
-    check(lib().instant_ckpt_unpack(pq, ps, _dev(x, "x"), rows, C, dtype_code(x.dtype),
-                                    _stream(stream)), "instant_ckpt_unpack")
+    rows, C = shape = x.shape
+    px = _ptr(x, shape, x.dtype)
+    pq, ps = _ckpt_ptrs(rows, C, q, s)
+    if -1 in (px, pq, ps):
+        _refuse("ckpt_unpack", ("x", x, shape, x.dtype), ckpts=[(q, s, rows, C, ("q", "s"))])
+    check(lib().instant_ckpt_unpack(pq, ps, px, rows, C, dtype_code(x.dtype), _stream(stream)),
+          "instant_ckpt_unpack")
     return x
 
 
@@ -564,19 +595,20 @@ def rms_norm(x: torch.Tensor, gamma: torch.Tensor, y: torch.Tensor | None, *,
     """``h = x + residual``, ``r = rsqrt(mean(h^2) + eps)``, ``u = h r``,
     ``y = u gamma``; q, s take the 8-bit checkpoint of u and r ``[rows]`` fp32
     the factor (both for :func:`rms_norm_backward`).  Returns y."""
-    rows, C = x.shape
-    _rows("rms_norm", C, x.dtype, rows, residual=residual, h=h, y=y)
-    _vec("rms_norm", C, x.dtype, gamma=gamma)
-    _vec("rms_norm", rows, torch.float32, r=r)
-    pq, ps = _ckpt("rms_norm", rows, C, q, s)
-    check(lib().instant_rms_norm(_dev(x, "x"), _opt(residual, "residual"), _dev(gamma, "gamma"),
-                                 _opt(h, "h"), _opt(y, "y"), pq, ps, _opt(r, "r"), rows, C, eps,
-                                 dtype_code(x.dtype), _stream(stream)), "instant_rms_norm")
+    rows, C = shape = x.shape
+    dt = x.dtype
+    p = (_ptr(x, shape, dt), _ptr(residual, shape, dt), _ptr(gamma, (C,), dt), _ptr(h, shape, dt),
+         _ptr(y, shape, dt), *_ckpt_ptrs(rows, C, q, s), _ptr(r, (rows,), torch.float32))
+    if -1 in p:
+        _refuse("rms_norm", ("x", x, shape, dt), ("residual", residual, shape, dt), ("h", h, shape, dt),
+                ("y", y, shape, dt), ("gamma", gamma, (C,), dt), ("r", r, (rows,), torch.float32),
+                ckpts=[(q, s, rows, C, ("q", "s"))])
+    check(lib().instant_rms_norm(*p, rows, C, eps, dtype_code(dt), _stream(stream)), "instant_rms_norm")
     return y
 
 
 def rms_norm_backward_workspace(rows: int, C: int, device) -> torch.Tensor:
-    n = int(lib().instant_rms_norm_backward_workspace_bytes(rows, C))
+    n = lib().instant_rms_norm_backward_workspace_bytes(rows, C)
     return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
 
 
@@ -587,17 +619,17 @@ def rms_norm_backward(g_y: torch.Tensor, q: torch.Tensor, s: torch.Tensor, r: to
     """Gradient of :func:`rms_norm` from the checkpoint of u: ``gx`` (with the
     gradient ``residual`` that bypassed the norm added) and ``ggamma`` ``[C]``
     fp32 (added to with ``accumulate``).  Returns ``(gx, ggamma)``."""
-    rows, C = g_y.shape
-    _rows("rms_norm_backward", C, g_y.dtype, rows, gx=gx, residual=residual)
-    _vec("rms_norm_backward", C, g_y.dtype, gamma=gamma)
-    _vec("rms_norm_backward", rows, torch.float32, r=r)
-    _vec("rms_norm_backward", C, torch.float32, ggamma=ggamma)
-    pq, ps = _ckpt("rms_norm_backward", rows, C, q, s)
-    check(lib().instant_rms_norm_backward(
-        _dev(g_y, "g_y"), pq, ps, _dev(r, "r"), _dev(gamma, "gamma"), _opt(residual, "residual"),
-        _dev(gx, "gx"), _dev(ggamma, "ggamma"), int(bool(accumulate)), _dev(ws, "ws"),
-        ws.numel() * ws.element_size(), rows, C, dtype_code(g_y.dtype), _stream(stream)),
-        "instant_rms_norm_backward")
+    rows, C = shape = g_y.shape
+    dt, f32 = g_y.dtype, torch.float32
+    p = (_ptr(g_y, shape, dt), *_ckpt_ptrs(rows, C, q, s), _ptr(r, (rows,), f32), _ptr(gamma, (C,), dt),
+         _ptr(residual, shape, dt), _ptr(gx, shape, dt), _ptr(ggamma, (C,), f32))
+    if -1 in p:
+        _refuse("rms_norm_backward", ("g_y", g_y, shape, dt), ("gx", gx, shape, dt),
+                ("residual", residual, shape, dt), ("gamma", gamma, (C,), dt), ("r", r, (rows,), f32),
+                ("ggamma", ggamma, (C,), f32), ckpts=[(q, s, rows, C, ("q", "s"))])
+    check(lib().instant_rms_norm_backward(*p, int(accumulate), _dev(ws, "ws"),
+                                          ws.numel() * ws.element_size(), rows, C, dtype_code(dt),
+                                          _stream(stream)), "instant_rms_norm_backward")
     return gx, ggamma
 
 
@@ -609,16 +641,17 @@ def linear_act(x: torch.Tensor, w: torch.Tensor, y: torch.Tensor | None, *,
     """``z = x w^T + bias``, ``y = act(z) + residual``: x ``[rows, Cx]``, w ``[Cy, Cx]``,
     y ``[rows, Cy]``; zq, zs take the 8-bit checkpoint of z, yq, ys that of y.
     act: "none", "relu", "gelu" (erf form) or "silu".  Returns y."""
-    rows, Cx = x.shape
+    rows, Cx = shape = x.shape
     Cy = w.shape[0]
-    _rows("linear_act", Cx, x.dtype, Cy, w=w)
-    _rows("linear_act", Cy, x.dtype, rows, y=y, residual=residual)
-    _vec("linear_act", Cy, x.dtype, bias=bias)
-    pzq, pzs = _ckpt("linear_act", rows, Cy, zq, zs, ("zq", "zs"))
-    pyq, pys = _ckpt("linear_act", rows, Cy, yq, ys, ("yq", "ys"))
-    check(lib().instant_linear_act(_dev(x, "x"), _dev(w, "w"), _opt(bias, "bias"),
-                                   _opt(residual, "residual"), _opt(y, "y"), pzq, pzs, pyq, pys, rows,
-                                   Cx, Cy, _act(act), dtype_code(x.dtype), _stream(stream)),
+    dt = x.dtype
+    out = (rows, Cy)
+    p = (_ptr(x, shape, dt), _ptr(w, (Cy, Cx), dt), _ptr(bias, (Cy,), dt), _ptr(residual, out, dt),
+         _ptr(y, out, dt), *_ckpt_ptrs(rows, Cy, zq, zs), *_ckpt_ptrs(rows, Cy, yq, ys))
+    if -1 in p:
+        _refuse("linear_act", ("x", x, shape, dt), ("w", w, (Cy, Cx), dt), ("y", y, out, dt),
+                ("residual", residual, out, dt), ("bias", bias, (Cy,), dt),
+                ckpts=[(zq, zs, rows, Cy, ("zq", "zs")), (yq, ys, rows, Cy, ("yq", "ys"))])
+    check(lib().instant_linear_act(*p, rows, Cx, Cy, _act(act), dtype_code(dt), _stream(stream)),
           "instant_linear_act")
     return y
 
@@ -628,20 +661,22 @@ def linear_act_grad(g_y: torch.Tensor, w: torch.Tensor, gx: torch.Tensor, *, act
                     residual: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """``gx = (g_y w) act'(z) + residual``: g_y ``[rows, Cy]``, w ``[Cy, Cx]``, gx
     ``[rows, Cx]``; zq, zs is the checkpoint of the activation's input z."""
-    rows, Cy = g_y.shape
+    rows, Cy = shape = g_y.shape
     Cx = w.shape[1] if w.dim() == 2 else -1
-    _rows("linear_act_grad", Cx, g_y.dtype, Cy, w=w)
-    _rows("linear_act_grad", Cx, g_y.dtype, rows, gx=gx, residual=residual)
-    pq, ps = _ckpt("linear_act_grad", rows, Cx, zq, zs, ("zq", "zs"))
-    check(lib().instant_linear_act_grad(_dev(g_y, "g_y"), _dev(w, "w"), pq, ps,
-                                        _opt(residual, "residual"), _dev(gx, "gx"), rows, Cx, Cy,
-                                        _act(act), dtype_code(g_y.dtype), _stream(stream)),
+    dt = g_y.dtype
+    out = (rows, Cx)
+    p = (_ptr(g_y, shape, dt), _ptr(w, (Cy, Cx), dt), *_ckpt_ptrs(rows, Cx, zq, zs),
+         _ptr(residual, out, dt), _ptr(gx, out, dt))
+    if -1 in p:
+        _refuse("linear_act_grad", ("g_y", g_y, shape, dt), ("w", w, (Cy, Cx), dt), ("gx", gx, out, dt),
+                ("residual", residual, out, dt), ckpts=[(zq, zs, rows, Cx, ("zq", "zs"))])
+    check(lib().instant_linear_act_grad(*p, rows, Cx, Cy, _act(act), dtype_code(dt), _stream(stream)),
           "instant_linear_act_grad")
     return gx
 
 
 def ckpt_grad_w_workspace(rows: int, Cx: int, Cy: int, device) -> torch.Tensor:
-    n = int(lib().instant_ckpt_grad_w_workspace_bytes(rows, Cx, Cy))
+    n = lib().instant_ckpt_grad_w_workspace_bytes(rows, Cx, Cy)
     return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
 
 
@@ -653,24 +688,25 @@ def ckpt_grad_w(g_y: torch.Tensor, q: torch.Tensor, s: torch.Tensor, gw: torch.T
     ``[Cy, Cx]`` fp32, gb ``[Cy]`` fp32 (needs ws).  ws from
     :func:`ckpt_grad_w_workspace`; without gb it may be left out, and bf16 calls
     then allocate it.  Returns ``(gw, gb)``."""
-    rows, Cy = g_y.shape
+    rows, Cy = shape = g_y.shape
     Cx = gw.shape[1] if gw.dim() == 2 else -1
-    _rows("ckpt_grad_w", Cx, torch.float32, Cy, gw=gw)
-    _vec("ckpt_grad_w", Cx, g_y.dtype, col_scale=col_scale)
-    _vec("ckpt_grad_w", Cy, torch.float32, gb=gb)
+    dt, f32 = g_y.dtype, torch.float32
     if gb is not None and ws is None:
         raise ValueError("ckpt_grad_w: gb needs a workspace")
-    pq, ps = _ckpt("ckpt_grad_w", rows, Cx, q, s)
-    if ws is None and g_y.dtype == torch.bfloat16:
+    p = (_ptr(g_y, shape, dt), *_ckpt_ptrs(rows, Cx, q, s), _ptr(col_scale, (Cx,), dt),
+         _ptr(gw, (Cy, Cx), f32), _ptr(gb, (Cy,), f32))
+    if -1 in p:
+        _refuse("ckpt_grad_w", ("gw", gw, (Cy, Cx), f32), ("g_y", g_y, shape, dt),
+                ("col_scale", col_scale, (Cx,), dt), ("gb", gb, (Cy,), f32),
+                ckpts=[(q, s, rows, Cx, ("q", "s"))])
+    if ws is None and dt == torch.bfloat16:
         ws = ckpt_grad_w_workspace(rows, Cx, Cy, g_y.device)
         if stream is not None:
             ws.record_stream(stream if isinstance(stream, torch.cuda.Stream)
                              else torch.cuda.ExternalStream(int(stream)))
-    check(lib().instant_ckpt_grad_w(_dev(g_y, "g_y"), pq, ps, _opt(col_scale, "col_scale"),
-                                    _dev(gw, "gw"), _opt(gb, "gb"), int(bool(accumulate)),
-                                    _opt(ws, "ws"),
+    check(lib().instant_ckpt_grad_w(*p, int(accumulate), None if ws is None else _dev(ws, "ws"),
                                     0 if ws is None else ws.numel() * ws.element_size(), rows, Cx, Cy,
-                                    dtype_code(g_y.dtype), _stream(stream)), "instant_ckpt_grad_w")
+                                    dtype_code(dt), _stream(stream)), "instant_ckpt_grad_w")
     return gw, gb
 
 

@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libinstant.so")
 SOURCES = ["capi.cu", "project.cu", "gemm.cu", "expand.cu", "gradx_fused.cu", "syrk.cu", "eig.cu",
            "static_scratch.cu", "recon.cu", "gradw_stream.cu",
            "forward.cu", "ckpt.cu", "rmsnorm.cu", "linear_simt.cu", "linear_tc.cu",
-           "block_capi.cu"]
+           "linear_few.cu", "block_capi.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-I", INCLUDE, "-I", CSRC]

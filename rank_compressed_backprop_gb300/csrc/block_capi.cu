@@ -2,6 +2,7 @@
 // in include/instant.h (norm, products with epilogues, 8-bit checkpoints):
 // argument validation and launch planning.  No device memory is allocated here.
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 
 #include "instant.h"
@@ -35,9 +36,26 @@ CkptRef ref(const void* q, const void* s) {
 bool align_ok(instant_dtype dt, int C) { return dt == INSTANT_F32 || C % 8 == 0; }
 bool vec_ok(instant_dtype dt, int C) { return C % (dt == INSTANT_F32 ? 4 : 8) == 0; }
 
-// bf16 products run on the tensor cores, fp32 ones on FFMA
+// bf16 products run on the tensor cores, fp32 ones on FFMA.  Of the two tensor-core
+// kernels the one with the smaller estimate runs:
+//   CTA pairs, 256 x 256 tiles      4.5 us + 0.34 us a chunk of 64 and wave of 76 tiles
+//   split K, 128 x NT tiles         8 us + 0.28 us (NT = 128), 0.15 (64) or 0.13 a
+//                                   chunk, over the SMs
+// which are fits to both kernels timed over 14 shapes of each product.  Measured
+// (rows x K -> N, split K against pairs, us): forward 1 x 4096 -> 11008 16.6 / 42.4,
+// 128 x 4096 -> 11008 21.8 / 26.5, 256 x 4096 -> 11008 33.6 / 26.9, 512 x 4096 -> 4096
+// 20.7 / 25.9, 2048 x 2048 -> 2048 20.1 / 16.3; back 1 x 11008 -> 4096 17.7 / 59.7,
+// 1024 x 4096 -> 1024 14.7 / 25.1; weight gradient over 4096 rows, 1024 x 1024
+// 17.9 / 31.4, over 700 rows, 1792 x 448 11.4 / 10.5.
 cudaError_t launch_linear(const LinearArgs& a, bool bf16, cudaStream_t st) {
-  return bf16 ? launch_linear_tc(a, st) : launch_linear_simt(a, false, st);
+  if (!bf16) return launch_linear_simt(a, false, st);
+  const int nt = few_rows_tile(a);
+  const double nk = cdiv(a.K, 64);
+  const double waves = std::ceil(static_cast<double>(cdiv(a.M, 256)) * cdiv(a.N, 256) / std::max(1, sm_count() / 2));
+  const double pairs_us = 4.5 + 0.34 * nk * waves;
+  const double chunk_us = nt == 128 ? 0.28 : nt == 64 ? 0.15 : 0.13;
+  const double few_us = 8.0 + chunk_us * nk * cdiv(a.N, 128) * cdiv(a.M, nt) / sm_count();
+  return few_us < pairs_us ? launch_linear_few(a, st) : launch_linear_tc(a, st);
 }
 
 }  // namespace

@@ -387,6 +387,20 @@ struct TcMaps {
 };
 cudaError_t launch_linear_tc(const LinearArgs& a, cudaStream_t st);
 
+// the same for outputs of few tiles (linear_few.cu)
+struct FewArgs {
+  int M, N, K;
+  int nk;              // 64-deep chunks
+  int splits, per;     // shares of K (CTAs of a cluster), chunks of a share
+  const void* bias;    // as in LinearArgs
+  const void* res;
+  void* out;
+  CkptRef zk, yk, ck;
+  int ld, act, accumulate;
+};
+int few_rows_tile(const LinearArgs& a);  // its row tile for this product: 16, 32, 64 or 128
+cudaError_t launch_linear_few(const LinearArgs& a, cudaStream_t st);
+
 // tiled tensor map with the 128-byte swizzle; dims/strides innermost first
 bool make_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
               const uint64_t* strides_bytes, const uint32_t* box,
@@ -469,5 +483,6 @@ cudaError_t read_fault_fused(unsigned int* out, int clear);
 cudaError_t read_fault_gradw(unsigned int* out, int clear);
 cudaError_t read_fault_forward(unsigned int* out, int clear);
 cudaError_t read_fault_linear(unsigned int* out, int clear);
+cudaError_t read_fault_few(unsigned int* out, int clear);
 
 }  // namespace instant
