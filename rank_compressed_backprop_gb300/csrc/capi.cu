@@ -1533,6 +1533,8 @@ instant_status instant_device_status(int clear, void* stream) {
   total |= v;
   if (read_fault_few(&v, clear) != cudaSuccess) return INSTANT_ERR_CUDA;
   total |= v;
+  if (read_fault_norm(&v, clear) != cudaSuccess) return INSTANT_ERR_CUDA;
+  total |= v;
   return total ? INSTANT_ERR_DEVICE : INSTANT_OK;
 }
 

@@ -5,6 +5,8 @@
 // All three are bound by HBM: pack reads each element once and writes one byte
 // for it, unpack the reverse.  A half warp owns one group of 128 channels, eight
 // channels a lane, so that the group's largest magnitude is four shuffles away.
+#include <algorithm>
+
 #include "ckpt.cuh"
 
 namespace instant {
@@ -13,57 +15,79 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// A CTA takes `gp` neighbouring groups (a power of two up to 16) of 16 / gp rows
+// at a time, four such steps under way together, and walks down its rows: no
+// index needs a division.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
     k_ckpt_pack(const T* __restrict__ x, int8_t* __restrict__ q, uint8_t* __restrict__ s, int rows,
-                int C, int ld, int groups, int vec) {
+                int C, int ld, int gp, int per, int vec) {
   pdl_launch_dependents();
   pdl_wait();
-  const int hl = threadIdx.x & 15;
-  const long long total = static_cast<long long>(rows) * groups;
-  const long long stride = static_cast<long long>(gridDim.x) * (kThreads / 16);
+  constexpr int kUnroll = 4;
+  const int hl = threadIdx.x & 15, h = threadIdx.x >> 4;
+  const int g = blockIdx.x * gp + (h & (gp - 1));
+  const int step = 16 / gp;
+  const int c = g * kCkptGroup + 8 * hl;
+  const int r1 = min(rows, (static_cast<int>(blockIdx.y) + 1) * per);
   // whole warps stay in the loop together: the shuffles name all 32 lanes
-  for (long long i0 = static_cast<long long>(blockIdx.x) * (kThreads / 16); i0 < total; i0 += stride) {
-    const long long i = i0 + (threadIdx.x >> 4);
-    const bool on = i < total;
-    const int row = on ? static_cast<int>(i / groups) : 0;
-    const int g = on ? static_cast<int>(i - static_cast<long long>(row) * groups) : 0;
-    const int c = g * kCkptGroup + 8 * hl;
-    float v[8];
-    load_part<8>(x + static_cast<size_t>(row) * C + c, on ? C - c : 0, vec, v);
-    uint32_t m = 0;
+  for (int r0 = blockIdx.y * per; r0 < r1; r0 += kUnroll * step) {
+    float2 v[kUnroll][4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) m = max(m, abs_bits(v[e]));
-    const uint32_t code = ckpt_scale_code(half_warp_max(m));
-    const float inv = ckpt_inv_scale(code);
-    if (on && c < C)
-      *reinterpret_cast<uint2*>(q + static_cast<size_t>(row) * ld + c) =
-          make_uint2(ckpt_code4(v[0], v[1], v[2], v[3], inv), ckpt_code4(v[4], v[5], v[6], v[7], inv));
-    if (on && hl == 0) s[static_cast<size_t>(g) * rows + row] = static_cast<uint8_t>(code);
+    for (int j = 0; j < kUnroll; ++j) {
+      const int row = r0 + j * step + h / gp;
+      const bool on = row < r1;
+      load_pairs(x + static_cast<size_t>(on ? row : 0) * C + c, on ? C - c : 0, vec, v[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j) {
+      const int row = r0 + j * step + h / gp;
+      const bool on = row < r1 && c < C;
+      const uint32_t code = group_code(v[j]);
+      const float inv = ckpt_inv_scale(code);
+      if (on) {
+        *reinterpret_cast<uint2*>(q + static_cast<size_t>(row) * ld + c) =
+            make_uint2(ckpt_code4_any(v[j][0], v[j][1], code, inv), ckpt_code4_any(v[j][2], v[j][3], code, inv));
+        if (hl == 0) s[static_cast<size_t>(g) * rows + row] = static_cast<uint8_t>(code);
+      }
+    }
   }
 }
 
+// A thread takes eight channels of a row (8 bytes in, 16 out), four rows at once;
+// a CTA `cp` neighbouring threads' channels of 256 / cp rows.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
     k_ckpt_unpack(const int8_t* __restrict__ q, const uint8_t* __restrict__ s, T* __restrict__ x,
-                  int rows, int C, int ld, int chunks, int vec) {
+                  int rows, int C, int ld, int cp, int per, int vec) {
   pdl_launch_dependents();
   pdl_wait();
-  const long long total = static_cast<long long>(rows) * chunks;  // 16 channels each
-  const long long stride = static_cast<long long>(gridDim.x) * kThreads;
-  for (long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; i < total; i += stride) {
-    const int row = static_cast<int>(i / chunks);
-    const int c = 16 * static_cast<int>(i - static_cast<long long>(row) * chunks);
-    const uint4 w = *reinterpret_cast<const uint4*>(q + static_cast<size_t>(row) * ld + c);
-    const float scale = ckpt_scale(s[static_cast<size_t>(c / kCkptGroup) * rows + row]);
-    float v[16];
-    ckpt_values4(w.x, scale, v);
-    ckpt_values4(w.y, scale, v + 4);
-    ckpt_values4(w.z, scale, v + 8);
-    ckpt_values4(w.w, scale, v + 12);
-    T* dst = x + static_cast<size_t>(row) * C + c;
-    store_part<8>(dst, C - c, vec, v);
-    if (C - c > 8) store_part<8>(dst + 8, C - c - 8, vec, v + 8);
+  constexpr int kUnroll = 4;
+  const int c = 8 * (blockIdx.x * cp + (threadIdx.x & (cp - 1)));
+  if (c >= C) return;
+  const int step = kThreads / cp;
+  const uint8_t* sg = s + static_cast<size_t>(c / kCkptGroup) * rows;
+  const int r1 = min(rows, (static_cast<int>(blockIdx.y) + 1) * per);
+  for (int r0 = blockIdx.y * per + static_cast<int>(threadIdx.x) / cp; r0 < r1; r0 += kUnroll * step) {
+    uint2 w[kUnroll];
+    float scale[kUnroll];
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j) {
+      const int row = r0 + j * step;
+      if (row < r1) {
+        w[j] = *reinterpret_cast<const uint2*>(q + static_cast<size_t>(row) * ld + c);
+        scale[j] = ckpt_scale(sg[row]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j) {
+      const int row = r0 + j * step;
+      if (row >= r1) break;
+      float2 v[4];
+      ckpt_pairs4(w[j].x, scale[j], v);
+      ckpt_pairs4(w[j].y, scale[j], v + 2);
+      store_pairs(x + static_cast<size_t>(row) * C + c, C - c, vec, v);
+    }
   }
 }
 
@@ -100,34 +124,43 @@ __global__ void __launch_bounds__(kThreads)
   if (col < C) part[static_cast<size_t>(blockIdx.y) * C + col] = sum;
 }
 
-// out[c] (+)= sum_p part[p][c]: 32 columns a CTA, eight warps share the parts
-__global__ void __launch_bounds__(kThreads)
+// out[c] (+)= sum_p part[p][c]: 32 columns a CTA, 32 warps share the parts
+__global__ void __launch_bounds__(1024)
     k_part_sum(const float* __restrict__ part, float* __restrict__ out, int parts, int C,
                int accumulate) {
-  __shared__ float red[8][32];
+  __shared__ float red[32][33];
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float acc = 0.f;
   if (c < C) {
-#pragma unroll 8
-    for (int p = warp; p < parts; p += 8) acc += part[static_cast<size_t>(p) * C + c];
+#pragma unroll 10
+    for (int p = warp; p < parts; p += 32) acc += part[static_cast<size_t>(p) * C + c];
   }
   red[warp][lane] = acc;
   __syncthreads();
-  if (warp == 0 && c < C) {
-    float sum = 0.f;
+  // warp w adds up column w
+  float sum = red[lane][warp];
 #pragma unroll
-    for (int w = 0; w < 8; ++w) sum += red[w][lane];
-    out[c] = accumulate ? out[c] + sum : sum;
-  }
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const int cw = blockIdx.x * 32 + warp;
+  if (lane == 0 && cw < C) out[cw] = accumulate ? out[cw] + sum : sum;
 }
 
-int grid_for(long long work, int per_cta, int per_sm) {
-  const long long n = (work + per_cta - 1) / per_cta;
-  const long long cap = static_cast<long long>(per_sm) * sm_count();
-  return static_cast<int>(n < cap ? n : cap);
+// the smallest power of two that is at least n, or `most`
+int pow2_up(int n, int most) {
+  int p = 1;
+  while (p < n && p < most) p *= 2;
+  return p;
+}
+
+// rows a CTA walks when a column of CTAs shares the rows: about `ctas` CTAs in
+// all, a multiple of `pass` rows, and no more than 65535 CTAs a column
+int rows_per_cta(int rows, int columns, int pass, int ctas) {
+  const long long want = std::max(1ll, static_cast<long long>(ctas) / columns);
+  const long long per = std::max((rows + want - 1) / want, (static_cast<long long>(rows) + 65534) / 65535);
+  return static_cast<int>((per + pass - 1) / pass * pass);
 }
 
 }  // namespace
@@ -135,25 +168,31 @@ int grid_for(long long work, int per_cta, int per_sm) {
 cudaError_t launch_ckpt_pack(const void* x, const CkptRef& k, int rows, int C, bool bf16, bool vec,
                              cudaStream_t st) {
   const int groups = (C + kCkptGroup - 1) / kCkptGroup;
-  const int grid = grid_for(static_cast<long long>(rows) * groups, kThreads / 16, 32);
+  const int gp = pow2_up(groups, 16);
+  const int columns = (groups + gp - 1) / gp;
+  const int per = rows_per_cta(rows, columns, 4 * 16 / gp, 16 * sm_count());
+  const dim3 grid(columns, (rows + per - 1) / per);
   if (bf16)
-    return launch_ex(k_ckpt_pack<uint16_t>, dim3(grid), dim3(kThreads), 0, st, 1, pdl_enabled(),
-                     static_cast<const uint16_t*>(x), k.q, k.s, rows, C, ckpt_ld(C), groups, int(vec));
-  return launch_ex(k_ckpt_pack<float>, dim3(grid), dim3(kThreads), 0, st, 1, pdl_enabled(),
-                   static_cast<const float*>(x), k.q, k.s, rows, C, ckpt_ld(C), groups, int(vec));
+    return launch_ex(k_ckpt_pack<uint16_t>, grid, dim3(kThreads), 0, st, 1, pdl_enabled(),
+                     static_cast<const uint16_t*>(x), k.q, k.s, rows, C, ckpt_ld(C), gp, per, int(vec));
+  return launch_ex(k_ckpt_pack<float>, grid, dim3(kThreads), 0, st, 1, pdl_enabled(),
+                   static_cast<const float*>(x), k.q, k.s, rows, C, ckpt_ld(C), gp, per, int(vec));
 }
 
 cudaError_t launch_ckpt_unpack(const CkptRef& k, void* x, int rows, int C, bool bf16, bool vec,
                                cudaStream_t st) {
-  const int chunks = (C + 15) / 16;
-  const int grid = grid_for(static_cast<long long>(rows) * chunks, kThreads, 32);
+  const int chunks = (C + 7) / 8;
+  const int cp = pow2_up(chunks, kThreads);
+  const int columns = (chunks + cp - 1) / cp;
+  const int per = rows_per_cta(rows, columns, 4 * kThreads / cp, 16 * sm_count());
+  const dim3 grid(columns, (rows + per - 1) / per);
   if (bf16)
-    return launch_ex(k_ckpt_unpack<uint16_t>, dim3(grid), dim3(kThreads), 0, st, 1, pdl_enabled(),
+    return launch_ex(k_ckpt_unpack<uint16_t>, grid, dim3(kThreads), 0, st, 1, pdl_enabled(),
                      static_cast<const int8_t*>(k.q), static_cast<const uint8_t*>(k.s),
-                     static_cast<uint16_t*>(x), rows, C, ckpt_ld(C), chunks, int(vec));
-  return launch_ex(k_ckpt_unpack<float>, dim3(grid), dim3(kThreads), 0, st, 1, pdl_enabled(),
+                     static_cast<uint16_t*>(x), rows, C, ckpt_ld(C), cp, per, int(vec));
+  return launch_ex(k_ckpt_unpack<float>, grid, dim3(kThreads), 0, st, 1, pdl_enabled(),
                    static_cast<const int8_t*>(k.q), static_cast<const uint8_t*>(k.s),
-                   static_cast<float*>(x), rows, C, ckpt_ld(C), chunks, int(vec));
+                   static_cast<float*>(x), rows, C, ckpt_ld(C), cp, per, int(vec));
 }
 
 // row shares of the column sums: enough CTAs for four per SM, at least 32 rows each
@@ -166,7 +205,7 @@ int col_sum_parts(int rows, int C) {
 
 cudaError_t launch_part_sum(const float* part, float* out, int parts, int C, int accumulate,
                             cudaStream_t st) {
-  return launch_ex(k_part_sum, dim3((C + 31) / 32), dim3(kThreads), 0, st, 1, pdl_enabled(), part, out,
+  return launch_ex(k_part_sum, dim3((C + 31) / 32), dim3(1024), 0, st, 1, pdl_enabled(), part, out,
                    parts, C, accumulate);
 }
 

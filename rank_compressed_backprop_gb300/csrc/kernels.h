@@ -484,5 +484,6 @@ cudaError_t read_fault_gradw(unsigned int* out, int clear);
 cudaError_t read_fault_forward(unsigned int* out, int clear);
 cudaError_t read_fault_linear(unsigned int* out, int clear);
 cudaError_t read_fault_few(unsigned int* out, int clear);
+cudaError_t read_fault_norm(unsigned int* out, int clear);
 
 }  // namespace instant
