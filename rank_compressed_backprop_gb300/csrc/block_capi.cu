@@ -31,10 +31,10 @@ CkptRef ref(const void* q, const void* s) {
   return r;
 }
 
-// bf16 rows are read and written 16 bytes at a time; fp32 rows may be any width
-// and take wide accesses where C is a multiple of 4
+// bf16 rows are read and written in whole vectors of eight channels; fp32 rows
+// may be any width and are where C allows it
 bool align_ok(instant_dtype dt, int C) { return dt == INSTANT_F32 || C % 8 == 0; }
-bool vec_ok(instant_dtype dt, int C) { return C % (dt == INSTANT_F32 ? 4 : 8) == 0; }
+bool vec_ok(int C) { return C % 8 == 0; }
 
 // bf16 products run on the tensor cores, fp32 ones on FFMA.  Of the two tensor-core
 // kernels the one with the smaller estimate runs:
@@ -68,7 +68,7 @@ instant_status instant_ckpt_pack(const void* x, void* q, void* s, int rows, int 
   if (!x || !q || !s) return INSTANT_ERR_ARG;
   if (!extent_ok(rows, C)) return INSTANT_ERR_SHAPE;
   if (!aligned16(x) || !aligned16(q) || !align_ok(dt, C)) return INSTANT_ERR_ALIGN;
-  return from_cuda(launch_ckpt_pack(x, ref(q, s), rows, C, dt == INSTANT_BF16, vec_ok(dt, C),
+  return from_cuda(launch_ckpt_pack(x, ref(q, s), rows, C, dt == INSTANT_BF16, vec_ok(C),
                                     static_cast<cudaStream_t>(stream)));
 }
 
@@ -78,7 +78,7 @@ instant_status instant_ckpt_unpack(const void* q, const void* s, void* x, int ro
   if (!x || !q || !s) return INSTANT_ERR_ARG;
   if (!extent_ok(rows, C)) return INSTANT_ERR_SHAPE;
   if (!aligned16(x) || !aligned16(q) || !align_ok(dt, C)) return INSTANT_ERR_ALIGN;
-  return from_cuda(launch_ckpt_unpack(ref(q, s), x, rows, C, dt == INSTANT_BF16, vec_ok(dt, C),
+  return from_cuda(launch_ckpt_unpack(ref(q, s), x, rows, C, dt == INSTANT_BF16, vec_ok(C),
                                       static_cast<cudaStream_t>(stream)));
 }
 
@@ -102,7 +102,7 @@ instant_status instant_rms_norm(const void* x, const void* residual, const void*
   a.rows = rows;
   a.C = C;
   a.ld = ckpt_ld(C);
-  a.vec = vec_ok(dt, C);
+  a.vec = vec_ok(C);
   a.eps = eps;
   return from_cuda(launch_rms_norm(a, dt == INSTANT_BF16, static_cast<cudaStream_t>(stream)));
 }
@@ -135,7 +135,7 @@ instant_status instant_rms_norm_backward(const void* gy, const void* q, const vo
   a.rows = rows;
   a.C = C;
   a.ld = ckpt_ld(C);
-  a.vec = vec_ok(dt, C);
+  a.vec = vec_ok(C);
   a.accumulate = accumulate != 0;
   return from_cuda(launch_rms_norm_back(a, dt == INSTANT_BF16, static_cast<cudaStream_t>(stream)));
 }
@@ -164,7 +164,7 @@ instant_status instant_linear_act(const void* x, const void* w, const void* bias
   a.yk = ref(yq, ys);
   a.ld = ckpt_ld(Cy);
   a.act = act;
-  a.vec = vec_ok(dt, Cy);
+  a.vec = vec_ok(Cy);
   return from_cuda(launch_linear(a, dt == INSTANT_BF16, static_cast<cudaStream_t>(stream)));
 }
 
@@ -190,7 +190,7 @@ instant_status instant_linear_act_grad(const void* gy, const void* w, const void
   a.ck = ref(zq, zs);
   a.ld = ckpt_ld(Cx);
   a.act = act;
-  a.vec = vec_ok(dt, Cx);
+  a.vec = vec_ok(Cx);
   return from_cuda(launch_linear(a, dt == INSTANT_BF16, static_cast<cudaStream_t>(stream)));
 }
 
@@ -228,7 +228,7 @@ instant_status instant_ckpt_grad_w(const void* gy, const void* q, const void* s,
   a.ck = ref(q, s);
   a.ld = ckpt_ld(Cx);
   a.accumulate = accumulate != 0;
-  a.vec = vec_ok(dt, Cx);
+  a.vec = vec_ok(Cx);
   cudaError_t e = cudaSuccess;
   if (bf16) {
     // the values are exact in bf16 and every row tile of gw reads them: made once
@@ -238,7 +238,7 @@ instant_status instant_ckpt_grad_w(const void* gy, const void* q, const void* s,
   if (e == cudaSuccess) e = launch_linear(a, bf16, st);
   if (e == cudaSuccess && gb)
     e = launch_col_sum(gy, gb, reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + values_bytes(rows, Cx)),
-                       rows, Cy, accumulate != 0, bf16, vec_ok(dt, Cy), st);
+                       rows, Cy, accumulate != 0, bf16, vec_ok(Cy), st);
   return from_cuda(e);
 }
 

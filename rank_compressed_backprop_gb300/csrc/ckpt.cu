@@ -18,10 +18,10 @@ constexpr int kThreads = 256;
 // A CTA takes `gp` neighbouring groups (a power of two up to 16) of 16 / gp rows
 // at a time, four such steps under way together, and walks down its rows: no
 // index needs a division.
-template <typename T>
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads)
     k_ckpt_pack(const T* __restrict__ x, int8_t* __restrict__ q, uint8_t* __restrict__ s, int rows,
-                int C, int ld, int gp, int per, int vec) {
+                int C, int ld, int gp, int per) {
   pdl_launch_dependents();
   pdl_wait();
   constexpr int kUnroll = 4;
@@ -29,25 +29,26 @@ __global__ void __launch_bounds__(kThreads)
   const int g = blockIdx.x * gp + (h & (gp - 1));
   const int step = 16 / gp;
   const int c = g * kCkptGroup + 8 * hl;
+  const int cc = VEC && c >= C ? 0 : c;
   const int r1 = min(rows, (static_cast<int>(blockIdx.y) + 1) * per);
   // whole warps stay in the loop together: the shuffles name all 32 lanes
   for (int r0 = blockIdx.y * per; r0 < r1; r0 += kUnroll * step) {
     float2 v[kUnroll][4];
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j) {
-      const int row = r0 + j * step + h / gp;
-      const bool on = row < r1;
-      load_pairs(x + static_cast<size_t>(on ? row : 0) * C + c, on ? C - c : 0, vec, v[j]);
+      // past the last row the last one again, past the last column the row's first
+      // (neither is stored, and the latter does not count for its group)
+      const int row = min(r0 + j * step + h / gp, r1 - 1);
+      load_pairs<VEC>(x + static_cast<size_t>(row) * C + cc, VEC ? 8 : C - c, v[j]);
     }
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j) {
       const int row = r0 + j * step + h / gp;
       const bool on = row < r1 && c < C;
-      const uint32_t code = group_code(v[j]);
-      const float inv = ckpt_inv_scale(code);
+      const uint32_t code = ckpt_scale_code(half_warp_max(c < C ? max_bits8(v[j]) : 0u));
+      const uint2 w = ckpt_code8(v[j], code);
       if (on) {
-        *reinterpret_cast<uint2*>(q + static_cast<size_t>(row) * ld + c) =
-            make_uint2(ckpt_code4_any(v[j][0], v[j][1], code, inv), ckpt_code4_any(v[j][2], v[j][3], code, inv));
+        *reinterpret_cast<uint2*>(q + static_cast<size_t>(row) * ld + c) = w;
         if (hl == 0) s[static_cast<size_t>(g) * rows + row] = static_cast<uint8_t>(code);
       }
     }
@@ -56,10 +57,10 @@ __global__ void __launch_bounds__(kThreads)
 
 // A thread takes eight channels of a row (8 bytes in, 16 out), four rows at once;
 // a CTA `cp` neighbouring threads' channels of 256 / cp rows.
-template <typename T>
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads)
     k_ckpt_unpack(const int8_t* __restrict__ q, const uint8_t* __restrict__ s, T* __restrict__ x,
-                  int rows, int C, int ld, int cp, int per, int vec) {
+                  int rows, int C, int ld, int cp, int per) {
   pdl_launch_dependents();
   pdl_wait();
   constexpr int kUnroll = 4;
@@ -84,9 +85,8 @@ __global__ void __launch_bounds__(kThreads)
       const int row = r0 + j * step;
       if (row >= r1) break;
       float2 v[4];
-      ckpt_pairs4(w[j].x, scale[j], v);
-      ckpt_pairs4(w[j].y, scale[j], v + 2);
-      store_pairs(x + static_cast<size_t>(row) * C + c, C - c, vec, v);
+      ckpt_pairs8(w[j], scale[j], v);
+      store_pairs<VEC>(x + static_cast<size_t>(row) * C + c, C - c, v);
     }
   }
 }
@@ -124,27 +124,30 @@ __global__ void __launch_bounds__(kThreads)
   if (col < C) part[static_cast<size_t>(blockIdx.y) * C + col] = sum;
 }
 
-// out[c] (+)= sum_p part[p][c]: 32 columns a CTA, 32 warps share the parts
-__global__ void __launch_bounds__(1024)
+// out[c] (+)= sum_p part[p][c]: eight columns a CTA (a 32-byte sector of each
+// share), 64 threads of each column take the shares in turn
+__global__ void __launch_bounds__(512)
     k_part_sum(const float* __restrict__ part, float* __restrict__ out, int parts, int C,
                int accumulate) {
-  __shared__ float red[32][33];
+  __shared__ float red[64][9];
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
+  const int col = threadIdx.x & 7, row = threadIdx.x >> 3;
+  const int c = blockIdx.x * 8 + col;
   float acc = 0.f;
   if (c < C) {
-#pragma unroll 10
-    for (int p = warp; p < parts; p += 32) acc += part[static_cast<size_t>(p) * C + c];
+#pragma unroll 8
+    for (int p = row; p < parts; p += 64) acc += part[static_cast<size_t>(p) * C + c];
   }
-  red[warp][lane] = acc;
+  red[row][col] = acc;
   __syncthreads();
   // warp w adds up column w
-  float sum = red[lane][warp];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (warp >= 8) return;
+  float sum = red[lane][warp] + red[lane + 32][warp];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  const int cw = blockIdx.x * 32 + warp;
+  const int cw = blockIdx.x * 8 + warp;
   if (lane == 0 && cw < C) out[cw] = accumulate ? out[cw] + sum : sum;
 }
 
@@ -172,11 +175,13 @@ cudaError_t launch_ckpt_pack(const void* x, const CkptRef& k, int rows, int C, b
   const int columns = (groups + gp - 1) / gp;
   const int per = rows_per_cta(rows, columns, 4 * 16 / gp, 16 * sm_count());
   const dim3 grid(columns, (rows + per - 1) / per);
-  if (bf16)
-    return launch_ex(k_ckpt_pack<uint16_t>, grid, dim3(kThreads), 0, st, 1, pdl_enabled(),
-                     static_cast<const uint16_t*>(x), k.q, k.s, rows, C, ckpt_ld(C), gp, per, int(vec));
-  return launch_ex(k_ckpt_pack<float>, grid, dim3(kThreads), 0, st, 1, pdl_enabled(),
-                   static_cast<const float*>(x), k.q, k.s, rows, C, ckpt_ld(C), gp, per, int(vec));
+  auto go = [&](auto kernel, auto* p) {
+    return launch_ex(kernel, grid, dim3(kThreads), 0, st, 1, pdl_enabled(), p, k.q, k.s, rows, C, ckpt_ld(C), gp,
+                     per);
+  };
+  if (bf16) return go(k_ckpt_pack<uint16_t, true>, static_cast<const uint16_t*>(x));
+  return vec ? go(k_ckpt_pack<float, true>, static_cast<const float*>(x))
+             : go(k_ckpt_pack<float, false>, static_cast<const float*>(x));
 }
 
 cudaError_t launch_ckpt_unpack(const CkptRef& k, void* x, int rows, int C, bool bf16, bool vec,
@@ -186,13 +191,13 @@ cudaError_t launch_ckpt_unpack(const CkptRef& k, void* x, int rows, int C, bool 
   const int columns = (chunks + cp - 1) / cp;
   const int per = rows_per_cta(rows, columns, 4 * kThreads / cp, 16 * sm_count());
   const dim3 grid(columns, (rows + per - 1) / per);
-  if (bf16)
-    return launch_ex(k_ckpt_unpack<uint16_t>, grid, dim3(kThreads), 0, st, 1, pdl_enabled(),
-                     static_cast<const int8_t*>(k.q), static_cast<const uint8_t*>(k.s),
-                     static_cast<uint16_t*>(x), rows, C, ckpt_ld(C), cp, per, int(vec));
-  return launch_ex(k_ckpt_unpack<float>, grid, dim3(kThreads), 0, st, 1, pdl_enabled(),
-                   static_cast<const int8_t*>(k.q), static_cast<const uint8_t*>(k.s),
-                   static_cast<float*>(x), rows, C, ckpt_ld(C), cp, per, int(vec));
+  auto go = [&](auto kernel, auto* p) {
+    return launch_ex(kernel, grid, dim3(kThreads), 0, st, 1, pdl_enabled(), static_cast<const int8_t*>(k.q),
+                     static_cast<const uint8_t*>(k.s), p, rows, C, ckpt_ld(C), cp, per);
+  };
+  if (bf16) return go(k_ckpt_unpack<uint16_t, true>, static_cast<uint16_t*>(x));
+  return vec ? go(k_ckpt_unpack<float, true>, static_cast<float*>(x))
+             : go(k_ckpt_unpack<float, false>, static_cast<float*>(x));
 }
 
 // row shares of the column sums: enough CTAs for four per SM, at least 32 rows each
@@ -205,7 +210,7 @@ int col_sum_parts(int rows, int C) {
 
 cudaError_t launch_part_sum(const float* part, float* out, int parts, int C, int accumulate,
                             cudaStream_t st) {
-  return launch_ex(k_part_sum, dim3((C + 31) / 32), dim3(1024), 0, st, 1, pdl_enabled(), part, out,
+  return launch_ex(k_part_sum, dim3((C + 7) / 8), dim3(512), 0, st, 1, pdl_enabled(), part, out,
                    parts, C, accumulate);
 }
 

@@ -304,42 +304,73 @@ __device__ __forceinline__ uint32_t ckpt_code4_in_range(float2 ab, float2 cd, fl
   return __byte_perm(lo, hi, 0x5410);
 }
 
-// codes of four values for any scale code
-__device__ __forceinline__ uint32_t ckpt_code4_any(float2 ab, float2 cd, uint32_t code, float inv) {
-  return code == 248u ? ckpt_code4(ab.x, ab.y, cd.x, cd.y, inv) : ckpt_code4_in_range(ab, cd, inv);
+// the codes of eight values
+__device__ __forceinline__ uint2 ckpt_code8(const float2* v, uint32_t code) {
+  const float inv = ckpt_inv_scale(code);
+  if (code == 248u)  // the upper clamp of the scale: a value may be up to 128 steps
+    return make_uint2(ckpt_code4(v[0].x, v[0].y, v[1].x, v[1].y, inv), ckpt_code4(v[2].x, v[2].y, v[3].x, v[3].y, inv));
+  return make_uint2(ckpt_code4_in_range(v[0], v[1], inv), ckpt_code4_in_range(v[2], v[3], inv));
 }
 
-// the values of four codes, in pairs (2^23 + 128 + q, less 2^23 + 128, times the
-// scale: folding the last two into one would overflow at the largest scales)
-__device__ __forceinline__ void ckpt_pairs4(uint32_t w, float scale, float2* v) {
-  const uint32_t x = w ^ 0x80808080u;
-  const float2 s = both(scale), o = both(-8388736.f);
-  v[0] = mul2(add2(make_float2(__uint_as_float(__byte_perm(x, 0x4b000000u, 0x7440)),
-                               __uint_as_float(__byte_perm(x, 0x4b000000u, 0x7441))), o), s);
-  v[1] = mul2(add2(make_float2(__uint_as_float(__byte_perm(x, 0x4b000000u, 0x7442)),
-                               __uint_as_float(__byte_perm(x, 0x4b000000u, 0x7443))), o), s);
+// eight codes as numbers, in pairs (2^23 + 128 + q, less 2^23 + 128)
+__device__ __forceinline__ void code_pairs(uint2 w, float2* v) {
+  const uint32_t x[2] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u};
+  const float2 o = both(-8388736.f);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    v[2 * i] = add2(make_float2(__uint_as_float(__byte_perm(x[i], 0x4b000000u, 0x7440)),
+                                __uint_as_float(__byte_perm(x[i], 0x4b000000u, 0x7441))), o);
+    v[2 * i + 1] = add2(make_float2(__uint_as_float(__byte_perm(x[i], 0x4b000000u, 0x7442)),
+                                    __uint_as_float(__byte_perm(x[i], 0x4b000000u, 0x7443))), o);
+  }
 }
 
-// eight elements as four pairs: load_part and store_part's forms
-template <typename T>
-__device__ __forceinline__ void load_pairs(const T* p, int n, bool vec, float2* v) {
+// the values of eight codes (folding the offset and the scale into one operation
+// would overflow at the largest scales)
+__device__ __forceinline__ void ckpt_pairs8(uint2 w, float scale, float2* v) {
+  code_pairs(w, v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], both(scale));
+}
+
+// Eight elements as four pairs, n of which exist.  VEC: the address is aligned
+// and rows are whole vectors, so it is all eight or none; otherwise any number.
+template <bool VEC, typename T>
+__device__ __forceinline__ void load_pairs(const T* p, int n, float2* v) {
   float t[8];
-  load_part<8>(p, n, vec, t);
+  if (VEC) {
+    if (n > 0) {
+      load_vec<8>(p, t);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[i] = 0.f;
+    }
+  } else {
+    load_part<8>(p, n, false, t);
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] = make_float2(t[2 * i], t[2 * i + 1]);
 }
-template <typename T>
-__device__ __forceinline__ void store_pairs(T* p, int n, bool vec, const float2* v) {
+template <bool VEC, typename T>
+__device__ __forceinline__ void store_pairs(T* p, int n, const float2* v) {
   const float t[8] = {v[0].x, v[0].y, v[1].x, v[1].y, v[2].x, v[2].y, v[3].x, v[3].y};
-  store_part<8>(p, n, vec, t);
+  if (VEC) {
+    if (n > 0) store_vec<8>(p, t);
+  } else {
+    store_part<8>(p, n, false, t);
+  }
+}
+
+// bits of the largest of eight magnitudes, NaN's if one is a NaN
+__device__ __forceinline__ uint32_t max_bits8(const float2* v) {
+  return __float_as_uint(max_abs3(max_abs3(v[0].x, v[0].y, max_abs3(v[1].x, v[1].y, v[2].x)), v[2].y,
+                                  max_abs3(v[3].x, v[3].y, 0.f)));
 }
 
 // the checkpoint of a group held by a half warp, eight channels a lane in pairs:
-// its scale code, for ckpt_code4_any
+// its scale code, for ckpt_code8
 __device__ __forceinline__ uint32_t group_code(const float2* v) {
-  const float m = max_abs3(max_abs3(v[0].x, v[0].y, max_abs3(v[1].x, v[1].y, v[2].x)), v[2].y,
-                           max_abs3(v[3].x, v[3].y, 0.f));
-  return ckpt_scale_code(half_warp_max(__float_as_uint(m)));
+  return ckpt_scale_code(half_warp_max(max_bits8(v)));
 }
 
 }  // namespace instant

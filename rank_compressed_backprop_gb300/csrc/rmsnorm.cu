@@ -11,14 +11,12 @@
 // takes several rows at a time when rows are short.  Sixteen neighbouring lanes
 // hold one checkpoint group.
 //
-// Two forms.  The direct one starts a CTA for a handful of rows and loads them
-// into registers.  The streaming one keeps two CTAs on each SM; a thread of each
+// The forward, and the backward of few or unaligned rows, start a CTA for a
+// handful of rows.  The streaming backward keeps CTAs on the SMs; a thread of each
 // copies blocks of whole rows (they are contiguous) into a ring in shared memory
-// with bulk copies, so that an SM always has 100 KB and more under way whatever
-// its warps wait for, and the backward's share of ggamma stays in registers over
-// all rows of a CTA.  Which one runs, with both measured: see stream_plan.
+// with bulk copies, so that an SM has up to 200 KB under way whatever its warps
+// wait for, and the share of ggamma stays in registers over all rows of a CTA.
 #include <algorithm>
-#include <cstdlib>
 
 #include "ckpt.cuh"
 
@@ -45,7 +43,7 @@ __device__ __forceinline__ float row_sum(float v, float* red, int warp) {
 
 // a row's outputs from its unnormalised values (all threads of the row; h is
 // spent); gamma(v, g) gives the thread's vector v of gamma
-template <typename T, int W, int V, typename Gamma>
+template <typename T, int W, int V, bool VEC, typename Gamma>
 __device__ __forceinline__ void norm_outputs(const NormArgs& a, float2 (&h)[V][4], float r, int row, int t,
                                              Gamma gamma) {
   const size_t base = static_cast<size_t>(row) * a.C;
@@ -54,15 +52,14 @@ __device__ __forceinline__ void norm_outputs(const NormArgs& a, float2 (&h)[V][4
   for (int v = 0; v < V; ++v) {
     const int c = 8 * (v * 32 * W + t);
     const int n = a.C - c;
-    if (a.h) store_pairs(static_cast<T*>(a.h) + base + c, n, a.vec, h[v]);
+    if (a.h) store_pairs<VEC>(static_cast<T*>(a.h) + base + c, n, h[v]);
 #pragma unroll
     for (int e = 0; e < 4; ++e) h[v][e] = mul2(h[v][e], both(r));
     if (a.k.q) {
       const uint32_t code = group_code(h[v]);
-      const float inv = ckpt_inv_scale(code);
+      const uint2 w = ckpt_code8(h[v], code);
       if (n > 0) {
-        *reinterpret_cast<uint2*>(a.k.q + static_cast<size_t>(row) * a.ld + c) =
-            make_uint2(ckpt_code4_any(h[v][0], h[v][1], code, inv), ckpt_code4_any(h[v][2], h[v][3], code, inv));
+        *reinterpret_cast<uint2*>(a.k.q + static_cast<size_t>(row) * a.ld + c) = w;
         if ((threadIdx.x & 15) == 0)
           a.k.s[static_cast<size_t>(c / kCkptGroup) * a.rows + row] = static_cast<uint8_t>(code);
       }
@@ -72,7 +69,7 @@ __device__ __forceinline__ void norm_outputs(const NormArgs& a, float2 (&h)[V][4
       gamma(v, g);
 #pragma unroll
       for (int e = 0; e < 4; ++e) g[e] = mul2(g[e], h[v][e]);
-      store_pairs(static_cast<T*>(a.y) + base + c, n, a.vec, g);
+      store_pairs<VEC>(static_cast<T*>(a.y) + base + c, n, g);
     }
   }
 }
@@ -83,7 +80,7 @@ __device__ __forceinline__ void add_squares(const float2* h, float2& ss) {
   for (int e = 0; e < 4; ++e) ss = fma2(h[e], h[e], ss);
 }
 
-template <typename T, int W, int V>
+template <typename T, int W, int V, bool VEC>
 __global__ void __launch_bounds__(W > 8 ? 32 * W : 256)
     k_rms_norm(NormArgs a) {
   constexpr int kWarps = W > 8 ? W : 8;
@@ -103,10 +100,10 @@ __global__ void __launch_bounds__(W > 8 ? 32 * W : 256)
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int c = 8 * (v * 32 * W + t);
-    load_pairs(x + c, on ? a.C - c : 0, a.vec, h[v]);
+    load_pairs<VEC>(x + c, on ? a.C - c : 0, h[v]);
     if (res) {
       float2 o[4];
-      load_pairs(res + c, on ? a.C - c : 0, a.vec, o);
+      load_pairs<VEC>(res + c, on ? a.C - c : 0, o);
 #pragma unroll
       for (int e = 0; e < 4; ++e) h[v][e] = add2(h[v][e], o[e]);
     }
@@ -114,20 +111,20 @@ __global__ void __launch_bounds__(W > 8 ? 32 * W : 256)
   }
   const float r = rsqrtf(row_sum<W>(ss.x + ss.y, red, warp) / static_cast<float>(a.C) + a.eps);
   if (!on) return;  // a whole warp at a time
-  norm_outputs<T, W, V>(a, h, r, row, t, [&](int v, float2* g) {
+  norm_outputs<T, W, V, VEC>(a, h, r, row, t, [&](int v, float2* g) {
     const int c = 8 * (v * 32 * W + t);
-    load_pairs(static_cast<const T*>(a.gamma) + c, a.C - c, a.vec, g);
+    load_pairs<VEC>(static_cast<const T*>(a.gamma) + c, a.C - c, g);
   });
 }
 
 // one vector of the backward: u from its codes, the share of ggamma, d = gy gamma
 // (in place of gy) and the share of the row's dot product.  n channels exist; the
 // codes past them are not defined
+template <bool VEC>
 __device__ __forceinline__ void back_vector(uint2 w, float scale, int n, const float2* gamma, float2* d,
                                             float2* u, float2* acc, float2& dot) {
-  ckpt_pairs4(w.x, scale, u);
-  ckpt_pairs4(w.y, scale, u + 2);
-  if (n < 8) {
+  ckpt_pairs8(w, scale, u);
+  if (!VEC && n < 8) {
     float* f = reinterpret_cast<float*>(u);
 #pragma unroll
     for (int e = 0; e < 8; ++e)
@@ -150,7 +147,7 @@ __device__ __forceinline__ void back_result(float r, float c, const float2* u, f
 // Rows go round the CTAs; a thread keeps its columns' share of ggamma in
 // registers over all its rows, the CTA's row slots add theirs in shared memory
 // at the end, and a second kernel adds the CTAs' shares in a fixed order.
-template <typename T, int W, int V>
+template <typename T, int W, int V, bool VEC>
 __global__ void __launch_bounds__(W > 8 ? 32 * W : 256)
     k_rms_norm_back(NormBackArgs a) {
   constexpr int kWarps = W > 8 ? W : 8;
@@ -181,15 +178,15 @@ __global__ void __launch_bounds__(W > 8 ? 32 * W : 256)
       const int c = 8 * (v * 32 * W + t);
       const int n = on ? a.C - c : 0;
       float2 gm[4];
-      load_pairs(static_cast<const T*>(a.gy) + base + c, n, a.vec, d[v]);
-      load_pairs(static_cast<const T*>(a.gamma) + c, n, a.vec, gm);
+      load_pairs<VEC>(static_cast<const T*>(a.gy) + base + c, n, d[v]);
+      load_pairs<VEC>(static_cast<const T*>(a.gamma) + c, n, gm);
       uint2 w = make_uint2(0u, 0u);
       float scale = 0.f;
       if (n > 0) {
         w = *reinterpret_cast<const uint2*>(a.k.q + static_cast<size_t>(row) * a.ld + c);
         scale = ckpt_scale(a.k.s[static_cast<size_t>(c / kCkptGroup) * a.rows + row]);
       }
-      back_vector(w, scale, n, gm, d[v], u[v], acc[v], dot);
+      back_vector<VEC>(w, scale, n, gm, d[v], u[v], acc[v], dot);
     }
     const float c1 = row_sum<W>(dot.x + dot.y, red[it & 1], warp) * inv_c;
 #pragma unroll
@@ -199,11 +196,11 @@ __global__ void __launch_bounds__(W > 8 ? 32 * W : 256)
       back_result(r, c1, u[v], d[v]);
       if (a.res) {
         float2 o[4];
-        load_pairs(static_cast<const T*>(a.res) + base + c, n, a.vec, o);
+        load_pairs<VEC>(static_cast<const T*>(a.res) + base + c, n, o);
 #pragma unroll
         for (int e = 0; e < 4; ++e) d[v][e] = add2(d[v][e], o[e]);
       }
-      store_pairs(static_cast<T*>(a.gx) + base + c, n, a.vec, d[v]);
+      store_pairs<VEC>(static_cast<T*>(a.gx) + base + c, n, d[v]);
     }
   }
   if (kRows > 1) {
@@ -227,7 +224,7 @@ __global__ void __launch_bounds__(W > 8 ? 32 * W : 256)
     for (int v = 0; v < V; ++v) {
       const int c = 8 * (v * 32 * W + t);
       float* p = a.part + static_cast<size_t>(blockIdx.x) * a.C + c;
-      store_pairs(p, a.C - c, a.C % 4 == 0, acc[v]);
+      store_pairs<VEC>(p, a.C - c, acc[v]);
     }
   }
 }
@@ -236,7 +233,9 @@ __global__ void __launch_bounds__(W > 8 ? 32 * W : 256)
 // them in its ring
 struct StreamPlan {
   int block, blocks, stages, grid;
-  uint32_t stage_bytes;
+  int per_cta, chunk;                   // blocks of a CTA, rows whose factors and scales it holds
+  uint32_t res_off, q_off;              // within a slot
+  uint32_t stage_bytes, gamma_off, r_off, s_off, bar_off;
   size_t smem;
 };
 
@@ -259,44 +258,37 @@ __device__ __forceinline__ float row_sum_stream(float v, float* red, int warp) {
   if (W == 1) return v;
   if ((threadIdx.x & 31) == 0) red[warp] = v;
   named_barrier<1>(THREADS);
-  float sum = 0.f;
-  const int first = warp / W * W;
+  const float* p = red + warp / W * W;
+  if (W == 2) return p[0] + p[1];
+  float4 sum = *reinterpret_cast<const float4*>(p);
 #pragma unroll
-  for (int i = 0; i < W; ++i) sum += red[first + i];
-  return sum;
+  for (int i = 4; i < W; i += 4) {
+    const float4 q = *reinterpret_cast<const float4*>(p + i);
+    sum.x += q.x; sum.y += q.y; sum.z += q.z; sum.w += q.w;
+  }
+  return (sum.x + sum.y) + (sum.z + sum.w);
 }
 
-// The ring of a streaming CTA: `stages` slots, each a block of `block` rows of up
-// to three tensors.  full: bytes of a slot's copies; empty: one arrival a warp.
-struct Ring {
-  uint8_t* base;
-  uint64_t *full, *empty;
-};
-
+// The copies of a CTA's blocks lo .. hi - 1 into the ring, one thread.  A slot
+// holds a block of rows: gy, residual, codes.
 template <typename T>
-__device__ __forceinline__ void produce(const StreamPlan& p, const Ring& g, const void* const (&src)[3],
-                                        const uint32_t (&row_bytes)[3], int rows) {
+__device__ __forceinline__ void produce(const NormBackArgs& a, const StreamPlan& p, uint8_t* ring,
+                                        uint64_t* full, uint64_t* empty, int lo, int hi) {
+  const uint32_t row_bytes = static_cast<uint32_t>(a.C * sizeof(T));
   int s = 0, par = 1, issued = 0;
-  for (int b = blockIdx.x; b < p.blocks; b += gridDim.x) {
-    if (!mbar_wait(&g.empty[s], par)) {
+  for (int b = lo; b < hi; ++b) {
+    if (!mbar_wait(&empty[s], par)) {
       raise_fault(FAULT_WAIT_EMPTY);
       break;
     }
     const int row0 = b * p.block;
-    const uint32_t n = static_cast<uint32_t>(min(p.block, rows - row0));
-    uint32_t bytes = 0;
-#pragma unroll
-    for (int i = 0; i < 3; ++i)
-      if (src[i]) bytes += n * row_bytes[i];
-    mbar_arrive_expect_tx(&g.full[s], bytes);
-    uint8_t* dst = g.base + static_cast<size_t>(s) * p.stage_bytes;
-#pragma unroll
-    for (int i = 0; i < 3; ++i)
-      if (src[i]) {
-        bulk_load(dst, static_cast<const uint8_t*>(src[i]) + static_cast<size_t>(row0) * row_bytes[i],
-                  n * row_bytes[i], &g.full[s]);
-        dst += p.block * row_bytes[i];
-      }
+    const int n = min(p.block, a.rows - row0);
+    uint8_t* dst = ring + static_cast<size_t>(s) * p.stage_bytes;
+    mbar_arrive_expect_tx(&full[s], n * (row_bytes * (a.res ? 2 : 1) + a.ld));
+    const size_t off = static_cast<size_t>(row0) * row_bytes;
+    bulk_load(dst, static_cast<const uint8_t*>(a.gy) + off, n * row_bytes, &full[s]);
+    if (a.res) bulk_load(dst + p.res_off, static_cast<const uint8_t*>(a.res) + off, n * row_bytes, &full[s]);
+    bulk_load(dst + p.q_off, a.k.q + static_cast<size_t>(row0) * a.ld, n * a.ld, &full[s]);
     if (issued < p.stages) ++issued;
     if (++s == p.stages) {
       s = 0;
@@ -310,218 +302,147 @@ __device__ __forceinline__ void produce(const StreamPlan& p, const Ring& g, cons
       s = p.stages - 1;
       par ^= 1;
     }
-    if (!mbar_wait(&g.full[s], par)) raise_fault(FAULT_WAIT_FULL);
+    if (!mbar_wait(&full[s], par)) raise_fault(FAULT_WAIT_FULL);
   }
 }
 
-template <int THREADS>
-__device__ __forceinline__ Ring ring_init(uint8_t* smem, const StreamPlan& p) {
-  Ring g;
-  g.base = smem;
-  g.full = reinterpret_cast<uint64_t*>(smem + static_cast<size_t>(p.stages) * p.stage_bytes);
-  g.empty = g.full + p.stages;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < p.stages; ++i) {
-      mbar_init(&g.full[i], 1);
-      mbar_init(&g.empty[i], THREADS / 32);
-    }
-    fence_barrier_init();
-  }
-  __syncthreads();
-  return g;
-}
-
-// One answer for all consumer threads, which meet at a barrier in every row.
-template <int THREADS>
-__device__ __forceinline__ bool wait_block(uint64_t* bar, uint32_t parity) {
-  const uint32_t mine = mbar_wait(bar, parity) ? 1u : 0u;
-  uint32_t all;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.and.pred q, 2, %2, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(all)
-      : "r"(mine), "n"(THREADS)
-      : "memory");
-  return all != 0;
-}
-
-template <typename T, int W, int V>
-__global__ void __launch_bounds__((W > 8 ? 32 * W : 256) + 32, W > 8 ? 1 : 2)
-    k_rms_norm_stream(NormArgs a, StreamPlan p) {
+// Streaming backward.  Only the shares of ggamma live in registers across a row:
+// u and d are made twice, before and after the row's sum, from what the ring holds,
+// so that the registers allow as many CTAs as the shared memory.  A CTA's rows are
+// neighbours: their factors and scale bytes are fetched for `chunk` rows at once (a
+// plain load a row would wait behind the copies that are under way: 5 us).
+template <typename T, int W, int V, int CTAS>
+__global__ void __launch_bounds__((W > 8 ? 32 * W : 256) + 32, CTAS)
+    k_rms_norm_back_stream(NormBackArgs a, StreamPlan p) {
   constexpr int kWarps = W > 8 ? W : 8;
   constexpr int kSlots = kWarps / W;  // rows at a time
   constexpr int kCons = 32 * kWarps;  // consumer threads; one more warp produces
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float red[2][32];
-  const Ring g = ring_init<kCons>(smem, p);
+  __shared__ __align__(16) float red[2][32];
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.bar_off);
+  uint64_t* empty = full + p.stages;
+  T* gamma = reinterpret_cast<T*>(smem + p.gamma_off);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], kWarps);
+    }
+    fence_barrier_init();
+  }
   pdl_launch_dependents();
   pdl_wait();
+  for (int c = 8 * threadIdx.x; c < a.C; c += 8 * (kCons + 32)) {
+    float2 g[4];
+    load_pairs<true>(static_cast<const T*>(a.gamma) + c, 8, g);
+    store_pairs<true>(gamma + c, 8, g);
+  }
+  __syncthreads();
   const int warp = threadIdx.x >> 5;
+  const int lo = min(p.blocks, static_cast<int>(blockIdx.x) * p.per_cta);
+  const int hi = min(p.blocks, lo + p.per_cta);
   if (warp == kWarps) {
-    if ((threadIdx.x & 31) == 0) {
-      const void* const src[3] = {a.x, a.res, nullptr};
-      const uint32_t bytes = static_cast<uint32_t>(a.C * sizeof(T));
-      const uint32_t row_bytes[3] = {bytes, bytes, 0};
-      produce<T>(p, g, src, row_bytes, a.rows);
-    }
+    if ((threadIdx.x & 31) == 0) produce<T>(a, p, smem, full, empty, lo, hi);
     return;
   }
   const int t = threadIdx.x % (32 * W);  // thread within its row
   const int slot = warp / W;
-  const int res_off = p.block * a.C;     // elements from a block's x to its residual
-  float2 gm[V][4];                       // this thread's columns of gamma
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int c = 8 * (v * 32 * W + t);
-    load_pairs(static_cast<const T*>(a.gamma) + c, a.C - c, a.vec, gm[v]);
-  }
-  int s = 0, par = 0, it = 0;
-  for (int b = blockIdx.x; b < p.blocks; b += gridDim.x) {
-    if (!wait_block<kCons>(&g.full[s], par)) {
-      raise_fault(FAULT_WAIT_FULL);
-      return;
-    }
-    const T* sx = reinterpret_cast<const T*>(g.base + static_cast<size_t>(s) * p.stage_bytes);
-    const int row0 = b * p.block;
-    const int n_rows = min(p.block, a.rows - row0);
-    for (int i0 = 0; i0 < n_rows; i0 += kSlots, ++it) {
-      const int i = i0 + slot;
-      const bool on = i < n_rows;
-      const T* xr = sx + (on ? i : 0) * a.C;
-      float2 h[V][4];
-      float2 ss = both(0.f);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int c = 8 * (v * 32 * W + t);
-        const int n = on ? a.C - c : 0;
-        load_pairs(xr + c, n, true, h[v]);
-        if (a.res) {
-          float2 o[4];
-          load_pairs(xr + res_off + c, n, true, o);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) h[v][e] = add2(h[v][e], o[e]);
-        }
-        add_squares(h[v], ss);
-      }
-      if (i0 + kSlots >= n_rows) {  // the block is in registers: its slot may be refilled
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0) mbar_arrive(&g.empty[s]);
-      }
-      const float r =
-          rsqrtf(row_sum_stream<W, kCons>(ss.x + ss.y, red[it & 1], warp) / static_cast<float>(a.C) + a.eps);
-      if (on)
-        norm_outputs<T, W, V>(a, h, r, row0 + i, t, [&](int v, float2* g) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) g[e] = gm[v][e];
-        });
-    }
-    if (++s == p.stages) {
-      s = 0;
-      par ^= 1;
-    }
-  }
-}
-
-template <typename T, int W, int V>
-__global__ void __launch_bounds__((W > 8 ? 32 * W : 256) + 32, W > 8 ? 1 : 2)
-    k_rms_norm_back_stream(NormBackArgs a, StreamPlan p) {
-  constexpr int kWarps = W > 8 ? W : 8;
-  constexpr int kSlots = kWarps / W;
-  constexpr int kCons = 32 * kWarps;
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float red[2][32];
-  const Ring g = ring_init<kCons>(smem, p);
-  pdl_launch_dependents();
-  pdl_wait();
-  const int warp = threadIdx.x >> 5;
-  if (warp == kWarps) {
-    if ((threadIdx.x & 31) == 0) {
-      const void* const src[3] = {a.gy, a.k.q, a.res};
-      const uint32_t bytes = static_cast<uint32_t>(a.C * sizeof(T));
-      const uint32_t row_bytes[3] = {bytes, static_cast<uint32_t>(a.ld), bytes};
-      produce<T>(p, g, src, row_bytes, a.rows);
-    }
-    return;
-  }
-  const int t = threadIdx.x % (32 * W);
-  const int slot = warp / W;
   const float inv_c = 1.f / static_cast<float>(a.C);
-  float2 acc[V][4], gm[V][4];
+  float2 acc[V][4];
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int c = 8 * (v * 32 * W + t);
-    load_pairs(static_cast<const T*>(a.gamma) + c, a.C - c, a.vec, gm[v]);
+  for (int v = 0; v < V; ++v)
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[v][e] = both(0.f);
-  }
-  // factor and scale bytes of the next row of this thread, asked for a row early:
-  // they lie a row apart in memory, and nothing else waits for a plain load here
-  float r_next = 0.f;
-  uint32_t s_next[V];
-  auto ask = [&](int row) {
-    const bool in = row < a.rows;
-    r_next = in ? a.r[row] : 0.f;
+  int col[V];  // this thread's columns, and whether they exist
+  bool in[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = 8 * (v * 32 * W + t);
-      s_next[v] = in && c < a.C ? a.k.s[static_cast<size_t>(c / kCkptGroup) * a.rows + row] : 0u;
-    }
-  };
-  ask(blockIdx.x * p.block + slot);
+  for (int v = 0; v < V; ++v) {
+    const int c = 8 * (v * 32 * W + t);
+    in[v] = c < a.C;
+    col[v] = in[v] ? c : 0;
+  }
   int s = 0, par = 0, it = 0;
-  bool ok = true;
-  for (int b = blockIdx.x; b < p.blocks; b += gridDim.x) {
-    ok = wait_block<kCons>(&g.full[s], par);
-    if (!ok) {
-      raise_fault(FAULT_WAIT_FULL);
-      break;
+  bool ok = true;  // after a wait that ran out no more are made: the loops stay in step
+  float* sr = reinterpret_cast<float*>(smem + p.r_off);  // factors of the chunk's rows
+  uint8_t* ssc = smem + p.s_off;                         // scale bytes, [group][chunk]
+  const int groups = (a.C + kCkptGroup - 1) / kCkptGroup;
+  int chunk0 = lo * p.block;                             // first row of the chunk
+  for (int b = lo; b < hi; ++b) {
+    if (b == lo || b * p.block - chunk0 >= p.chunk) {
+      if (b != lo) named_barrier<1>(kCons);
+      chunk0 = b * p.block;
+      const int n = min(p.chunk, min(a.rows, hi * p.block) - chunk0);
+      for (int i = threadIdx.x; i < n; i += kCons) sr[i] = a.r[chunk0 + i];
+      for (int g = warp; g < groups; g += kWarps)
+        for (int i = threadIdx.x & 31; i < n; i += 32)
+          ssc[g * p.chunk + i] = a.k.s[static_cast<size_t>(g) * a.rows + chunk0 + i];
+      named_barrier<1>(kCons);
     }
-    const uint8_t* base = g.base + static_cast<size_t>(s) * p.stage_bytes;
+    if (ok && !mbar_wait(&full[s], par)) {
+      raise_fault(FAULT_WAIT_FULL);
+      ok = false;
+    }
+    const uint8_t* base = smem + static_cast<size_t>(s) * p.stage_bytes;
     const T* sgy = reinterpret_cast<const T*>(base);
-    const int8_t* sq = reinterpret_cast<const int8_t*>(base + static_cast<size_t>(p.block) * a.C * sizeof(T));
-    const T* sres = reinterpret_cast<const T*>(sq + static_cast<size_t>(p.block) * a.ld);
+    const T* sres = reinterpret_cast<const T*>(base + p.res_off);
+    const int8_t* sq = reinterpret_cast<const int8_t*>(base + p.q_off);
     const int row0 = b * p.block;
+    const int in_chunk = row0 - chunk0;
     const int n_rows = min(p.block, a.rows - row0);
     for (int i0 = 0; i0 < n_rows; i0 += kSlots, ++it) {
       const int i = i0 + slot;
-      const bool on = i < n_rows;
-      const float r = r_next;
-      float scale[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) scale[v] = ckpt_scale(s_next[v]);
-      // the row after this one: in this block, or the first of the CTA's next
-      ask(i0 + kSlots < n_rows ? row0 + i + kSlots : row0 + static_cast<int>(gridDim.x) * p.block + slot);
-      float2 u[V][4], d[V][4];
+      const bool on = i < n_rows;  // the same for all warps of a row
+      const T* gyr = sgy + i * a.C;
+      const int8_t* qr = sq + i * a.ld;
+      // a vector past the row's end repeats its first one with a scale of zero
+      // (columns that are never written, terms of zero in the row's sum)
       float2 dot = both(0.f);
+      if (on) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int c = 8 * (v * 32 * W + t);
-        const int n = on ? a.C - c : 0;
-        load_pairs(sgy + (on ? i : 0) * a.C + c, n, true, d[v]);
-        uint2 w = make_uint2(0u, 0u);
-        if (n > 0) w = *reinterpret_cast<const uint2*>(sq + static_cast<size_t>(i) * a.ld + c);
-        else scale[v] = 0.f;
-        back_vector(w, scale[v], n, gm[v], d[v], u[v], acc[v], dot);
-      }
-      const float c1 = row_sum_stream<W, kCons>(dot.x + dot.y, red[it & 1], warp) * inv_c;
+        for (int v = 0; v < V; ++v) {
+          const float scale = in[v] ? ckpt_scale(ssc[(col[v] / kCkptGroup) * p.chunk + in_chunk + i]) : 0.f;
+          float2 gy[4], q[4], gm[4];
+          load_pairs<true>(gyr + col[v], 8, gy);
+          code_pairs(*reinterpret_cast<const uint2*>(qr + col[v]), q);
+          load_pairs<true>(gamma + col[v], 8, gm);
+          float2 part = both(0.f);
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int c = 8 * (v * 32 * W + t);
-        const int n = on ? a.C - c : 0;
-        back_result(r, c1, u[v], d[v]);
-        if (a.res) {
-          float2 o[4];
-          load_pairs(sres + (on ? i : 0) * a.C + c, n, true, o);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) d[v][e] = add2(d[v][e], o[e]);
+          for (int e = 0; e < 4; ++e) {
+            const float2 x = mul2(gy[e], q[e]);
+            acc[v][e] = fma2(x, both(scale), acc[v][e]);
+            part = fma2(x, gm[e], part);
+          }
+          dot = fma2(part, both(scale), dot);
         }
-        store_pairs(static_cast<T*>(a.gx) + static_cast<size_t>(row0 + (on ? i : 0)) * a.C + c, n, true, d[v]);
+      }
+      const float c1 = row_sum_stream<W, kCons>(dot.x + dot.y, red[it & 1], warp) * -inv_c;
+      if (on) {
+        const float r = sr[in_chunk + i];
+        const T* resr = sres + i * a.C;
+        T* gxr = static_cast<T*>(a.gx) + static_cast<size_t>(row0 + i) * a.C;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          // r (gy gamma - u c) + residual
+          const float uc = (in[v] ? ckpt_scale(ssc[(col[v] / kCkptGroup) * p.chunk + in_chunk + i]) : 0.f) * c1;
+          float2 d[4], q[4], gm[4];
+          load_pairs<true>(gyr + col[v], 8, d);
+          code_pairs(*reinterpret_cast<const uint2*>(qr + col[v]), q);
+          load_pairs<true>(gamma + col[v], 8, gm);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) d[e] = fma2(q[e], both(uc), mul2(d[e], gm[e]));
+          if (a.res) {
+            load_pairs<true>(resr + col[v], 8, gm);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) d[e] = fma2(d[e], both(r), gm[e]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) d[e] = mul2(d[e], both(r));
+          }
+          store_pairs<true>(gxr + col[v], in[v] ? 8 : 0, d);
+        }
       }
     }
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(&g.empty[s]);
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[s]);
     if (++s == p.stages) {
       s = 0;
       par ^= 1;
@@ -546,8 +467,9 @@ __global__ void __launch_bounds__((W > 8 ? 32 * W : 256) + 32, W > 8 ? 1 : 2)
   for (int c = threadIdx.x; c < a.C; c += kCons) a.part[static_cast<size_t>(blockIdx.x) * a.C + c] = gsum[c];
 }
 
-// warps a row and vectors a thread: the fewest threads that hold the row in two
-// vectors each, and four vectors only for rows beyond 32 x 32 x 16 channels
+// direct forms, warps a row and vectors a thread: two vectors a thread up to 16
+// warps, then more vectors (1024 x 2 at 11008 channels took 181 us over 8191 rows,
+// 512 x 3 139)
 #define INSTANT_NORM_DISPATCH(C, GO)                     \
   do {                                                   \
     if ((C) <= 256) GO(1, 1);                            \
@@ -556,66 +478,72 @@ __global__ void __launch_bounds__((W > 8 ? 32 * W : 256) + 32, W > 8 ? 1 : 2)
     if ((C) <= 2048) GO(4, 2);                           \
     if ((C) <= 4096) GO(8, 2);                           \
     if ((C) <= 8192) GO(16, 2);                          \
-    if ((C) <= 16384) GO(32, 2);                         \
+    if ((C) <= 12288) GO(16, 3);                         \
+    if ((C) <= 16384) GO(16, 4);                         \
     GO(32, 4);                                           \
   } while (0)
 
-// the same with the widest rows in three or four vectors of 16 warps
+// streaming backward: warps a row, vectors a thread, CTAs an SM
 #define INSTANT_STREAM_DISPATCH(C, GO)                   \
   do {                                                   \
-    if ((C) <= 256) GO(1, 1);                            \
-    if ((C) <= 512) GO(1, 2);                            \
-    if ((C) <= 1024) GO(2, 2);                           \
-    if ((C) <= 2048) GO(4, 2);                           \
-    if ((C) <= 4096) GO(8, 2);                           \
-    if ((C) <= 8192) GO(16, 2);                          \
-    if ((C) <= 12288) GO(16, 3);                         \
-    GO(16, 4);                                           \
+    if ((C) <= 256) GO(1, 1, 3);                         \
+    if ((C) <= 512) GO(1, 2, 3);                         \
+    if ((C) <= 1024) GO(2, 2, 3);                        \
+    if ((C) <= 2048) GO(4, 2, 3);                        \
+    if ((C) <= 4096) GO(8, 2, 3);                        \
+    if ((C) <= 8192) GO(8, 4, 2);                        \
+    GO(16, 3, 1);                                        \
   } while (0)
 
-// Streaming plan of `rows` rows that bring row_bytes each, W warps a row; false
-// where the direct form runs: rows whose copies are not multiples of 16 bytes or
-// do not fit a ring of two.  A slot holds about 16 KB, a CTA about 100 KB (two an
-// SM; one of 16 warps with 200 KB).
-bool stream_plan(StreamPlan& p, int rows, int C, size_t row_bytes, bool vec) {
-  if (!vec || C > 16384) return false;
-  if (const char* v = getenv("STREAM")) { if (atoi(v) == 0) return false; }
-  int w = 1;
-  while (w < 16 && 512 * w < C) w *= 2;
+// Streaming plan; false where the direct form runs: rows too wide for a ring of
+// two, or fewer than two blocks a CTA, where its start costs more than its ring
+// gives (us, streaming / direct, bf16: 8192 x 4096 48.7 / 95.5, 8191 x 11008
+// 116 / 267, 512 x 11008 21 / 29, 16384 x 768 30 / 44; 300 x 8192 14.6 / 12.4,
+// 8192 x 64 8.7 / 8.1).  A slot holds about 16 KB, the CTAs of an SM about 220 KB.
+bool stream_plan(StreamPlan& p, const NormBackArgs& a, size_t elem, int w, int v, int ctas) {
   const int slots = w > 8 ? 1 : 8 / w;
-  const size_t pass = slots * row_bytes;
-  const size_t passes = pass >= 16384 ? 1 : std::min<size_t>(16, 16384 / pass);
+  const int groups = (a.C + kCkptGroup - 1) / kCkptGroup;
+  const size_t row = elem * a.C;
+  const size_t pass = slots * (row * (a.res ? 2 : 1) + a.ld);
+  const size_t passes = pass >= 16384 ? 1 : std::min<size_t>(8, 16384 / pass);
   p.block = static_cast<int>(slots * passes);
-  p.blocks = (rows + p.block - 1) / p.block;
-  p.stage_bytes = static_cast<uint32_t>((passes * pass + 127) / 128 * 128);
-  p.stages = static_cast<int>(std::min<size_t>(8, (w > 8 ? 200 * 1024 : 100 * 1024) / p.stage_bytes));
-  if (p.stages < 2) return false;
-  const int sms = std::min(sm_count(), kColSumSMs);
-  p.grid = std::min(p.blocks, w > 8 ? sms : 2 * sms);
-  // the ring is also the place of a CTA's column sums (the backward)
-  p.smem = std::max<size_t>(static_cast<size_t>(p.stages) * p.stage_bytes, sizeof(float) * 512 * 2 * w * 2) +
-           16 * p.stages;
-  return true;
+  p.blocks = (a.rows + p.block - 1) / p.block;
+  const int full = ctas * std::min(sm_count(), kColSumSMs);
+  if (p.blocks < 2 * full) return false;
+  p.grid = std::min(full, norm_back_parts(a.rows, a.C));  // the workspace's shares
+  p.per_cta = (p.blocks + p.grid - 1) / p.grid;
+  p.grid = (p.blocks + p.per_cta - 1) / p.per_cta;
+  // about 4 KB of factors and scales
+  p.chunk = std::min(p.per_cta, std::max(1, 4096 / (groups + 4) / p.block)) * p.block;
+  size_t at = p.block * row;
+  p.res_off = static_cast<uint32_t>(at);
+  if (a.res) at += p.block * row;
+  p.q_off = static_cast<uint32_t>(at);
+  at += static_cast<size_t>(p.block) * a.ld;
+  const size_t stage = (at + 127) / 128 * 128;
+  const size_t gamma = (row + 127) / 128 * 128;
+  const size_t rest = gamma + (static_cast<size_t>(p.chunk) * (4 + groups) + 127) / 128 * 128 + 256;
+  const size_t room = 220 * 1024 / ctas - 1024;
+  if (rest + 2 * stage > room) return false;
+  p.stage_bytes = static_cast<uint32_t>(stage);
+  p.stages = static_cast<int>(std::min<size_t>(8, (room - rest) / stage));
+  // the ring is also the place of a CTA's column sums
+  const size_t ring = std::max<size_t>(p.stages * stage, sizeof(float) * 256 * w * v);
+  p.gamma_off = static_cast<uint32_t>(ring);
+  p.r_off = static_cast<uint32_t>(ring + gamma);
+  p.s_off = static_cast<uint32_t>(p.r_off + 4 * p.chunk);
+  p.bar_off = static_cast<uint32_t>(ring + rest - 256);
+  p.smem = ring + rest;
+  return p.smem <= room;
 }
 
-template <typename T, int W, int V>
-cudaError_t norm_stream_go(const NormArgs& a, const StreamPlan& p, cudaStream_t st) {
-  auto k = k_rms_norm_stream<T, W, V>;
-  const cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(k), p.smem, true);
-  if (e != cudaSuccess) return e;
-  return launch_ex(k, dim3(p.grid), dim3((W > 8 ? 32 * W : 256) + 32), p.smem, st, 1, pdl_enabled(), a, p);
-}
-
-template <typename T>
-cudaError_t norm_stream_dispatch(const NormArgs& a, const StreamPlan& p, cudaStream_t st) {
-#define GO(W, V) return norm_stream_go<T, W, V>(a, p, st)
-  INSTANT_STREAM_DISPATCH(a.C, GO);
-#undef GO
-}
-
-template <typename T, int W, int V>
-cudaError_t back_stream_go(const NormBackArgs& a, const StreamPlan& p, cudaStream_t st) {
-  auto k = k_rms_norm_back_stream<T, W, V>;
+template <typename T, int W, int V, int CTAS>
+cudaError_t back_stream_go(const NormBackArgs& a, bool* done, cudaStream_t st) {
+  StreamPlan p;
+  *done = false;
+  for (int ctas = CTAS; ctas >= 1 && !*done; --ctas)  // fewer CTAs have wider rings *done = stream_plan(p, a, sizeof(T), W, V, ctas);
+  if (!*done) return cudaSuccess;
+  auto k = k_rms_norm_back_stream<T, W, V, CTAS>;
   cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(k), p.smem, true);
   if (e == cudaSuccess)
     e = launch_ex(k, dim3(p.grid), dim3((W > 8 ? 32 * W : 256) + 32), p.smem, st, 1, pdl_enabled(), a, p);
@@ -624,42 +552,42 @@ cudaError_t back_stream_go(const NormBackArgs& a, const StreamPlan& p, cudaStrea
 }
 
 template <typename T>
-cudaError_t back_stream_dispatch(const NormBackArgs& a, const StreamPlan& p, cudaStream_t st) {
-#define GO(W, V) return back_stream_go<T, W, V>(a, p, st)
+cudaError_t back_stream_dispatch(const NormBackArgs& a, bool* done, cudaStream_t st) {
+#define GO(W, V, CTAS) return back_stream_go<T, W, V, CTAS>(a, done, st)
   INSTANT_STREAM_DISPATCH(a.C, GO);
 #undef GO
 }
 
-template <typename T, int W, int V>
+template <typename T, bool VEC, int W, int V>
 cudaError_t norm_go(const NormArgs& a, cudaStream_t st) {
   constexpr int kWarps = W > 8 ? W : 8;
   constexpr int kRows = kWarps / W;
-  return launch_ex(k_rms_norm<T, W, V>, dim3((a.rows + kRows - 1) / kRows), dim3(32 * kWarps), 0, st, 1,
+  return launch_ex(k_rms_norm<T, W, V, VEC>, dim3((a.rows + kRows - 1) / kRows), dim3(32 * kWarps), 0, st, 1,
                    pdl_enabled(), a);
 }
 
-template <typename T>
+template <typename T, bool VEC>
 cudaError_t norm_dispatch(const NormArgs& a, cudaStream_t st) {
-#define GO(W, V) return norm_go<T, W, V>(a, st)
+#define GO(W, V) return norm_go<T, VEC, W, V>(a, st)
   INSTANT_NORM_DISPATCH(a.C, GO);
 #undef GO
 }
 
-template <typename T, int W, int V>
+template <typename T, bool VEC, int W, int V>
 cudaError_t back_go(const NormBackArgs& a, cudaStream_t st) {
   constexpr int kWarps = W > 8 ? W : 8;
   constexpr int kRows = kWarps / W;
   const size_t smem = kRows > 1 ? sizeof(float) * 8 * 32 * W * V : 0;
   const cudaError_t e =
-      launch_ex(k_rms_norm_back<T, W, V>, dim3(norm_back_parts(a.rows, a.C)), dim3(32 * kWarps), smem, st,
+      launch_ex(k_rms_norm_back<T, W, V, VEC>, dim3(norm_back_parts(a.rows, a.C)), dim3(32 * kWarps), smem, st,
                 1, pdl_enabled(), a);
   if (e != cudaSuccess) return e;
   return launch_part_sum(a.part, a.ggamma, norm_back_parts(a.rows, a.C), a.C, a.accumulate, st);
 }
 
-template <typename T>
+template <typename T, bool VEC>
 cudaError_t back_dispatch(const NormBackArgs& a, cudaStream_t st) {
-#define GO(W, V) return back_go<T, W, V>(a, st)
+#define GO(W, V) return back_go<T, VEC, W, V>(a, st)
   INSTANT_NORM_DISPATCH(a.C, GO);
 #undef GO
 }
@@ -667,30 +595,27 @@ cudaError_t back_dispatch(const NormBackArgs& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_rms_norm(const NormArgs& a, bool bf16, cudaStream_t st) {
-  const size_t row = static_cast<size_t>(a.C) * (bf16 ? 2 : 4);
-  StreamPlan p;
-  if (stream_plan(p, a.rows, a.C, a.res ? 2 * row : row, a.vec))
-    return bf16 ? norm_stream_dispatch<uint16_t>(a, p, st) : norm_stream_dispatch<float>(a, p, st);
-  return bf16 ? norm_dispatch<uint16_t>(a, st) : norm_dispatch<float>(a, st);
+  if (bf16) return norm_dispatch<uint16_t, true>(a, st);
+  return a.vec ? norm_dispatch<float, true>(a, st) : norm_dispatch<float, false>(a, st);
 }
 
-// CTAs of the backward, each with one share of ggamma: two to eight per SM
-// (about 2048 threads), no more than there are row slots
+// the most CTAs of the backward, each with one share of ggamma: four an SM, no
+// more than there are row slots of the form with the fewest
 int norm_back_parts(int rows, int C) {
-  int w = 1;
-  while (w < 32 && 512 * w < C) w *= 2;
-  const int slots = w > 8 ? 1 : 8 / w;
+  const int slots = C <= 512 ? 8 : C <= 1024 ? 4 : C <= 2048 ? 2 : 1;
   const long long ctas = (static_cast<long long>(rows) + slots - 1) / slots;
-  const long long most = static_cast<long long>(kColSumSMs) * (w > 8 ? 64 / w : 4);
+  const long long most = static_cast<long long>(kColSumSMs) * 4;
   return static_cast<int>(ctas < most ? ctas : most);
 }
 
 cudaError_t launch_rms_norm_back(const NormBackArgs& a, bool bf16, cudaStream_t st) {
-  const size_t row = static_cast<size_t>(a.C) * (bf16 ? 2 : 4);
-  StreamPlan p;
-  if (stream_plan(p, a.rows, a.C, (a.res ? 2 * row : row) + a.ld, a.vec))
-    return bf16 ? back_stream_dispatch<uint16_t>(a, p, st) : back_stream_dispatch<float>(a, p, st);
-  return bf16 ? back_dispatch<uint16_t>(a, st) : back_dispatch<float>(a, st);
+  if (a.vec && a.C <= 12288) {
+    bool done;
+    const cudaError_t e = bf16 ? back_stream_dispatch<uint16_t>(a, &done, st) : back_stream_dispatch<float>(a, &done, st);
+    if (done) return e;
+  }
+  if (bf16) return back_dispatch<uint16_t, true>(a, st);
+  return a.vec ? back_dispatch<float, true>(a, st) : back_dispatch<float, false>(a, st);
 }
 
 INSTANT_FAULT_READER(read_fault_norm)
