@@ -48,7 +48,7 @@ bool vec_ok(int C) { return C % 8 == 0; }
 // 1024 x 4096 -> 1024 14.7 / 25.1; weight gradient over 4096 rows, 1024 x 1024
 // 17.9 / 31.4, over 700 rows, 1792 x 448 11.4 / 10.5.
 cudaError_t launch_linear(const LinearArgs& a, bool bf16, cudaStream_t st) {
-  if (!bf16) return launch_linear_simt(a, false, st);
+  if (!bf16) return launch_linear_simt(a, st);
   const int nt = few_rows_tile(a);
   const double nk = cdiv(a.K, 64);
   const double waves = std::ceil(static_cast<double>(cdiv(a.M, 256)) * cdiv(a.N, 256) / std::max(1, sm_count() / 2));
@@ -164,7 +164,6 @@ instant_status instant_linear_act(const void* x, const void* w, const void* bias
   a.yk = ref(yq, ys);
   a.ld = ckpt_ld(Cy);
   a.act = act;
-  a.vec = vec_ok(Cy);
   return from_cuda(launch_linear(a, dt == INSTANT_BF16, static_cast<cudaStream_t>(stream)));
 }
 
@@ -190,7 +189,6 @@ instant_status instant_linear_act_grad(const void* gy, const void* w, const void
   a.ck = ref(zq, zs);
   a.ld = ckpt_ld(Cx);
   a.act = act;
-  a.vec = vec_ok(Cx);
   return from_cuda(launch_linear(a, dt == INSTANT_BF16, static_cast<cudaStream_t>(stream)));
 }
 
@@ -228,7 +226,6 @@ instant_status instant_ckpt_grad_w(const void* gy, const void* q, const void* s,
   a.ck = ref(q, s);
   a.ld = ckpt_ld(Cx);
   a.accumulate = accumulate != 0;
-  a.vec = vec_ok(Cx);
   cudaError_t e = cudaSuccess;
   if (bf16) {
     // the values are exact in bf16 and every row tile of gw reads them: made once

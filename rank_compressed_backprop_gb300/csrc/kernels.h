@@ -347,7 +347,6 @@ struct LinearArgs {
   int ld;              // code pitch of the checkpoints
   int act;             // instant_act
   int accumulate;      // kind 2
-  int vec;             // rows of N elements start on 16-byte boundaries
 };
 
 // shares of a column reduction are counted from the SMs of the one device this
@@ -365,7 +364,7 @@ cudaError_t launch_col_sum(const void* x, float* out, float* part, int rows, int
                            bool bf16, bool vec, cudaStream_t st);
 cudaError_t launch_rms_norm(const NormArgs& a, bool bf16, cudaStream_t st);
 cudaError_t launch_rms_norm_back(const NormBackArgs& a, bool bf16, cudaStream_t st);
-cudaError_t launch_linear_simt(const LinearArgs& a, bool bf16, cudaStream_t st);
+cudaError_t launch_linear_simt(const LinearArgs& a, cudaStream_t st);  // fp32
 
 // the same products on the tensor cores, bf16 (linear_tc.cu)
 struct TcArgs {

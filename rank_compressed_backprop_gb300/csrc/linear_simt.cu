@@ -3,219 +3,302 @@
 //   forward   z = x w^T + bias, y = act(z) + res, checkpoints of z and y
 //   back      gx = (gy w) * act'(z) + res, z from its checkpoint
 //   grad_w    gw (+)= (gy^T v) * col_scale, v the checkpoint's values
-// One kernel: a 64 x 128 output tile, 16-deep slices of both operands staged in
-// shared memory, 4 x 8 outputs a thread.  A tile is 128 columns wide so that the
-// 16 threads of a half warp hold whole checkpoint groups of their rows.
+// A warp owns R rows and 128 columns of the output, each lane the columns lane,
+// lane + 32, lane + 64 and lane + 96, so that it holds whole checkpoint groups of its
+// rows.  16-deep slices of both operands go through three stages of shared memory
+// by asynchronous copies: the operand of rows is read by broadcast (R values a
+// step), the one of columns without bank conflicts, and 4 R products a lane follow
+// from R + 4 values.  Few tiles leave too few warps on an SM to hide the latency of
+// a slice, so K is then split across the CTAs of a cluster: each leaves its partial
+// tile in shared memory, and a warp adds a row's partial sums in the order of the
+// ranks through distributed shared memory and carries the row through the epilogue.
+#include <algorithm>
+
 #include "ckpt.cuh"
 
 namespace instant {
 
 namespace {
 
-constexpr int BM = 64, BN = 128, BK = 16;
-constexpr int kThreads = 256;
+constexpr int BN = 128, BK = 16, NS = 3;
+constexpr int LDK = BK + 4;   // floats of a staged row of K: eight rows 16 bytes apart cover all banks
 enum { FORWARD = 0, BACK = 1, GRAD_W = 2 };
 
-// checkpoint of a row's 128 columns, eight in each lane of a half warp: four at
-// c0 and four at c1
-__device__ __forceinline__ void put_ckpt(const CkptRef& k, int ld, int rows, int row, bool on, int c0,
-                                         int c1, int C, const float* v) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if (c0 + e < C) m = max(m, abs_bits(v[e]));
-    if (c1 + e < C) m = max(m, abs_bits(v[4 + e]));
-  }
-  const uint32_t code = ckpt_scale_code(half_warp_max(m));
-  const float inv = ckpt_inv_scale(code);
-  if (!on) return;
-  int8_t* q = k.q + static_cast<size_t>(row) * ld;
-  if (c0 < C) *reinterpret_cast<uint32_t*>(q + c0) = ckpt_code4(v[0], v[1], v[2], v[3], inv);
-  if (c1 < C) *reinterpret_cast<uint32_t*>(q + c1) = ckpt_code4(v[4], v[5], v[6], v[7], inv);
-  if ((threadIdx.x & 15) == 0 && c0 < C)
-    k.s[static_cast<size_t>(c0 / kCkptGroup) * rows + row] = static_cast<uint8_t>(code);
+// 16 or 4 bytes global -> shared, asynchronous; zeros where `on` is false
+template <int BYTES>
+__device__ __forceinline__ void copy_async(float* dst, const float* src, bool on) {
+  const int n = on ? BYTES : 0;
+  if (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
 }
 
-template <typename T, int KIND>
-__global__ void __launch_bounds__(kThreads) k_linear_simt(LinearArgs a) {
-  __shared__ float As[BK][BM + 4];
-  __shared__ float Bs[BK][BN + 4];
+__device__ __forceinline__ float dsmem_ld(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// a block of `rows` x `cols` floats at (r0, c0) of a row-major [nr, nc] tensor into
+// shared memory with row pitch `ld`; zeros past the tensor's end
+template <int ROWS, int COLS, int THREADS, bool VEC>
+__device__ __forceinline__ void stage_block(float* dst, int ld, const float* src, int r0, int c0, int nr, int nc) {
+  constexpr int W = VEC ? 4 : 1;
+  for (int i = threadIdx.x; i < ROWS * COLS / W; i += THREADS) {
+    const int r = i / (COLS / W), c = W * (i % (COLS / W));
+    const bool on = r0 + r < nr && c0 + c < nc;
+    const float* p = on ? src + static_cast<size_t>(r0 + r) * nc + c0 + c : src;
+    copy_async<4 * W>(dst + r * ld + c, p, on);
+  }
+}
+
+// checkpoint of a row's 128 columns, four in each lane
+__device__ __forceinline__ void put_ckpt(const CkptRef& k, int ld, int rows, int row, int n0, int C, const float* v) {
+  const int lane = threadIdx.x & 31;
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (n0 + lane + 32 * j < C) m = max(m, abs_bits(v[j]));
+  const uint32_t code = ckpt_scale_code(__reduce_max_sync(0xffffffffu, m));
+  const float inv = ckpt_inv_scale(code);
+  int8_t* q = k.q + static_cast<size_t>(row) * ld + n0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (n0 + lane + 32 * j < C) q[lane + 32 * j] = static_cast<int8_t>(ckpt_code(v[j], inv));
+  if (lane == 0) k.s[static_cast<size_t>(n0 / kCkptGroup) * rows + row] = static_cast<uint8_t>(code);
+}
+
+// VEC: rows of both operands start on 16-byte boundaries
+template <int KIND, int BM, int R, bool VEC>
+__global__ void __launch_bounds__(32 * BM / R) k_linear_simt(LinearArgs a, int splits, int per) {
+  constexpr int T = 32 * BM / R;
+  constexpr bool A_KM = KIND == GRAD_W;    // A staged [k][m], else [m][k]
+  constexpr bool B_KN = KIND != FORWARD;   // B staged [k][n], else [n][k]
+  constexpr int LDA = A_KM ? BM : LDK, LDB = B_KN ? BN : LDK;
+  constexpr int A_FLOATS = A_KM ? BK * BM : BM * LDK, B_FLOATS = B_KN ? BK * BN : BN * LDK;
+  __shared__ __align__(16) float buf[NS * (A_FLOATS + B_FLOATS)];
+  static_assert(BM * BN <= NS * (A_FLOATS + B_FLOATS), "the partial tile goes over the stages");
+  auto As = [&](int s) { return buf + s * A_FLOATS; };
+  auto Bs = [&](int s) { return buf + NS * A_FLOATS + s * B_FLOATS; };
   pdl_launch_dependents();
   pdl_wait();
   const int nt = (a.N + BN - 1) / BN;
   const int m0 = blockIdx.x / nt * BM;
   const int n0 = blockIdx.x % nt * BN;
-  const int tid = threadIdx.x;
-  const int tx = tid & 15, ty = tid >> 4;
-  const T* A = static_cast<const T*>(a.a);
-  const T* B = static_cast<const T*>(a.b);
-  float acc[4][8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float* A = static_cast<const float*>(a.a);
+  const float* B = static_cast<const float*>(a.b);
 
-  float ra[4], rb[8];
-  auto fetch = [&](int k0) {
-    if (KIND == GRAD_W) {  // gy [K, M]
-      const int k = k0 + (tid >> 4), m = m0 + 4 * (tid & 15);
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        ra[e] = k < a.K && m + e < a.M ? elem_to_f<T>(A[static_cast<size_t>(k) * a.M + m + e]) : 0.f;
-    } else {               // x or gy [M, K]
-      const int m = m0 + (tid >> 2), k = k0 + 4 * (tid & 3);
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        ra[e] = m < a.M && k + e < a.K ? elem_to_f<T>(A[static_cast<size_t>(m) * a.K + k + e]) : 0.f;
-    }
-    if (KIND == FORWARD) {  // w [N, K]
-      const int n = n0 + (tid >> 1), k = k0 + 8 * (tid & 1);
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        rb[e] = n < a.N && k + e < a.K ? elem_to_f<T>(B[static_cast<size_t>(n) * a.K + k + e]) : 0.f;
-    } else if (KIND == BACK) {  // w [K, N]
-      const int k = k0 + (tid >> 4), n = n0 + 8 * (tid & 15);
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        rb[e] = k < a.K && n + e < a.N ? elem_to_f<T>(B[static_cast<size_t>(k) * a.N + n + e]) : 0.f;
-    } else {                // codes [K, ld]
-      const int k = k0 + (tid >> 4), n = n0 + 8 * (tid & 15);
-      const bool on = k < a.K && n < a.N;
-      uint2 w = make_uint2(0u, 0u);
-      float scale = 0.f;
-      if (on) {
-        w = *reinterpret_cast<const uint2*>(a.ck.q + static_cast<size_t>(k) * a.ld + n);
-        scale = ckpt_scale(a.ck.s[static_cast<size_t>(n / kCkptGroup) * a.K + k]);
-      }
-      ckpt_values4(w.x, scale, rb);
-      ckpt_values4(w.y, scale, rb + 4);
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (n + e >= a.N) rb[e] = 0.f;  // padding codes are not defined
-    }
-  };
-  auto stage = [&]() {
-    if (KIND == GRAD_W) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) As[tid >> 4][4 * (tid & 15) + e] = ra[e];
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) As[4 * (tid & 3) + e][tid >> 2] = ra[e];
-    }
+  auto stage = [&](int s, int k0) {
+    if (A_KM) stage_block<BK, BM, T, VEC>(As(s), LDA, A, k0, m0, a.K, a.M);
+    else stage_block<BM, BK, T, VEC>(As(s), LDA, A, m0, k0, a.M, a.K);
     if (KIND == FORWARD) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) Bs[8 * (tid & 1) + e][tid >> 1] = rb[e];
+      stage_block<BN, BK, T, VEC>(Bs(s), LDB, B, n0, k0, a.N, a.K);
+    } else if (KIND == BACK) {
+      stage_block<BK, BN, T, VEC>(Bs(s), LDB, B, k0, n0, a.K, a.N);
     } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) Bs[tid >> 4][8 * (tid & 15) + e] = rb[e];
+      // eight codes of a token a thread (rows of codes are padded to 16)
+      for (int i = threadIdx.x; i < BK * BN / 8; i += T) {
+        const int k = i / (BN / 8), c = 8 * (i % (BN / 8));
+        const bool on = k0 + k < a.K && n0 + c < a.N;
+        uint2 w = make_uint2(0u, 0u);
+        float scale = 0.f;
+        if (on) {
+          w = *reinterpret_cast<const uint2*>(a.ck.q + static_cast<size_t>(k0 + k) * a.ld + n0 + c);
+          scale = ckpt_scale(a.ck.s[static_cast<size_t>(n0 / kCkptGroup) * a.K + k0 + k]);
+        }
+        float2 v[4];
+        ckpt_pairs8(w, scale, v);
+        float* d = Bs(s) + k * LDB + c;
+        *reinterpret_cast<float4*>(d) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+        *reinterpret_cast<float4*>(d + 4) = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+      }
     }
   };
 
-  fetch(0);
-  for (int k0 = 0; k0 < a.K; k0 += BK) {
-    __syncthreads();
-    stage();
-    __syncthreads();
-    if (k0 + BK < a.K) fetch(k0 + BK);  // in flight over the products of this slice
+  float acc[R][4];
 #pragma unroll
-    for (int k = 0; k < BK; ++k) {
-      const float4 av = *reinterpret_cast<const float4*>(&As[k][4 * ty]);
-      const float4 b0 = *reinterpret_cast<const float4*>(&Bs[k][4 * tx]);
-      const float4 b1 = *reinterpret_cast<const float4*>(&Bs[k][64 + 4 * tx]);
-      const float am[4] = {av.x, av.y, av.z, av.w};
-      const float bn[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+  for (int i = 0; i < R; ++i)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+
+  const int rank = blockIdx.z;  // == rank in the cluster (1 x 1 x splits)
+  const int k_begin = rank * per * BK;
+  const int nk = max(0, min(per, (a.K + BK - 1) / BK - rank * per));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[i][j] = fmaf(am[i], bn[j], acc[i][j]);
+  for (int s = 0; s < NS - 1; ++s) {
+    if (s < nk) stage(s, k_begin + s * BK);
+    cp_async_commit();
+  }
+  int s = 0;
+  for (int kc = 0; kc < nk; ++kc) {
+    cp_async_wait<NS - 2>();
+    __syncthreads();  // slice kc is there for all, and slot kc + NS - 1 was read by all
+    {
+      const int next = kc + NS - 1;
+      if (next < nk) stage(next % NS, k_begin + next * BK);
+      cp_async_commit();
     }
+    const float* as = As(s) + (A_KM ? warp * R : warp * R * LDA);
+    const float* bs = Bs(s);
+#pragma unroll
+    for (int k4 = 0; k4 < BK; k4 += 4) {
+      float b[4][4];  // [k][column]
+      if (B_KN) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) b[k][j] = bs[(k4 + k) * LDB + lane + 32 * j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float4 v = *reinterpret_cast<const float4*>(bs + (lane + 32 * j) * LDB + k4);
+          b[0][j] = v.x; b[1][j] = v.y; b[2][j] = v.z; b[3][j] = v.w;
+        }
+      }
+      if (A_KM) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int i = 0; i < R; i += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(as + (k4 + k) * LDA + i);
+            const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) acc[i + e][j] = fmaf(x[e], b[k][j], acc[i + e][j]);
+          }
+      } else {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          const float4 v = *reinterpret_cast<const float4*>(as + i * LDA + k4);
+          const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(x[k], b[k][j], acc[i][j]);
+        }
+      }
+    }
+    if (++s == NS) s = 0;
   }
 
-  const int c0 = n0 + 4 * tx, c1 = c0 + 64;
-  const bool vec = a.vec;
-  float bias[8];
-  if (KIND != BACK && a.bias) {  // forward: bias; grad_w: column scale
-    load_part<4>(static_cast<const T*>(a.bias) + c0, a.N - c0, vec, bias);
-    load_part<4>(static_cast<const T*>(a.bias) + c1, a.N - c1, vec, bias + 4);
-  }
+  // partial tile [row][column] over the stages
+  cp_async_wait<0>();
+  __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int m = m0 + 4 * ty + i;
-    const bool on = m < a.M;
-    const size_t base = static_cast<size_t>(on ? m : 0) * a.N;
-    const int n_0 = on ? a.N - c0 : 0, n_1 = on ? a.N - c1 : 0;
-    float* v = acc[i];
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) buf[(warp * R + i) * BN + lane + 32 * j] = acc[i][j];
+  if (splits > 1) cluster_sync(); else __syncwarp();  // one CTA: a warp finishes its own rows
+
+  float bias[4];
+  bool on[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int c = n0 + lane + 32 * j;
+    on[j] = c < a.N;
+    bias[j] = a.bias && on[j] ? static_cast<const float*>(a.bias)[c] : 0.f;  // grad_w: column scale
+  }
+  const int first = splits > 1 ? rank + splits * warp : warp * R;
+  const int step = splits > 1 ? splits * (BM / R) : 1;
+  const int last = min(splits > 1 ? BM : warp * R + R, a.M - m0);
+#pragma unroll 2
+  for (int i = first; i < last; i += step) {
+    const int m = m0 + i;
+    const size_t base = static_cast<size_t>(m) * a.N + n0 + lane;
+    const float* src = buf + i * BN + lane;
+    float v[4];
+    if (splits == 1) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = src[32 * j];
+    } else {
+      float part[8][4];
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (q < splits) {
+          const uint32_t at = dsmem_addr(src, q);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) part[q][j] = dsmem_ld(at + 128 * j);
+        }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[j] = part[0][j];
+#pragma unroll
+        for (int q = 1; q < 8; ++q)
+          if (q < splits) v[j] += part[q][j];
+      }
+    }
     if (KIND == GRAD_W) {
       float* out = static_cast<float*>(a.out) + base;
-      if (a.bias) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= bias[j];
-      }
-      if (a.accumulate) {
-        float o[8];
-        load_part<4>(out + c0, n_0, vec, o);
-        load_part<4>(out + c1, n_1, vec, o + 4);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] += o[j];
-      }
-      store_part<4>(out + c0, n_0, vec, v);
-      store_part<4>(out + c1, n_1, vec, v + 4);
+      for (int j = 0; j < 4; ++j)
+        if (on[j]) {
+          const float x = a.bias ? v[j] * bias[j] : v[j];
+          out[32 * j] = a.accumulate ? out[32 * j] + x : x;
+        }
       continue;
     }
     if (KIND == FORWARD) {
-      if (a.bias) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] += bias[j];
-      }
-      if (a.zk.q) put_ckpt(a.zk, a.ld, a.M, m, on, c0, c1, a.N, v);
+      for (int j = 0; j < 4; ++j) v[j] += bias[j];
+      if (a.zk.q) put_ckpt(a.zk, a.ld, a.M, m, n0, a.N, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = act_f32(v[j], a.act);
+      for (int j = 0; j < 4; ++j) v[j] = act_f32(v[j], a.act);
     } else if (a.act != INSTANT_ACT_NONE) {
-      uint32_t w0 = 0, w1 = 0;
-      float scale = 0.f;
-      if (on && c0 < a.N) {
-        const int8_t* q = a.ck.q + static_cast<size_t>(m) * a.ld;
-        w0 = *reinterpret_cast<const uint32_t*>(q + c0);
-        if (c1 < a.N) w1 = *reinterpret_cast<const uint32_t*>(q + c1);
-        scale = ckpt_scale(a.ck.s[static_cast<size_t>(c0 / kCkptGroup) * a.M + m]);
-      }
-      float z[8];
-      ckpt_values4(w0, scale, z);
-      ckpt_values4(w1, scale, z + 4);
+      const float scale = ckpt_scale(a.ck.s[static_cast<size_t>(n0 / kCkptGroup) * a.M + m]);
+      const int8_t* q = a.ck.q + static_cast<size_t>(m) * a.ld + n0 + lane;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= act_slope_f32(z[j], a.act);
+      for (int j = 0; j < 4; ++j)
+        if (on[j]) v[j] *= act_slope_f32(static_cast<float>(q[32 * j]) * scale, a.act);
     }
     if (a.res) {
-      float o[8];
-      load_part<4>(static_cast<const T*>(a.res) + base + c0, n_0, vec, o);
-      load_part<4>(static_cast<const T*>(a.res) + base + c1, n_1, vec, o + 4);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] += o[j];
+      for (int j = 0; j < 4; ++j)
+        if (on[j]) v[j] += static_cast<const float*>(a.res)[base + 32 * j];
     }
-    if (KIND == FORWARD && a.yk.q) put_ckpt(a.yk, a.ld, a.M, m, on, c0, c1, a.N, v);
+    if (KIND == FORWARD && a.yk.q) put_ckpt(a.yk, a.ld, a.M, m, n0, a.N, v);
     if (a.out) {
-      T* out = static_cast<T*>(a.out) + base;
-      store_part<4>(out + c0, n_0, vec, v);
-      store_part<4>(out + c1, n_1, vec, v + 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (on[j]) static_cast<float*>(a.out)[base + 32 * j] = v[j];
     }
   }
+  if (splits > 1) cluster_sync();  // peers may still read this CTA's tile
 }
 
-template <typename T, int KIND>
+template <int KIND, int BM, int R>
 cudaError_t go(const LinearArgs& a, cudaStream_t st) {
   const long long tiles = static_cast<long long>((a.M + BM - 1) / BM) * ((a.N + BN - 1) / BN);
   if (tiles > 0x7fffffffll) return cudaErrorInvalidValue;
-  return launch_ex(k_linear_simt<T, KIND>, dim3(static_cast<unsigned>(tiles)), dim3(kThreads), 0, st, 1,
-                   pdl_enabled(), a);
+  // 16-byte copies where every row of both operands starts on a 16-byte boundary
+  const bool vec = (KIND == GRAD_W ? a.M : a.K) % 4 == 0 &&
+                   (KIND == GRAD_W ? true : (KIND == BACK ? a.N : a.K) % 4 == 0);
+  // shares of K: about two CTAs an SM, at least four slices each
+  const int nk = (a.K + BK - 1) / BK;
+  const int want = static_cast<int>(std::min<long long>(8, 2ll * sm_count() / tiles));
+  int splits = std::max(1, std::min(want, nk / 4));
+  const int per = (nk + splits - 1) / splits;
+  splits = (nk + per - 1) / per;
+  const dim3 grid(static_cast<unsigned>(tiles), 1, splits), block(32 * BM / R);
+  return vec ? launch_ex(k_linear_simt<KIND, BM, R, true>, grid, block, 0, st, splits, pdl_enabled(), a, splits, per)
+             : launch_ex(k_linear_simt<KIND, BM, R, false>, grid, block, 0, st, splits, pdl_enabled(), a, splits, per);
+}
+
+// row tiles of 64 where the rows or the grid call for them, else 16
+template <int KIND>
+cudaError_t go_rows(const LinearArgs& a, cudaStream_t st) {
+  return a.M > 32 ? go<KIND, 64, 8>(a, st) : go<KIND, 16, 4>(a, st);
 }
 
 }  // namespace
 
-cudaError_t launch_linear_simt(const LinearArgs& a, bool bf16, cudaStream_t st) {
+cudaError_t launch_linear_simt(const LinearArgs& a, cudaStream_t st) {
   switch (a.kind) {
-    case FORWARD: return bf16 ? go<uint16_t, FORWARD>(a, st) : go<float, FORWARD>(a, st);
-    case BACK: return bf16 ? go<uint16_t, BACK>(a, st) : go<float, BACK>(a, st);
-    default: return bf16 ? go<uint16_t, GRAD_W>(a, st) : go<float, GRAD_W>(a, st);
+    case FORWARD: return go_rows<FORWARD>(a, st);
+    case BACK: return go_rows<BACK>(a, st);
+    default: return go_rows<GRAD_W>(a, st);
   }
 }
 

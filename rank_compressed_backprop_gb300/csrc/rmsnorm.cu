@@ -500,7 +500,7 @@ __global__ void __launch_bounds__((W > 8 ? 32 * W : 256) + 32, CTAS)
 // gives (us, streaming / direct, bf16: 8192 x 4096 48.7 / 95.5, 8191 x 11008
 // 116 / 267, 512 x 11008 21 / 29, 16384 x 768 30 / 44; 300 x 8192 14.6 / 12.4,
 // 8192 x 64 8.7 / 8.1).  A slot holds about 16 KB, the CTAs of an SM about 220 KB.
-bool stream_plan(StreamPlan& p, const NormBackArgs& a, size_t elem, int w, int v, int ctas) {
+bool stream_plan(StreamPlan& p, const NormBackArgs& a, size_t elem, int w, int v, int ctas, int most_ctas) {
   const int slots = w > 8 ? 1 : 8 / w;
   const int groups = (a.C + kCkptGroup - 1) / kCkptGroup;
   const size_t row = elem * a.C;
@@ -509,7 +509,7 @@ bool stream_plan(StreamPlan& p, const NormBackArgs& a, size_t elem, int w, int v
   p.block = static_cast<int>(slots * passes);
   p.blocks = (a.rows + p.block - 1) / p.block;
   const int full = ctas * std::min(sm_count(), kColSumSMs);
-  if (p.blocks < 2 * full) return false;
+  if (p.blocks < 2 * most_ctas * sm_count()) return false;
   p.grid = std::min(full, norm_back_parts(a.rows, a.C));  // the workspace's shares
   p.per_cta = (p.blocks + p.grid - 1) / p.grid;
   p.grid = (p.blocks + p.per_cta - 1) / p.per_cta;
@@ -541,7 +541,7 @@ template <typename T, int W, int V, int CTAS>
 cudaError_t back_stream_go(const NormBackArgs& a, bool* done, cudaStream_t st) {
   StreamPlan p;
   *done = false;
-  for (int ctas = CTAS; ctas >= 1 && !*done; --ctas)  // fewer CTAs have wider rings *done = stream_plan(p, a, sizeof(T), W, V, ctas);
+  for (int ctas = CTAS; ctas >= 1 && !*done; --ctas)  // fewer CTAs have wider rings *done = stream_plan(p, a, sizeof(T), W, V, ctas, CTAS);
   if (!*done) return cudaSuccess;
   auto k = k_rms_norm_back_stream<T, W, V, CTAS>;
   cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(k), p.smem, true);
