@@ -15,9 +15,12 @@
 //              ring; the arrivals of both CTAs are counted on the leader's
 //              barrier (the leader issues the products of both)
 //   warp 1     MMA issuer (the leader's only); commits free the stage in both CTAs
-//   warps 4-7, 8-11  epilogue: columns 0-127 and 128-255 of the accumulator, a
-//              thread a row, so that a thread sees a whole checkpoint group and
-//              finds its largest magnitude without talking to another
+//   warps 4-19  epilogue: four groups of four warps, each 64 columns of the
+//              accumulator, a thread a row.  (Two groups of 128 columns a thread left
+//              two warps on each scheduler, whose latencies showed: 12544 x 448 ->
+//              1792 with gelu and both checkpoints 53 us.)  Two groups share the 128
+//              columns of a checkpoint group and exchange the scale byte of their
+//              halves' largest magnitudes: the larger byte is the group's
 // The tensor cores' fp32 accumulation cuts low bits at every step, which adds
 // up over a long contraction (6e-6 of a 8192-token weight gradient).  Where the
 // output shows it (fp32 gradients, and checkpoints, whose codes flip) the
@@ -38,13 +41,19 @@ constexpr uint32_t A_BYTES = 128 * BK * 2;   // 16 KB
 constexpr uint32_t B_BYTES = 128 * BK * 2;   // 16 KB
 enum { FORWARD = 0, BACK = 1, GRAD_W = 2 };
 constexpr uint32_t STAGE = A_BYTES + B_BYTES;
-constexpr int NS = 5;                        // ring depth
 constexpr uint32_t BOX = 128 * 128;          // staging box: 128 rows x 128 bytes
-constexpr uint32_t BOX_OFF = NS * STAGE;     // two boxes for each epilogue group
-constexpr uint32_t VEC_OFF = BOX_OFF + 4 * BOX;  // 2 x 128 floats: the tile's bias or column scale
-constexpr uint32_t BAR_OFF = VEC_OFF + 1024;
-constexpr uint32_t SMEM = BAR_OFF + 128;
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;
+// Shared memory: the ring of chunks, the staging boxes (one for each epilogue
+// group; with checkpoints three for each pair of groups, at the cost of a stage), the tile's bias or column scale, scale bytes under exchange
+template <bool KEEP>
+struct Lay {
+  static constexpr int ns = KEEP ? 4 : 5;
+  static constexpr uint32_t box = ns * STAGE;
+  static constexpr uint32_t vec = box + (KEEP ? 6 : 4) * BOX;  // 4 groups x 64 floats
+  static constexpr uint32_t code = vec + 1024;                 // 2 pairs x 2 halves x 128 bytes
+  static constexpr uint32_t bar = code + 512;
+  static constexpr uint32_t total = bar + 128;
+};
 
 // ---- cluster-scope barriers and pair-wide tensor-core operations ----------
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
@@ -70,18 +79,24 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
   return true;
 }
 
-// one answer for the 128 threads of an epilogue group, which meet at barriers
-template <int ID>
-__device__ __forceinline__ bool mbar_wait_group(uint64_t* bar, uint32_t parity) {
+// barrier among the `count` threads of an epilogue group or pair of groups.  (An
+// id in a register reserves all barriers of the SM; this kernel has it to itself,
+// and its epilogue is one piece of code for all groups.)
+__device__ __forceinline__ void group_barrier(int id, int count) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
+// one answer for the threads of a group or pair, which meet at barriers
+__device__ __forceinline__ bool mbar_wait_group(uint64_t* bar, uint32_t parity, int id, int count) {
   const uint32_t mine = mbar_wait_cluster(bar, parity) ? 1u : 0u;
   uint32_t all;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.and.pred q, %2, 128, p;\n\t"
+      "barrier.cta.red.and.pred q, %2, %3, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(all)
-      : "r"(mine), "n"(ID)
+      : "r"(mine), "r"(id), "r"(count)
       : "memory");
   return all != 0;
 }
@@ -211,31 +226,16 @@ __device__ __forceinline__ void load_row8(const uint16_t* p, int n, float* v) {
   }
 }
 
-struct Boxes {  // the staging boxes of one epilogue group of 128 threads
-  uint8_t* base;
-  int used;
-  int lead;     // the thread that issues the stores
-  // a box whose previous store has been read out; every thread of the group calls it
-  template <int BARRIER>
-  __device__ __forceinline__ uint8_t* next() {
-    if (lead) tma_store_wait_read<1>();
-    named_barrier<BARRIER>(128);
-    uint8_t* b = base + (used & 1) * BOX;
-    ++used;
-    return b;
-  }
-};
-
 // ---------------------------------------------------------------------------
-// epilogues: one 128-column group of the tile, a row a thread, values in pairs
+// epilogues: 64 columns of the tile, a row a thread, values in pairs
 // ---------------------------------------------------------------------------
-// `n` pairs of a row vector of the tile (bias or column scale, fp32 in shared
-// memory: one address for the whole warp) starting at column c
+// 2 N columns of a row vector of the tile (bias or column scale, fp32 in shared
+// memory: one address for the whole warp)
 template <int N, bool MUL>
-__device__ __forceinline__ void with_row_vector(const float* vec, int c, float2* v) {
+__device__ __forceinline__ void with_row_vector(const float* vec, float2* v) {
 #pragma unroll
   for (int i = 0; i < N; i += 2) {
-    const float4 b = *reinterpret_cast<const float4*>(vec + c + 2 * i);
+    const float4 b = *reinterpret_cast<const float4*>(vec + 2 * i);
     const float2 lo = make_float2(b.x, b.y), hi = make_float2(b.z, b.w);
     v[i] = MUL ? mul2(v[i], lo) : add2(v[i], lo);
     v[i + 1] = MUL ? mul2(v[i + 1], hi) : add2(v[i + 1], hi);
@@ -254,150 +254,63 @@ __device__ __forceinline__ void add_row(const uint16_t* p, int n, float2* v) {
   }
 }
 
-// 64 columns in bf16
-template <int BARRIER>
-__device__ __forceinline__ void put_box_bf16(const TcArgs& a, const CUtensorMap* map, Boxes& bx, int r,
-                                             const float2* v, int col, int row0) {
-  uint8_t* row = bx.next<BARRIER>() + r * 128;
-#pragma unroll
-  for (int c = 0; c < 8; ++c)
-    *reinterpret_cast<uint4*>(row + ((c ^ (r & 7)) << 4)) =
-        make_uint4(pack_bf16x2(v[4 * c].x, v[4 * c].y), pack_bf16x2(v[4 * c + 1].x, v[4 * c + 1].y),
-                   pack_bf16x2(v[4 * c + 2].x, v[4 * c + 2].y), pack_bf16x2(v[4 * c + 3].x, v[4 * c + 3].y));
-  fence_proxy_async_smem();
-  named_barrier<BARRIER>(128);
-  if (bx.lead) {
-    if (col < a.N && row0 < a.M) tma_store_2d(map, row - r * 128, col, row0);
-    tma_store_commit();
-  }
+// 16-byte piece c of row r of a staging box
+__device__ __forceinline__ void put_piece(uint8_t* box, int r, int c, uint4 v) {
+  *reinterpret_cast<uint4*>(box + r * 128 + ((c ^ (r & 7)) << 4)) = v;
 }
 
-// the checkpoint of 128 columns; columns past the tensor's end hold zeros
-template <int BARRIER>
-__device__ __forceinline__ void put_codes(const TcArgs& a, const CUtensorMap* map, uint8_t* s, Boxes& bx,
-                                          int r, const float2* v, int col, int row0) {
+// 2 N columns in bf16 from piece c0 of the box on
+template <int N>
+__device__ __forceinline__ void put_bf16(uint8_t* box, int r, int c0, const float2* v) {
+#pragma unroll
+  for (int c = 0; c < N / 4; ++c)
+    put_piece(box, r, c0 + c,
+              make_uint4(pack_bf16x2(v[4 * c].x, v[4 * c].y), pack_bf16x2(v[4 * c + 1].x, v[4 * c + 1].y),
+                         pack_bf16x2(v[4 * c + 2].x, v[4 * c + 2].y), pack_bf16x2(v[4 * c + 3].x, v[4 * c + 3].y)));
+}
+
+// scale code of the largest of 64 magnitudes
+__device__ __forceinline__ uint32_t half_code(const float2* v) {
   float m[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int j = 0; j < 64; ++j) m[j & 3] = max_abs3(m[j & 3], v[j].x, v[j].y);
-  const uint32_t code = ckpt_scale_code(__float_as_uint(max_abs3(max_abs3(m[0], m[1], m[2]), m[3], 0.f)));
+  for (int j = 0; j < 32; ++j) m[j & 3] = max_abs3(m[j & 3], v[j].x, v[j].y);
+  return ckpt_scale_code(__float_as_uint(max_abs3(max_abs3(m[0], m[1], m[2]), m[3], 0.f)));
+}
+
+// codes of 64 columns
+__device__ __forceinline__ void make_codes(uint4 (&q)[4], uint32_t code, const float2* v) {
   const float inv = ckpt_inv_scale(code);
-  uint8_t* row = bx.next<BARRIER>() + r * 128;
-  if (code != 248u) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const float2* w = v + 8 * c;
-      *reinterpret_cast<uint4*>(row + ((c ^ (r & 7)) << 4)) =
-          make_uint4(ckpt_code4_in_range(w[0], w[1], inv), ckpt_code4_in_range(w[2], w[3], inv),
-                     ckpt_code4_in_range(w[4], w[5], inv), ckpt_code4_in_range(w[6], w[7], inv));
-    }
-  } else {
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const float2* w = v + 8 * c;
-      *reinterpret_cast<uint4*>(row + ((c ^ (r & 7)) << 4)) =
-          make_uint4(ckpt_code4(w[0].x, w[0].y, w[1].x, w[1].y, inv), ckpt_code4(w[2].x, w[2].y, w[3].x, w[3].y, inv),
-                     ckpt_code4(w[4].x, w[4].y, w[5].x, w[5].y, inv), ckpt_code4(w[6].x, w[6].y, w[7].x, w[7].y, inv));
-    }
-  }
-  if (col < a.N && row0 + r < a.M)
-    s[static_cast<size_t>(col / kCkptGroup) * a.M + row0 + r] = static_cast<uint8_t>(code);
-  fence_proxy_async_smem();
-  named_barrier<BARRIER>(128);
-  if (bx.lead) {
-    if (col < a.N && row0 < a.M) tma_store_2d(map, row - r * 128, col, row0);
-    tma_store_commit();
+  for (int c = 0; c < 4; ++c) {
+    const float2* w = v + 8 * c;
+    if (code != 248u)
+      q[c] = make_uint4(ckpt_code4_in_range(w[0], w[1], inv), ckpt_code4_in_range(w[2], w[3], inv),
+                        ckpt_code4_in_range(w[4], w[5], inv), ckpt_code4_in_range(w[6], w[7], inv));
+    else
+      q[c] = make_uint4(ckpt_code4(w[0].x, w[0].y, w[1].x, w[1].y, inv), ckpt_code4(w[2].x, w[2].y, w[3].x, w[3].y, inv),
+                        ckpt_code4(w[4].x, w[4].y, w[5].x, w[5].y, inv), ckpt_code4(w[6].x, w[6].y, w[7].x, w[7].y, inv));
   }
 }
 
-// forward with checkpoints: the group's 128 values stay in registers from the
-// accumulator to the last output
-template <int ACT, int BARRIER>
-__device__ __forceinline__ void epi_forward_keep(const TcArgs& a, const CUtensorMap* my,
-                                                 const CUtensorMap* mz, const CUtensorMap* mk, Boxes& bx,
-                                                 const float* vec, float2* v, int r, int col, int row0) {
-  const bool on = row0 + r < a.M;
-  if (a.bias) with_row_vector<64, false>(vec, 0, v);
-  if (a.zs) put_codes<BARRIER>(a, mz, a.zs, bx, r, v, col, row0);
-#pragma unroll
-  for (int j = 0; j < 64; ++j) v[j] = act_fast<ACT>(v[j]);
-  if (a.res)
-    add_row<64>(static_cast<const uint16_t*>(a.res) + static_cast<size_t>(on ? row0 + r : 0) * a.N + col,
-                on ? a.N - col : 0, v);
-  if (a.ys) put_codes<BARRIER>(a, mk, a.ys, bx, r, v, col, row0);
-  if (a.out) {
-    put_box_bf16<BARRIER>(a, my, bx, r, v, col, row0);
-    put_box_bf16<BARRIER>(a, my, bx, r, v + 32, col + 64, row0);
-  }
-}
-
-// forward without checkpoints, and back: 64 columns at a time, c0 of the group
-template <int KIND, int ACT, int BARRIER>
-__device__ __forceinline__ void epi_half(const TcArgs& a, const CUtensorMap* my, Boxes& bx, const float* vec,
-                                         float2* v, const uint4* codes, float scale, int r, int c0, int col,
-                                         int row0) {
-  const bool on = row0 + r < a.M;
-  if (KIND == FORWARD) {
-    if (a.bias) with_row_vector<32, false>(vec, c0, v);
-#pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = act_fast<ACT>(v[j]);
-  } else if (ACT != INSTANT_ACT_NONE) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const uint32_t w[4] = {codes[c].x, codes[c].y, codes[c].z, codes[c].w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float z[4];
-        ckpt_values4(w[k], scale, z);
-        float2* p = v + 8 * c + 2 * k;
-        p[0] = mul2(p[0], act_slope_fast<ACT>(make_float2(z[0], z[1])));
-        p[1] = mul2(p[1], act_slope_fast<ACT>(make_float2(z[2], z[3])));
-      }
-    }
-  }
-  if (a.res)
-    add_row<32>(static_cast<const uint16_t*>(a.res) + static_cast<size_t>(on ? row0 + r : 0) * a.N + col + c0,
-                on ? a.N - col - c0 : 0, v);
-  put_box_bf16<BARRIER>(a, my, bx, r, v, col + c0, row0);
-}
-
-// grad_w: column scale, then four boxes of 32 fp32 columns
-template <int BARRIER>
-__device__ __forceinline__ void epi_grad_w(const TcArgs& a, const CUtensorMap* my, Boxes& bx, const float* vec,
-                                           float2* v, int r, int col, int row0) {
-  if (a.bias) with_row_vector<64, true>(vec, 0, v);
-#pragma unroll
-  for (int h = 0; h < 4; ++h) {
-    const int c0 = col + 32 * h;
-    const float2* w = v + 16 * h;
-    uint8_t* row = bx.next<BARRIER>() + r * 128;
-#pragma unroll
-    for (int c = 0; c < 8; ++c)
-      *reinterpret_cast<float4*>(row + ((c ^ (r & 7)) << 4)) =
-          make_float4(w[2 * c].x, w[2 * c].y, w[2 * c + 1].x, w[2 * c + 1].y);
-    fence_proxy_async_smem();
-    named_barrier<BARRIER>(128);
-    if (bx.lead) {
-      if (c0 < a.N && row0 < a.M) {
-        if (a.accumulate) tma_add_2d(my, row - r * 128, c0, row0);
-        else tma_store_2d(my, row - r * 128, c0, row0);
-      }
-      tma_store_commit();
-    }
-  }
-}
-
-template <int KIND, int ACT, bool KEEP, int BARRIER>
+template <int KIND, int ACT, bool KEEP>
 __device__ __forceinline__ void epilogue(const TcArgs& a, const CUtensorMap* my, const CUtensorMap* mz,
-                                         const CUtensorMap* mk, uint8_t* boxes, float* vec, uint32_t tmem,
+                                         const CUtensorMap* mk, uint8_t* smem, uint32_t tmem,
                                          uint64_t* t_full, uint32_t t_empty_leader, uint32_t rank,
-                                         int pair, int pairs, int half) {
+                                         int pair, int pairs) {
+  using L = Lay<KEEP>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int quarter = warp & 3;
-  const int r = quarter * 32 + lane;
-  Boxes bx{boxes, 0, (threadIdx.x & 127) == 0};
+  const int group = (warp - 4) >> 2;        // 64 columns each
+  const int r = (warp & 3) * 32 + lane;     // TMEM lane
+  // with checkpoints two groups work as one of 256 threads
+  const int id = KEEP ? 5 + (group >> 1) : 1 + group, count = KEEP ? 256 : 128;
+  const bool lead = r == 0 && (!KEEP || (group & 1) == 0);  // issues the stores
+  uint8_t* boxes = smem + L::box + (KEEP ? (group >> 1) * 3 : group) * BOX;
+  float* vec = reinterpret_cast<float*>(smem + L::vec) + 64 * group;
+  uint8_t* zcode = smem + L::code + 256 * (group >> 1);                                 // [half][row]
+  uint8_t* ycode = reinterpret_cast<uint8_t*>(smem + L::vec) + 512 * (group >> 1);      // over vec
   const int tiles = a.mt * a.nt;
-  const uint32_t tbase = tmem + half * 128 + (static_cast<uint32_t>(quarter * 32) << 16);
-  int q = 0;  // accumulators read so far
+  const uint32_t tbase = tmem + 64 * group + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+  int q = 0;    // accumulators read so far
   auto release = [&](int acc) {  // the accumulator may be overwritten
     tc_fence_before();
     __syncwarp();
@@ -407,25 +320,26 @@ __device__ __forceinline__ void epilogue(const TcArgs& a, const CUtensorMap* my,
     int m, n;
     tile_at(a, t, m, n);
     const int row0 = m * BM + static_cast<int>(rank) * 128;
-    const int col = n * BN + half * 128;
-    // the columns' bias or scale, for the whole group: read by all of it before
-    // its last box of the tile before, and written before the wait below
-    if (a.bias && KIND != BACK)
+    const int col = n * BN + 64 * group;
+    const bool on = row0 + r < a.M;
+    // the columns' bias or scale, read by the whole group (or, as ycode, pair)
+    // before a barrier that all pass before the next tile, and written before the
+    // wait below
+    if (a.bias && KIND != BACK && r < 64)
       vec[r] = col + r < a.N ? bf16_to_f32(static_cast<const uint16_t*>(a.bias)[col + r]) : 0.f;
     if (KEEP || KIND == GRAD_W) {
-      float2 v[64];
+      float2 v[32];
       bool ok = true;
       for (int k0 = 0; k0 < a.nk; k0 += a.seg, ++q) {
         const int acc = q & 1;
-        ok = mbar_wait_group<BARRIER>(&t_full[acc], (q >> 1) & 1);
+        ok = mbar_wait_group(&t_full[acc], (q >> 1) & 1, id, count);
         if (!ok) break;
         tc_fence_after();
         if (k0 == 0) {
           tmem_read<64>(tbase + acc * BN, v);
-          tmem_read<64>(tbase + acc * BN + 64, v + 32);
         } else {
 #pragma unroll
-          for (int h = 0; h < 8; ++h) {
+          for (int h = 0; h < 4; ++h) {
             float w[16];
             tmem_ld16(tbase + acc * BN + 16 * h, w);
 #pragma unroll
@@ -439,42 +353,143 @@ __device__ __forceinline__ void epilogue(const TcArgs& a, const CUtensorMap* my,
         raise_fault(FAULT_WAIT_DONE);
         break;
       }
-      if (KIND == GRAD_W) epi_grad_w<BARRIER>(a, my, bx, vec, v, r, col, row0);
-      else epi_forward_keep<ACT, BARRIER>(a, my, mz, mk, bx, vec, v, r, col, row0);
+      if (a.bias) with_row_vector<32, KIND == GRAD_W>(vec, v);
+      if (KIND == GRAD_W) {
+        // two boxes of 32 fp32 columns
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (lead) tma_store_wait_read<0>();
+          group_barrier(id, count);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const float2* w = v + 16 * h + 2 * c;
+            put_piece(boxes, r, c, make_uint4(__float_as_uint(w[0].x), __float_as_uint(w[0].y),
+                                              __float_as_uint(w[1].x), __float_as_uint(w[1].y)));
+          }
+          fence_proxy_async_smem();
+          group_barrier(id, count);
+          if (lead) {
+            const int c0 = col + 32 * h;
+            if (c0 < a.N && row0 < a.M) {
+              if (a.accumulate) tma_add_2d(my, boxes, c0, row0);
+              else tma_store_2d(my, boxes, c0, row0);
+            }
+            tma_store_commit();
+          }
+        }
+        continue;
+      }
+      // Forward with checkpoints: z's codes go out through box 0, y's two halves
+      // through boxes 1 and 2, then y's codes through box 0 again, made in registers
+      // while z's are read out.  Columns past the tensor's end hold zeros.
+      const int half = group & 1, col0 = col - 64 * half;  // first column of the pair
+      const bool stores = col0 < a.N && row0 < a.M;
+      const size_t at = static_cast<size_t>(col0 / kCkptGroup) * a.M + row0 + r;
+      uint32_t code = 0;
+      uint4 codes[4];
+      if (a.zs) {
+        code = half_code(v);
+        zcode[128 * half + r] = static_cast<uint8_t>(code);
+      }
+      if (lead) tma_store_wait_read<0>();
+      group_barrier(id, count);  // scale bytes of z there, boxes free
+      if (a.zs) {
+        code = max(code, static_cast<uint32_t>(zcode[128 * (half ^ 1) + r]));
+        make_codes(codes, code, v);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) put_piece(boxes, r, 4 * half + c, codes[c]);
+        if (half == 0 && on && col0 < a.N) a.zs[at] = static_cast<uint8_t>(code);
+      }
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = act_fast<ACT>(v[j]);
+      if (a.res)
+        add_row<32>(static_cast<const uint16_t*>(a.res) + static_cast<size_t>(on ? row0 + r : 0) * a.N + col,
+                    on ? a.N - col : 0, v);
+      if (a.ys) {
+        code = half_code(v);
+        ycode[128 * half + r] = static_cast<uint8_t>(code);
+      }
+      if (a.out) put_bf16<32>(boxes + (1 + half) * BOX, r, 0, v);
+      fence_proxy_async_smem();
+      group_barrier(id, count);  // z's codes, y and its scale bytes there
+      if (lead) {
+        if (a.zs && stores) tma_store_2d(mz, boxes, col0, row0);
+        tma_store_commit();
+        if (a.out && stores) {
+          tma_store_2d(my, boxes + BOX, col0, row0);
+          if (col0 + 64 < a.N) tma_store_2d(my, boxes + 2 * BOX, col0 + 64, row0);
+        }
+        tma_store_commit();
+      }
+      if (a.ys) {
+        code = max(code, static_cast<uint32_t>(ycode[128 * (half ^ 1) + r]));
+        make_codes(codes, code, v);
+        if (half == 0 && on && col0 < a.N) a.ys[at] = static_cast<uint8_t>(code);
+        if (lead) tma_store_wait_read<1>();
+        group_barrier(id, count);  // box 0 free again
+#pragma unroll
+        for (int c = 0; c < 4; ++c) put_piece(boxes, r, 4 * half + c, codes[c]);
+        fence_proxy_async_smem();
+        group_barrier(id, count);
+        if (lead) {
+          if (stores) tma_store_2d(mk, boxes, col0, row0);
+          tma_store_commit();
+        }
+      }
     } else {
-      const bool on = row0 + r < a.M;
-      uint4 codes[8];
+      uint4 codes[4];
       float scale = 0.f;
       if (KIND == BACK && ACT != INSTANT_ACT_NONE) {
-        // this row's codes of the group, asked for before the products are done
+        // this row's codes, asked for before the products are done
         const int8_t* p = a.cq + static_cast<size_t>(on ? row0 + r : 0) * a.ld + col;
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
+        for (int c = 0; c < 4; ++c)
           codes[c] = on && col + 16 * c < a.N ? *reinterpret_cast<const uint4*>(p + 16 * c)
                                               : make_uint4(0u, 0u, 0u, 0u);
         if (on && col < a.N)
           scale = ckpt_scale(a.cs[static_cast<size_t>(col / kCkptGroup) * a.M + row0 + r]);
       }
       const int acc = q & 1;
-      if (!mbar_wait_group<BARRIER>(&t_full[acc], (q >> 1) & 1)) {
+      if (lead) tma_store_wait_read<0>();  // the group's box is free after the barrier of the wait
+      if (!mbar_wait_group(&t_full[acc], (q >> 1) & 1, id, count)) {
         raise_fault(FAULT_WAIT_DONE);
         break;
       }
       tc_fence_after();
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        float2 v[32];
-        tmem_read<64>(tbase + acc * BN + 64 * h, v);
-        if (h == 1) release(acc);
-        uint4 cc[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) cc[c] = h ? codes[4 + c] : codes[c];
-        epi_half<KIND, ACT, BARRIER>(a, my, bx, vec, v, cc, scale, r, 64 * h, col, row0);
+      for (int h = 0; h < 2; ++h) {  // 32 columns at a time
+        float2 v[16];
+        tmem_read<32>(tbase + acc * BN + 32 * h, v);
+        if (h == 1) release(acc);
+        if (KIND == FORWARD) {
+          if (a.bias) with_row_vector<16, false>(vec + 32 * h, v);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = act_fast<ACT>(v[j]);
+        } else if (ACT != INSTANT_ACT_NONE) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint4 w = codes[2 * h + (c >> 1)];
+            float2 z[4];
+            ckpt_pairs8(c & 1 ? make_uint2(w.z, w.w) : make_uint2(w.x, w.y), scale, z);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[4 * c + e] = mul2(v[4 * c + e], act_slope_fast<ACT>(z[e]));
+          }
+        }
+        if (a.res)
+          add_row<16>(static_cast<const uint16_t*>(a.res) + static_cast<size_t>(on ? row0 + r : 0) * a.N + col + 32 * h,
+                      on ? a.N - col - 32 * h : 0, v);
+        put_bf16<16>(boxes, r, 4 * h, v);
       }
       ++q;
+      fence_proxy_async_smem();
+      group_barrier(id, count);
+      if (lead) {
+        if (col < a.N && row0 < a.M) tma_store_2d(my, boxes, col, row0);
+        tma_store_commit();
+      }
     }
   }
-  if (bx.lead) tma_store_wait_all();
+  if (lead) tma_store_wait_all();
 }
 
 // ---------------------------------------------------------------------------
@@ -483,17 +498,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     k_linear_tc(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                 const __grid_constant__ CUtensorMap map_y, const __grid_constant__ CUtensorMap map_z,
                 const __grid_constant__ CUtensorMap map_k, TcArgs a) {
+  using L = Lay<KEEP>;
+  constexpr int NS = L::ns;
   constexpr bool A_MN = KIND == GRAD_W, B_MN = KIND != FORWARD;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + BAR_OFF);  // leader's: both CTAs' TMA bytes
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::bar);  // leader's: both CTAs' TMA bytes
   uint64_t* empty = full + NS;       // each CTA's: products of a chunk done
   uint64_t* t_full = empty + NS;     // [2] each CTA's: accumulator done
   uint64_t* t_empty = t_full + 2;    // [2] leader's: accumulator read
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(t_empty + 2);
-
-  float* vec = reinterpret_cast<float*>(smem + VEC_OFF);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -508,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&t_full[i], 1);
-      mbar_init(&t_empty[i], 16);  // epilogue warps of both CTAs
+      mbar_init(&t_empty[i], 32);  // epilogue warps of both CTAs
     }
     fence_barrier_init();
     prefetch_tmap(&map_a);
@@ -623,12 +638,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         }
       }
     }
-  } else if (warp >= 4 && warp < 8) {
-    epilogue<KIND, ACT, KEEP, 1>(a, &map_y, &map_z, &map_k, smem + BOX_OFF, vec, tmem, t_full,
-                                 dsmem_addr(t_empty, 0), rank, pair, pairs, 0);
-  } else if (warp >= 8) {
-    epilogue<KIND, ACT, KEEP, 2>(a, &map_y, &map_z, &map_k, smem + BOX_OFF + 2 * BOX, vec + 128, tmem, t_full,
-                                 dsmem_addr(t_empty, 0), rank, pair, pairs, 1);
+  } else if (warp >= 4) {
+    epilogue<KIND, ACT, KEEP>(a, &map_y, &map_z, &map_k, smem, tmem, t_full, dsmem_addr(t_empty, 0), rank, pair,
+                              pairs);
   }
   __syncwarp();
   tc_fence_before();
@@ -638,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 
 template <int KIND, int ACT, bool KEEP>
 cudaError_t go(const TcMaps& m, const TcArgs& a, cudaStream_t st) {
-  constexpr size_t bytes = SMEM + 1024;
+  constexpr size_t bytes = Lay<KEEP>::total + 1024;
   auto k = k_linear_tc<KIND, ACT, KEEP>;
   const cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(k), bytes);
   if (e != cudaSuccess) return e;
