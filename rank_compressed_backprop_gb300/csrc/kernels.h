@@ -378,11 +378,11 @@ struct TcArgs {
   uint8_t *zs, *ys;    // scale bytes of the checkpoints written (null: none)
   const int8_t* cq;    // checkpoint read
   const uint8_t* cs;
-  int ld;              // code pitch
+  int ld;              // its code pitch
   int accumulate;
 };
 struct TcMaps {
-  CUtensorMap a, b, y, z, k;
+  CUtensorMap a, b, y, z, k, r;
 };
 cudaError_t launch_linear_tc(const LinearArgs& a, cudaStream_t st);
 

@@ -27,9 +27,11 @@
 // accumulator holds `seg` chunks at a time and the epilogue threads add the
 // segments into registers in ordinary fp32, under the products of the next.
 // Operands contracted over their rows (w in back, gy and v in grad_w)
-// are MN-major operands read from their natural layout.  Outputs leave through
-// 128-byte-swizzled staging boxes and TMA stores, which also clip ragged edges;
-// accumulation into gw is the TMA's own add (each element is added to once).
+// are MN-major operands read from their natural layout.  The residual
+// comes by TMA into swizzled boxes while the products run -- a thread's own row by
+// plain loads touches 32 lines an access and doubled the time of 12544 x 448 ->
+// 1792 -- and the results leave through the same boxes by TMA stores, which also clip ragged edges; accumulation into gw is the TMA's own add
+// (each element is added to once).
 #include "ckpt.cuh"
 
 namespace instant {
@@ -43,16 +45,18 @@ enum { FORWARD = 0, BACK = 1, GRAD_W = 2 };
 constexpr uint32_t STAGE = A_BYTES + B_BYTES;
 constexpr uint32_t BOX = 128 * 128;          // staging box: 128 rows x 128 bytes
 constexpr int kThreads = 640;
-// Shared memory: the ring of chunks, the staging boxes (one for each epilogue
-// group; with checkpoints three for each pair of groups, at the cost of a stage), the tile's bias or column scale, scale bytes under exchange
+// Shared memory: the ring of chunks, the boxes through which epilogue operands
+// come in and results go out (one of 64 columns for each group; where checkpoints
+// are written a pair of groups has one of codes besides, at the cost of a stage),
+// the tile's bias or column scale, scale bytes under exchange
 template <bool KEEP>
 struct Lay {
   static constexpr int ns = KEEP ? 4 : 5;
   static constexpr uint32_t box = ns * STAGE;
   static constexpr uint32_t vec = box + (KEEP ? 6 : 4) * BOX;  // 4 groups x 64 floats
-  static constexpr uint32_t code = vec + 1024;                 // 2 pairs x 2 halves x 128 bytes
+  static constexpr uint32_t code = vec + 1024;                  // 2 pairs x 2 halves x 128 bytes
   static constexpr uint32_t bar = code + 512;
-  static constexpr uint32_t total = bar + 128;
+  static constexpr uint32_t total = bar + 160;
 };
 
 // ---- cluster-scope barriers and pair-wide tensor-core operations ----------
@@ -216,16 +220,6 @@ __device__ __forceinline__ void tmem_read(uint32_t taddr, float2* v) {
   for (int i = 0; i < N / 2; ++i) v[i] = make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
 }
 
-// eight elements of a row, 0 past its end
-__device__ __forceinline__ void load_row8(const uint16_t* p, int n, float* v) {
-  if (n >= 8) {
-    load_vec<8>(p, v);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.f;
-  }
-}
-
 // ---------------------------------------------------------------------------
 // epilogues: 64 columns of the tile, a row a thread, values in pairs
 // ---------------------------------------------------------------------------
@@ -242,21 +236,26 @@ __device__ __forceinline__ void with_row_vector(const float* vec, float2* v) {
   }
 }
 
-// adds 2 N columns of this thread's row of `p` (n of them exist)
-template <int N>
-__device__ __forceinline__ void add_row(const uint16_t* p, int n, float2* v) {
-#pragma unroll
-  for (int c = 0; c < N / 4; ++c) {
-    float o[8];
-    load_row8(p + 8 * c, n - 8 * c, o);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[4 * c + e] = add2(v[4 * c + e], make_float2(o[2 * e], o[2 * e + 1]));
-  }
-}
-
 // 16-byte piece c of row r of a staging box
 __device__ __forceinline__ void put_piece(uint8_t* box, int r, int c, uint4 v) {
   *reinterpret_cast<uint4*>(box + r * 128 + ((c ^ (r & 7)) << 4)) = v;
+}
+
+__device__ __forceinline__ uint4 get_piece(const uint8_t* box, int r, int c) {
+  return *reinterpret_cast<const uint4*>(box + r * 128 + ((c ^ (r & 7)) << 4));
+}
+
+// adds 2 N columns in bf16 from piece c0 of the box on
+template <int N>
+__device__ __forceinline__ void add_bf16(const uint8_t* box, int r, int c0, float2* v) {
+#pragma unroll
+  for (int c = 0; c < N / 4; ++c) {
+    const uint4 u = get_piece(box, r, c0 + c);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      v[4 * c + e] = add2(v[4 * c + e], make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u)));
+  }
 }
 
 // 2 N columns in bf16 from piece c0 of the box on
@@ -294,17 +293,23 @@ __device__ __forceinline__ void make_codes(uint4 (&q)[4], uint32_t code, const f
 
 template <int KIND, int ACT, bool KEEP>
 __device__ __forceinline__ void epilogue(const TcArgs& a, const CUtensorMap* my, const CUtensorMap* mz,
-                                         const CUtensorMap* mk, uint8_t* smem, uint32_t tmem,
-                                         uint64_t* t_full, uint32_t t_empty_leader, uint32_t rank,
-                                         int pair, int pairs) {
+                                         const CUtensorMap* mk, const CUtensorMap* mr, uint8_t* smem,
+                                         uint32_t tmem, uint64_t* t_full, uint64_t* in_full,
+                                         uint32_t t_empty_leader, uint32_t rank, int pair, int pairs) {
+  constexpr bool PAIRS = KEEP;  // two groups share the 128 columns of a checkpoint's groups
+  constexpr bool CODES = KIND == BACK && ACT != INSTANT_ACT_NONE;
   using L = Lay<KEEP>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = (warp - 4) >> 2;        // 64 columns each
   const int r = (warp & 3) * 32 + lane;     // TMEM lane
-  // with checkpoints two groups work as one of 256 threads
-  const int id = KEEP ? 5 + (group >> 1) : 1 + group, count = KEEP ? 256 : 128;
-  const bool lead = r == 0 && (!KEEP || (group & 1) == 0);  // issues the stores
-  uint8_t* boxes = smem + L::box + (KEEP ? (group >> 1) * 3 : group) * BOX;
+  const int half = group & 1;               // of a pair
+  const int id = PAIRS ? 5 + (group >> 1) : 1 + group, count = PAIRS ? 256 : 128;
+  const bool lead = r == 0 && (!PAIRS || half == 0);  // issues loads and stores
+  // a pair's boxes: codes, y's first half, y's second; a group's: y
+  uint8_t* boxes = smem + L::box + (PAIRS ? (group >> 1) * 3 : group) * BOX;
+  uint8_t* ybox = PAIRS ? boxes + (1 + half) * BOX : boxes;
+  in_full += PAIRS ? group >> 1 : group;    // epilogue operands arrived
+  int in_par = 0;
   float* vec = reinterpret_cast<float*>(smem + L::vec) + 64 * group;
   uint8_t* zcode = smem + L::code + 256 * (group >> 1);                                 // [half][row]
   uint8_t* ycode = reinterpret_cast<uint8_t*>(smem + L::vec) + 512 * (group >> 1);      // over vec
@@ -325,6 +330,18 @@ __device__ __forceinline__ void epilogue(const TcArgs& a, const CUtensorMap* my,
     // the columns' bias or scale, read by the whole group (or, as ycode, pair)
     // before a barrier that all pass before the next tile, and written before the
     // wait below
+    const int col0 = PAIRS ? col - 64 * half : col;  // first column of the pair or group
+    const bool stores = col0 < a.N && row0 < a.M;
+    auto wait_in = [&]() {
+      if (!mbar_wait(in_full, in_par)) raise_fault(FAULT_WAIT_FULL);
+      in_par ^= 1;
+    };
+    if (lead) tma_store_wait_read<0>();  // the boxes are free
+    if (lead && a.res) {
+      mbar_arrive_expect_tx(in_full, PAIRS ? 2 * BOX : BOX);
+      tma_load_2d(PAIRS ? boxes + BOX : boxes, mr, in_full, col0, row0);
+      if (PAIRS) tma_load_2d(boxes + 2 * BOX, mr, in_full, col0 + 64, row0);
+    }
     if (a.bias && KIND != BACK && r < 64)
       vec[r] = col + r < a.N ? bf16_to_f32(static_cast<const uint16_t*>(a.bias)[col + r]) : 0.f;
     if (KEEP || KIND == GRAD_W) {
@@ -358,8 +375,10 @@ __device__ __forceinline__ void epilogue(const TcArgs& a, const CUtensorMap* my,
         // two boxes of 32 fp32 columns
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (lead) tma_store_wait_read<0>();
-          group_barrier(id, count);
+          if (h == 1) {
+            if (lead) tma_store_wait_read<0>();
+            group_barrier(id, count);
+          }
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             const float2* w = v + 16 * h + 2 * c;
@@ -382,8 +401,6 @@ __device__ __forceinline__ void epilogue(const TcArgs& a, const CUtensorMap* my,
       // Forward with checkpoints: z's codes go out through box 0, y's two halves
       // through boxes 1 and 2, then y's codes through box 0 again, made in registers
       // while z's are read out.  Columns past the tensor's end hold zeros.
-      const int half = group & 1, col0 = col - 64 * half;  // first column of the pair
-      const bool stores = col0 < a.N && row0 < a.M;
       const size_t at = static_cast<size_t>(col0 / kCkptGroup) * a.M + row0 + r;
       uint32_t code = 0;
       uint4 codes[4];
@@ -391,7 +408,6 @@ __device__ __forceinline__ void epilogue(const TcArgs& a, const CUtensorMap* my,
         code = half_code(v);
         zcode[128 * half + r] = static_cast<uint8_t>(code);
       }
-      if (lead) tma_store_wait_read<0>();
       group_barrier(id, count);  // scale bytes of z there, boxes free
       if (a.zs) {
         code = max(code, static_cast<uint32_t>(zcode[128 * (half ^ 1) + r]));
@@ -402,14 +418,15 @@ __device__ __forceinline__ void epilogue(const TcArgs& a, const CUtensorMap* my,
       }
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] = act_fast<ACT>(v[j]);
-      if (a.res)
-        add_row<32>(static_cast<const uint16_t*>(a.res) + static_cast<size_t>(on ? row0 + r : 0) * a.N + col,
-                    on ? a.N - col : 0, v);
+      if (a.res) {
+        wait_in();
+        add_bf16<32>(ybox, r, 0, v);
+      }
       if (a.ys) {
         code = half_code(v);
         ycode[128 * half + r] = static_cast<uint8_t>(code);
       }
-      if (a.out) put_bf16<32>(boxes + (1 + half) * BOX, r, 0, v);
+      if (a.out) put_bf16<32>(ybox, r, 0, v);
       fence_proxy_async_smem();
       group_barrier(id, count);  // z's codes, y and its scale bytes there
       if (lead) {
@@ -437,10 +454,11 @@ __device__ __forceinline__ void epilogue(const TcArgs& a, const CUtensorMap* my,
         }
       }
     } else {
+      // the row's codes, asked for while the products run (by plain loads: half a
+      // line a thread, 4% faster here than through a box by TMA)
       uint4 codes[4];
       float scale = 0.f;
-      if (KIND == BACK && ACT != INSTANT_ACT_NONE) {
-        // this row's codes, asked for before the products are done
+      if (CODES) {
         const int8_t* p = a.cq + static_cast<size_t>(on ? row0 + r : 0) * a.ld + col;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
@@ -450,11 +468,11 @@ __device__ __forceinline__ void epilogue(const TcArgs& a, const CUtensorMap* my,
           scale = ckpt_scale(a.cs[static_cast<size_t>(col / kCkptGroup) * a.M + row0 + r]);
       }
       const int acc = q & 1;
-      if (lead) tma_store_wait_read<0>();  // the group's box is free after the barrier of the wait
       if (!mbar_wait_group(&t_full[acc], (q >> 1) & 1, id, count)) {
         raise_fault(FAULT_WAIT_DONE);
         break;
       }
+      if (a.res) wait_in();
       tc_fence_after();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {  // 32 columns at a time
@@ -465,26 +483,25 @@ __device__ __forceinline__ void epilogue(const TcArgs& a, const CUtensorMap* my,
           if (a.bias) with_row_vector<16, false>(vec + 32 * h, v);
 #pragma unroll
           for (int j = 0; j < 16; ++j) v[j] = act_fast<ACT>(v[j]);
-        } else if (ACT != INSTANT_ACT_NONE) {
+        } else if (CODES) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint4 w = codes[2 * h + (c >> 1)];
-            float2 z[4];
-            ckpt_pairs8(c & 1 ? make_uint2(w.z, w.w) : make_uint2(w.x, w.y), scale, z);
+          for (int c = 0; c < 2; ++c) {
+            const uint4 w = codes[2 * h + c];
+            float2 z[8];
+            ckpt_pairs8(make_uint2(w.x, w.y), scale, z);
+            ckpt_pairs8(make_uint2(w.z, w.w), scale, z + 4);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[4 * c + e] = mul2(v[4 * c + e], act_slope_fast<ACT>(z[e]));
+            for (int e = 0; e < 8; ++e) v[8 * c + e] = mul2(v[8 * c + e], act_slope_fast<ACT>(z[e]));
           }
         }
-        if (a.res)
-          add_row<16>(static_cast<const uint16_t*>(a.res) + static_cast<size_t>(on ? row0 + r : 0) * a.N + col + 32 * h,
-                      on ? a.N - col - 32 * h : 0, v);
-        put_bf16<16>(boxes, r, 4 * h, v);
+        if (a.res) add_bf16<16>(ybox, r, 4 * h, v);
+        put_bf16<16>(ybox, r, 4 * h, v);
       }
       ++q;
       fence_proxy_async_smem();
       group_barrier(id, count);
       if (lead) {
-        if (col < a.N && row0 < a.M) tma_store_2d(my, boxes, col, row0);
+        if (stores) tma_store_2d(my, boxes, col0, row0);
         tma_store_commit();
       }
     }
@@ -497,7 +514,7 @@ template <int KIND, int ACT, bool KEEP>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     k_linear_tc(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                 const __grid_constant__ CUtensorMap map_y, const __grid_constant__ CUtensorMap map_z,
-                const __grid_constant__ CUtensorMap map_k, TcArgs a) {
+                const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_r, TcArgs a) {
   using L = Lay<KEEP>;
   constexpr int NS = L::ns;
   constexpr bool A_MN = KIND == GRAD_W, B_MN = KIND != FORWARD;
@@ -508,7 +525,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   uint64_t* empty = full + NS;       // each CTA's: products of a chunk done
   uint64_t* t_full = empty + NS;     // [2] each CTA's: accumulator done
   uint64_t* t_empty = t_full + 2;    // [2] leader's: accumulator read
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(t_empty + 2);
+  uint64_t* in_full = t_empty + 2;   // [4] each CTA's: epilogue operands arrived
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(in_full + 4);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -525,6 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       mbar_init(&t_full[i], 1);
       mbar_init(&t_empty[i], 32);  // epilogue warps of both CTAs
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&in_full[i], 1);
     fence_barrier_init();
     prefetch_tmap(&map_a);
     prefetch_tmap(&map_b);
@@ -639,8 +658,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       }
     }
   } else if (warp >= 4) {
-    epilogue<KIND, ACT, KEEP>(a, &map_y, &map_z, &map_k, smem, tmem, t_full, dsmem_addr(t_empty, 0), rank, pair,
-                              pairs);
+    epilogue<KIND, ACT, KEEP>(a, &map_y, &map_z, &map_k, &map_r, smem, tmem, t_full, in_full,
+                              dsmem_addr(t_empty, 0), rank, pair, pairs);
   }
   __syncwarp();
   tc_fence_before();
@@ -657,7 +676,7 @@ cudaError_t go(const TcMaps& m, const TcArgs& a, cudaStream_t st) {
   const long long tiles = static_cast<long long>(a.mt) * a.nt;
   const int pairs = static_cast<int>(tiles < sm_count() / 2 ? tiles : sm_count() / 2);
   return launch_ex(k, dim3(2 * pairs), dim3(kThreads), bytes, st, 1, pdl_enabled(), m.a, m.b, m.y, m.z,
-                   m.k, a);
+                   m.k, m.r, a);
 }
 
 template <int KIND, bool KEEP>
@@ -719,6 +738,7 @@ cudaError_t launch_linear_tc(const LinearArgs& l, cudaStream_t st) {
   else if (l.out)
     ok = ok && map2(&m.y, l.out, l.N, l.M, 2ll * l.N, 64, 128, kBf);
   if (l.zk.q) ok = ok && map2(&m.z, l.zk.q, l.N, l.M, l.ld, 128, 128, kU8);
+  if (l.res) ok = ok && map2(&m.r, l.res, l.N, l.M, 2ll * l.N, 64, 128, kBf);
   if (l.yk.q) ok = ok && map2(&m.k, l.yk.q, l.N, l.M, l.ld, 128, 128, kU8);
   if (!ok) return cudaErrorInvalidValue;
   if (l.kind == GRAD_W) return go<GRAD_W, INSTANT_ACT_NONE, false>(m, a, st);
