@@ -330,19 +330,21 @@ __global__ void __launch_bounds__((W > 8 ? 32 * W : 256) + 32, CTAS)
     fence_barrier_init();
   }
   pdl_launch_dependents();
-  pdl_wait();
-  for (int c = 8 * threadIdx.x; c < a.C; c += 8 * (kCons + 32)) {
-    float2 g[4];
-    load_pairs<true>(static_cast<const T*>(a.gamma) + c, 8, g);
-    store_pairs<true>(gamma + c, 8, g);
-  }
   __syncthreads();
+  pdl_wait();
   const int warp = threadIdx.x >> 5;
   const int lo = min(p.blocks, static_cast<int>(blockIdx.x) * p.per_cta);
   const int hi = min(p.blocks, lo + p.per_cta);
   if (warp == kWarps) {
     if ((threadIdx.x & 31) == 0) produce<T>(a, p, smem, full, empty, lo, hi);
     return;
+  }
+  // gamma into shared memory under the first copies (the first chunk's barrier
+  // below makes it visible)
+  for (int c = 8 * threadIdx.x; c < a.C; c += 8 * kCons) {
+    float2 g[4];
+    load_pairs<true>(static_cast<const T*>(a.gamma) + c, 8, g);
+    store_pairs<true>(gamma + c, 8, g);
   }
   const int t = threadIdx.x % (32 * W);  // thread within its row
   const int slot = warp / W;
@@ -487,9 +489,9 @@ __global__ void __launch_bounds__((W > 8 ? 32 * W : 256) + 32, CTAS)
 #define INSTANT_STREAM_DISPATCH(C, GO)                   \
   do {                                                   \
     if ((C) <= 256) GO(1, 1, 3);                         \
-    if ((C) <= 512) GO(1, 2, 3);                         \
-    if ((C) <= 1024) GO(2, 2, 3);                        \
-    if ((C) <= 2048) GO(4, 2, 3);                        \
+    if ((C) <= 512) GO(2, 1, 3);                         \
+    if ((C) <= 1024) GO(4, 1, 3);                        \
+    if ((C) <= 2048) GO(8, 1, 3);                        \
     if ((C) <= 4096) GO(8, 2, 3);                        \
     if ((C) <= 8192) GO(8, 4, 2);                        \
     GO(16, 3, 1);                                        \
@@ -541,7 +543,8 @@ template <typename T, int W, int V, int CTAS>
 cudaError_t back_stream_go(const NormBackArgs& a, bool* done, cudaStream_t st) {
   StreamPlan p;
   *done = false;
-  for (int ctas = CTAS; ctas >= 1 && !*done; --ctas)  // fewer CTAs have wider rings *done = stream_plan(p, a, sizeof(T), W, V, ctas, CTAS);
+  for (int ctas = CTAS; ctas >= 1 && !*done; --ctas)  // fewer CTAs an SM have wider rings
+    *done = stream_plan(p, a, sizeof(T), W, V, ctas, CTAS);
   if (!*done) return cudaSuccess;
   auto k = k_rms_norm_back_stream<T, W, V, CTAS>;
   cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(k), p.smem, true);
@@ -602,7 +605,7 @@ cudaError_t launch_rms_norm(const NormArgs& a, bool bf16, cudaStream_t st) {
 // the most CTAs of the backward, each with one share of ggamma: four an SM, no
 // more than there are row slots of the form with the fewest
 int norm_back_parts(int rows, int C) {
-  const int slots = C <= 512 ? 8 : C <= 1024 ? 4 : C <= 2048 ? 2 : 1;
+  const int slots = C <= 256 ? 8 : C <= 512 ? 4 : C <= 1024 ? 2 : 1;
   const long long ctas = (static_cast<long long>(rows) + slots - 1) / slots;
   const long long most = static_cast<long long>(kColSumSMs) * 4;
   return static_cast<int>(ctas < most ? ctas : most);
