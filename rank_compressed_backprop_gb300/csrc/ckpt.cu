@@ -94,9 +94,9 @@ __global__ void __launch_bounds__(kThreads)
 // Column sums in two fixed-order stages (no atomics: the same bits on every
 // call).  Stage 1: a CTA sums `per` rows of 8 x 32 columns, eight warps taking
 // the rows in turn; stage 2 adds the row shares.
-template <typename T>
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads)
-    k_col_sum(const T* __restrict__ x, float* __restrict__ part, int rows, int C, int per, int vec) {
+    k_col_sum(const T* __restrict__ x, float* __restrict__ part, int rows, int C, int per) {
   __shared__ float red[8][kThreads];
   pdl_launch_dependents();
   pdl_wait();
@@ -104,16 +104,21 @@ __global__ void __launch_bounds__(kThreads)
   const int c = blockIdx.x * 256 + 8 * lane;
   const int r0 = blockIdx.y * per;
   const int r1 = min(rows, r0 + per);
-  float acc[8];
+  float2 sum2[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-#pragma unroll 4
-  for (int r = r0 + warp; r < r1; r += 8) {
-    float v[8];
-    load_part<8>(x + static_cast<size_t>(r) * C + c, C - c, vec, v);
+  for (int e = 0; e < 4; ++e) sum2[e] = both(0.f);
+  if (c < C) {
+    const T* p = x + static_cast<size_t>(r0 + warp) * C + c;
+    const size_t step = 8 * static_cast<size_t>(C);
+#pragma unroll 8
+    for (int r = r0 + warp; r < r1; r += 8, p += step) {
+      float2 v[4];
+      load_pairs<VEC>(p, VEC ? 8 : C - c, v);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] += v[e];
+      for (int e = 0; e < 4; ++e) sum2[e] = add2(sum2[e], v[e]);
+    }
   }
+  const float acc[8] = {sum2[0].x, sum2[0].y, sum2[1].x, sum2[1].y, sum2[2].x, sum2[2].y, sum2[3].x, sum2[3].y};
 #pragma unroll
   for (int e = 0; e < 8; ++e) red[warp][8 * lane + e] = acc[e];
   __syncthreads();
@@ -220,11 +225,12 @@ cudaError_t launch_col_sum(const void* x, float* out, float* part, int rows, int
   const int per = (rows + parts - 1) / parts;
   parts = (rows + per - 1) / per;
   const dim3 grid((C + 255) / 256, parts);
-  const cudaError_t e =
-      bf16 ? launch_ex(k_col_sum<uint16_t>, grid, dim3(kThreads), 0, st, 1, pdl_enabled(),
-                       static_cast<const uint16_t*>(x), part, rows, C, per, int(vec))
-           : launch_ex(k_col_sum<float>, grid, dim3(kThreads), 0, st, 1, pdl_enabled(),
-                       static_cast<const float*>(x), part, rows, C, per, int(vec));
+  auto go = [&](auto kernel, auto* p) {
+    return launch_ex(kernel, grid, dim3(kThreads), 0, st, 1, pdl_enabled(), p, part, rows, C, per);
+  };
+  const cudaError_t e = bf16 ? go(k_col_sum<uint16_t, true>, static_cast<const uint16_t*>(x))
+                        : vec ? go(k_col_sum<float, true>, static_cast<const float*>(x))
+                              : go(k_col_sum<float, false>, static_cast<const float*>(x));
   if (e != cudaSuccess) return e;
   return launch_part_sum(part, out, parts, C, accumulate, st);
 }

@@ -529,3 +529,120 @@ def test_mlp_block(torch, dtype, rows, C, H):
     for k, v in first.items():
         assert rel(to_np(getattr(mlp, k)), 2 * to_np(v)) < 1e-5, k
     assert api.device_status() == 0
+
+
+# ---------------------------------------------------------------------------
+# sizes at which every CTA has several tiles, segments or blocks of rows to do;
+# the reference is the same formula in float64 on the GPU
+# ---------------------------------------------------------------------------
+def act64(torch, z, kind):
+    return {"none": lambda: z, "relu": lambda: z.clamp_min(0), "gelu": lambda: z * torch.special.ndtr(z),
+            "silu": lambda: z * torch.sigmoid(z)}[kind]()
+
+
+def slope64(torch, z, kind):
+    if kind == "relu":
+        return (z > 0).double()
+    if kind == "gelu":
+        return torch.special.ndtr(z) + z * torch.exp(-z * z / 2) / (2 * np.pi) ** 0.5
+    s = torch.sigmoid(z)
+    return s + z * s * (1 - s)
+
+
+def far(torch, got, ref, bound):
+    """The largest error in units of its bound (NaN where an element was not written)."""
+    return float(((got.double() - ref).abs() / bound).max())
+
+
+def values64(torch, q, s, C):
+    step = torch.exp2(s.double() - 127).t().repeat_interleave(128, 1)[:, :C]
+    return q[:, :C].double() * step, step
+
+
+@pytest.mark.parametrize("rows,Cx,Cy", [(2600, 328, 2056), (3001, 4104, 1800), (20000, 64, 136)])
+@pytest.mark.parametrize("act,res", [("gelu", True), ("silu", False), ("none", True)])
+def test_products_of_many_tiles(torch, rows, Cx, Cy, act, res):
+    api = _api()
+    gen = torch.Generator("cuda").manual_seed(rows + Cx)
+    rn = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    bf = torch.bfloat16
+    x, w, b = rn(rows, Cx).to(bf), (rn(Cy, Cx) * Cx ** -0.5).to(bf), rn(Cy).to(bf)
+    r = rn(rows, Cy).to(bf) if res else None
+    X, Wt = x.double(), w.double()
+    z = X @ Wt.t() + b.double()
+    y = act64(torch, z, act) + (r.double() if res else 0)
+    ez = (X.abs() @ Wt.abs().t()) * (Cx * 2.0 ** -23) + z.abs() * 2.0 ** -22
+    ey = 1.13 * ez + 2.0 ** -16 * z.abs() * (act != "none") + y.abs() * 2.0 ** -22
+    plain = nan_like(torch, (rows, Cy), bf)
+    api.linear_act(x, w, plain, bias=b, act=act, residual=r)
+    assert far(torch, plain, y, y.abs() * 2.0 ** -8 + ey) <= 1
+    kept = nan_like(torch, (rows, Cy), bf)
+    (zq, zs), (yq, ys) = blank_ckpt(torch, rows, Cy), blank_ckpt(torch, rows, Cy)
+    api.linear_act(x, w, kept, bias=b, act=act, residual=r, zq=zq, zs=zs, yq=yq, ys=ys)
+    assert far(torch, kept, y, y.abs() * 2.0 ** -8 + ey) <= 1
+    for q, s, t, e in ((zq, zs, z, ez), (yq, ys, y, ey)):
+        v, step = values64(torch, q, s, Cy)
+        assert ((v - t).abs() <= 0.5 * step + e).all()
+    # back, from z's checkpoint
+    zv, _ = values64(torch, zq, zs, Cy)
+    g, w2 = (rn(rows, Cx) * 1e-2).to(bf), w.t().contiguous()     # a layer [Cx, Cy] after the activation
+    want = g.double() @ w2.double()
+    eg = (g.double().abs() @ w2.double().abs()) * (Cx * 2.0 ** -23) * 1.13
+    if act != "none":
+        eg = eg + 2.0 ** -16 * want.abs()
+        want = want * slope64(torch, zv, act)
+    if res:
+        want = want + r.double()
+    gx = nan_like(torch, (rows, Cy), bf)
+    api.linear_act_grad(g, w2, gx, act=act, zq=zq, zs=zs, residual=r)
+    assert far(torch, gx, want, want.abs() * (2.0 ** -8 + 2.0 ** -22) + eg) <= 1
+    # weight gradient, from y's checkpoint
+    yv, _ = values64(torch, yq, ys, Cy)
+    want, mag = g.double().t() @ yv, g.double().abs().t() @ yv.abs()
+    gw = nan_like(torch, (Cx, Cy), torch.float32)
+    gb = nan_like(torch, (Cx,), torch.float32)
+    ws = api.ckpt_grad_w_workspace(rows, Cy, Cx, "cuda")
+    api.ckpt_grad_w(g, yq, ys, gw, ws, gb=gb)
+    assert far(torch, gw, want, mag * (rows + 4) * 2.0 ** -23) <= 1
+    assert far(torch, gb, g.double().sum(0), g.double().abs().sum(0) * (rows + 4) * 2.0 ** -23) <= 1
+    first = gw.clone()
+    api.ckpt_grad_w(g, yq, ys, gw, ws, accumulate=True)
+    assert far(torch, gw, 2 * want, 2 * mag * (rows + 4) * 2.0 ** -23 + want.abs() * 2.0 ** -22) <= 1
+    api.ckpt_grad_w(g, yq, ys, gw, ws)
+    assert torch.equal(gw, first)
+    assert api.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,C,res", [
+    (1000000, 64, False), (9001, 448, True), (5003, 1024, False), (3001, 2048, True), (2003, 4096, True),
+    (1501, 8192, False), (1001, 11008, True), (400, 11008, False)])
+def test_norm_backward_of_many_rows(torch, dtype, rows, C, res):
+    """Several blocks of rows a CTA, more rows than it holds factors and scales of."""
+    api = _api()
+    dt = tdt(torch, dtype)
+    gen = torch.Generator("cuda").manual_seed(rows + C)
+    rn = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    h = rn(rows, C).to(dt)
+    gamma = (1 + 0.1 * rn(C)).to(dt)
+    y = torch.empty_like(h)
+    q, s = blank_ckpt(torch, rows, C)
+    r = torch.empty(rows, device="cuda")
+    api.rms_norm(h, gamma, y, q=q, s=s, r=r)
+    gy = (rn(rows, C) * 1e-2).to(dt)
+    bypass = (rn(rows, C) * 1e-2).to(dt) if res else None
+    gx, gg = nan_like(torch, (rows, C), dt), nan_like(torch, (C,), torch.float32)
+    ws = api.rms_norm_backward_workspace(rows, C, "cuda")
+    api.rms_norm_backward(gy, q, s, r, gamma, gx, gg, ws, residual=bypass)
+    u, _ = values64(torch, q, s, C)
+    d = gy.double() * gamma.double()
+    c, ca = (d * u).mean(1, keepdim=True), (d * u).abs().mean(1, keepdim=True)
+    want = r.double()[:, None] * (d - u * c) + (bypass.double() if res else 0)
+    e = r.double()[:, None] * (2.0 ** -21 * (d.abs() + u.abs() * ca) + u.abs() * ca * C * 2.0 ** -23)
+    assert far(torch, gx, want, want.abs() * (ulp(dtype) + 2.0 ** -22) + e) <= 1
+    p = gy.double() * u
+    assert far(torch, gg, p.sum(0), p.abs().sum(0) * (rows + 8) * 2.0 ** -23) <= 1
+    first = gg.clone()
+    api.rms_norm_backward(gy, q, s, r, gamma, gx, gg, ws, residual=bypass)
+    assert torch.equal(gg, first)
+    assert api.device_status() == 0
