@@ -403,6 +403,7 @@ instant_status instant_reconstruction_error(const void* t, const void* Q, const 
  *
  * Sums and statistics are fp32; every output is rounded once.  bf16: widths
  * are multiples of 8; f32: any width.  Tensors of dtype dt unless stated.
+ * Limits: 1 <= rows <= 2^30, 1 <= widths <= 2^24.
  * ------------------------------------------------------------------------ */
 
 /* Activations: gelu is z Phi(z) (the erf form), silu is z / (1 + exp(-z)). */

@@ -18,8 +18,8 @@ bool dtype_ok(instant_dtype dt) { return dt == INSTANT_F32 || dt == INSTANT_BF16
 bool act_ok(int act) { return act >= INSTANT_ACT_NONE && act <= INSTANT_ACT_SILU; }
 instant_status from_cuda(cudaError_t e) { return e == cudaSuccess ? INSTANT_OK : INSTANT_ERR_CUDA; }
 
-// largest extents: a row index and a padded row stay within an int
-bool extent_ok(int rows, int C) { return rows >= 1 && C >= 1 && C <= (1 << 24); }
+// largest extents: row counts rounded up to a tile and padded rows stay within an int
+bool extent_ok(int rows, int C) { return rows >= 1 && rows <= (1 << 30) && C >= 1 && C <= (1 << 24); }
 
 // a checkpoint's two arrays come together
 bool pair_ok(const void* q, const void* s) { return (q == nullptr) == (s == nullptr); }
@@ -47,15 +47,20 @@ bool vec_ok(int C) { return C % 8 == 0; }
 // 20.7 / 25.9, 2048 x 2048 -> 2048 20.1 / 16.3; back 1 x 11008 -> 4096 17.7 / 59.7,
 // 1024 x 4096 -> 1024 14.7 / 25.1; weight gradient over 4096 rows, 1024 x 1024
 // 17.9 / 31.4, over 700 rows, 1792 x 448 11.4 / 10.5.
+double pairs_us(const LinearArgs& a) {
+  const double waves = std::ceil(static_cast<double>(cdiv(a.M, 256)) * cdiv(a.N, 256) / std::max(1, sm_count() / 2));
+  return 4.5 + 0.34 * cdiv(a.K, 64) * waves;
+}
+
+bool runs_on_pairs(const LinearArgs& a) {
+  const int nt = few_rows_tile(a);
+  const double chunk_us = nt == 128 ? 0.28 : nt == 64 ? 0.15 : 0.13;
+  return pairs_us(a) <= 8.0 + chunk_us * cdiv(a.K, 64) * cdiv(a.N, 128) * cdiv(a.M, nt) / sm_count();
+}
+
 cudaError_t launch_linear(const LinearArgs& a, bool bf16, cudaStream_t st) {
   if (!bf16) return launch_linear_simt(a, st);
-  const int nt = few_rows_tile(a);
-  const double nk = cdiv(a.K, 64);
-  const double waves = std::ceil(static_cast<double>(cdiv(a.M, 256)) * cdiv(a.N, 256) / std::max(1, sm_count() / 2));
-  const double pairs_us = 4.5 + 0.34 * nk * waves;
-  const double chunk_us = nt == 128 ? 0.28 : nt == 64 ? 0.15 : 0.13;
-  const double few_us = 8.0 + chunk_us * nk * cdiv(a.N, 128) * cdiv(a.M, nt) / sm_count();
-  return few_us < pairs_us ? launch_linear_few(a, st) : launch_linear_tc(a, st);
+  return runs_on_pairs(a) ? launch_linear_tc(a, st) : launch_linear_few(a, st);
 }
 
 }  // namespace
@@ -226,16 +231,28 @@ instant_status instant_ckpt_grad_w(const void* gy, const void* q, const void* s,
   a.ck = ref(q, s);
   a.ld = ckpt_ld(Cx);
   a.accumulate = accumulate != 0;
+  float* part = gb ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + values_bytes(rows, Cx)) : nullptr;
   cudaError_t e = cudaSuccess;
+  bool side = false;
   if (bf16) {
     // the values are exact in bf16 and every row tile of gw reads them: made once
     a.b = ws;
     e = launch_ckpt_unpack(a.ck, ws, rows, Cx, true, true, st);
+    // gb on the side of a product long enough for the pair kernel's idle warps to
+    // read gy, which they do at about 0.8 TB/s; else in a launch of its own
+    side = gb && runs_on_pairs(a) && 2e-6 * rows * Cy / 0.8 <= pairs_us(a);
+    if (side) {
+      a.sum_part = part;
+      a.sum_parts = std::min(col_sum_parts(rows, Cy), std::max(1, 2 * kColSumSMs / cdiv(Cy, 256)));
+      a.sum_per = cdiv(rows, a.sum_parts);
+      a.sum_parts = cdiv(rows, a.sum_per);
+    }
   }
   if (e == cudaSuccess) e = launch_linear(a, bf16, st);
-  if (e == cudaSuccess && gb)
-    e = launch_col_sum(gy, gb, reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + values_bytes(rows, Cx)),
-                       rows, Cy, accumulate != 0, bf16, vec_ok(Cy), st);
+  if (e == cudaSuccess && side)
+    e = launch_part_sum(part, gb, a.sum_parts, Cy, accumulate != 0, st);
+  else if (e == cudaSuccess && gb)
+    e = launch_col_sum(gy, gb, part, rows, Cy, accumulate != 0, bf16, vec_ok(Cy), st);
   return from_cuda(e);
 }
 

@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kThreads)
 // call).  Stage 1: a CTA sums `per` rows of 8 x 32 columns, eight warps taking
 // the rows in turn; stage 2 adds the row shares.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
     k_col_sum(const T* __restrict__ x, float* __restrict__ part, int rows, int C, int per) {
   __shared__ float red[8][kThreads];
   pdl_launch_dependents();
@@ -110,8 +110,19 @@ __global__ void __launch_bounds__(kThreads)
   if (c < C) {
     const T* p = x + static_cast<size_t>(r0 + warp) * C + c;
     const size_t step = 8 * static_cast<size_t>(C);
-#pragma unroll 8
-    for (int r = r0 + warp; r < r1; r += 8, p += step) {
+    // eight rows' loads under way together
+    constexpr int kBatch = 8;
+    int r = r0 + warp;
+    for (; r + 8 * (kBatch - 1) < r1; r += 8 * kBatch, p += kBatch * step) {
+      float2 v[kBatch][4];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) load_pairs<VEC>(p + j * step, VEC ? 8 : C - c, v[j]);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum2[e] = add2(sum2[e], v[j][e]);
+    }
+    for (; r < r1; r += 8, p += step) {
       float2 v[4];
       load_pairs<VEC>(p, VEC ? 8 : C - c, v);
 #pragma unroll

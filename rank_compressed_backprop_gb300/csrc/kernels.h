@@ -347,6 +347,8 @@ struct LinearArgs {
   int ld;              // code pitch of the checkpoints
   int act;             // instant_act
   int accumulate;      // kind 2
+  float* sum_part;     // kind 2, pair kernel: shares of the column sums of a, or null
+  int sum_parts, sum_per;  // how many, rows of a share
 };
 
 // shares of a column reduction are counted from the SMs of the one device this
@@ -380,6 +382,9 @@ struct TcArgs {
   const uint8_t* cs;
   int ld;              // its code pitch
   int accumulate;
+  const void* sum_src; // [K, M] bf16 whose columns are summed on the side (grad_w), or null
+  float* sum_part;     // [sum_parts, M]
+  int sum_parts, sum_per;
 };
 struct TcMaps {
   CUtensorMap a, b, y, z, k, r;

@@ -509,6 +509,42 @@ __device__ __forceinline__ void epilogue(const TcArgs& a, const CUtensorMap* my,
   if (lead) tma_store_wait_all();
 }
 
+// Column sums of gy on the side (grad_w's bias gradient): the pair kernel's two
+// idle warps stream gy from L2 and HBM at a rate that a long product does not
+// notice.  A share of the rows of 256 columns a warp, eight rows' loads under way.
+__device__ __forceinline__ void side_sums(const TcArgs& a, int w, int warps) {
+  const int lane = threadIdx.x & 31;
+  const int strips = (a.M + 255) / 256;
+  for (int task = w; task < strips * a.sum_parts; task += warps) {
+    const int part = task / strips;
+    const int c = (task - part * strips) * 256 + 8 * lane;
+    if (c >= a.M) continue;
+    const int r1 = min(a.K, (part + 1) * a.sum_per);
+    const uint16_t* p = static_cast<const uint16_t*>(a.sum_src) + static_cast<size_t>(part) * a.sum_per * a.M + c;
+    float2 sum[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] = both(0.f);
+    auto add = [&](uint4 u) {
+      const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        sum[e] = add2(sum[e], make_float2(__uint_as_float(x[e] << 16), __uint_as_float(x[e] & 0xffff0000u)));
+    };
+    int r = part * a.sum_per;
+    for (; r + 8 <= r1; r += 8, p += 8 * static_cast<size_t>(a.M)) {
+      uint4 u[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[j] = *reinterpret_cast<const uint4*>(p + j * static_cast<size_t>(a.M));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) add(u[j]);
+    }
+    for (; r < r1; ++r, p += a.M) add(*reinterpret_cast<const uint4*>(p));
+    float* dst = a.sum_part + static_cast<size_t>(part) * a.M + c;
+    *reinterpret_cast<float4*>(dst) = make_float4(sum[0].x, sum[0].y, sum[1].x, sum[1].y);
+    *reinterpret_cast<float4*>(dst + 4) = make_float4(sum[2].x, sum[2].y, sum[3].x, sum[3].y);
+  }
+}
+
 // ---------------------------------------------------------------------------
 template <int KIND, int ACT, bool KEEP>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
@@ -657,6 +693,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         }
       }
     }
+  } else if (KIND == GRAD_W && warp < 4) {
+    if (a.sum_part) side_sums(a, 2 * blockIdx.x + warp - 2, 2 * gridDim.x);
   } else if (warp >= 4) {
     epilogue<KIND, ACT, KEEP>(a, &map_y, &map_z, &map_k, &map_r, smem, tmem, t_full, in_full,
                               dsmem_addr(t_empty, 0), rank, pair, pairs);
@@ -724,6 +762,10 @@ cudaError_t launch_linear_tc(const LinearArgs& l, cudaStream_t st) {
   a.cs = l.ck.s;
   a.ld = l.ld;
   a.accumulate = l.accumulate;
+  a.sum_src = l.a;
+  a.sum_part = l.sum_part;
+  a.sum_parts = l.sum_parts;
+  a.sum_per = l.sum_per;
   TcMaps m{};
   bool ok;
   if (l.kind == FORWARD) {
