@@ -652,6 +652,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     // ---------------- MMA issuer of the pair ----------------
     if (rank == 0 && lane == 0) {
       constexpr uint32_t idesc = idesc_bf16_f32(BM, BN, A_MN, B_MN);
+      // one thread issues every product: what it computes a chunk is kept to a few
+      // additions (the descriptors' address field counts 16 bytes)
+      const uint32_t base = smem_u32(smem);
+      const uint64_t a_desc0 = A_MN ? sdesc_sw128(base, A_BYTES / 2, 1024) : sdesc_sw128(base, 16, 1024);
+      const uint64_t b_desc0 =
+          B_MN ? sdesc_sw128(base + A_BYTES, B_BYTES / 2, 1024) : sdesc_sw128(base + A_BYTES, 16, 1024);
+      uint64_t a_desc = a_desc0, b_desc = b_desc0;
+      uint32_t d = tmem;
       int s = 0, par = 0, q = 0;
       bool ok = true;
       for (int t = pair; ok && t < tiles; t += pairs) {
@@ -660,6 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           const bool first = left == 0;
           if (first) {
             acc = q & 1;
+            d = tmem + acc * BN;
             left = min(a.seg, a.nk - kc);
             if (q >= 2 && !mbar_wait_cluster(&t_empty[acc], ((q >> 1) - 1) & 1)) {
               raise_fault(FAULT_WAIT_EMPTY);
@@ -674,21 +683,20 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t a_base = smem_u32(smem + s * STAGE);
-          const uint32_t b_base = a_base + A_BYTES;
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) {
-            const uint64_t ad = A_MN ? sdesc_sw128(a_base + kk * 2048, A_BYTES / 2, 1024)
-                                     : sdesc_sw128(a_base + kk * 32, 16, 1024);
-            const uint64_t bd = B_MN ? sdesc_sw128(b_base + kk * 2048, B_BYTES / 2, 1024)
-                                     : sdesc_sw128(b_base + kk * 32, 16, 1024);
-            umma_bf16_pair(tmem + acc * BN, ad, bd, idesc, !(first && kk == 0));
-          }
+          for (int kk = 0; kk < BK / 16; ++kk)
+            umma_bf16_pair(d, a_desc + kk * (A_MN ? 2048 >> 4 : 32 >> 4), b_desc + kk * (B_MN ? 2048 >> 4 : 32 >> 4),
+                           idesc, kk == 0 ? !first : 1u);
           umma_commit_pair(&empty[s]);
           if (--left == 0) umma_commit_pair(&t_full[acc]);
           if (++s == NS) {
             s = 0;
             par ^= 1;
+            a_desc = a_desc0;
+            b_desc = b_desc0;
+          } else {
+            a_desc += STAGE >> 4;
+            b_desc += STAGE >> 4;
           }
         }
       }
