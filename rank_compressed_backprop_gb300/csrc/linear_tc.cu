@@ -83,6 +83,22 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
   return true;
 }
 
+// One lane of a converged warp.  The producer and the MMA issuer run their loops
+// with the whole warp and let one lane issue: what goes into a TMA or tensor-core
+// instruction then is uniform and stays in the warp's uniform registers.  With the
+// loop in one lane's branch each product took some 96 cycles to issue, and four of
+// them with their barrier 640 where the tensor cores need 512.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+// one answer for a converged warp
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity)) != 0;
+}
+
 // barrier among the `count` threads of an epilogue group or pair of groups.  (An
 // id in a register reserves all barriers of the SM; this kernel has it to itself,
 // and its epilogue is one piece of code for all groups.)
@@ -598,22 +614,22 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 
   if (warp == 0) {
     // ---------------- producer ----------------
-    if (lane == 0) {
-      const uint32_t full_leader = dsmem_addr(full, 0);
-      constexpr uint32_t kPairBytes = 2 * STAGE;
-      int s = 0, par = 1, issued = 0;  // slot, and parity of its last release (1: never used)
-      bool ok = true;
-      for (int t = pair; ok && t < tiles; t += pairs) {
-        int m, n;
-        tile_at(a, t, m, n);
-        const int m0 = m * BM + static_cast<int>(rank) * 128;
-        const int n0 = n * BN + static_cast<int>(rank) * 128;
-        for (int kc = 0; kc < a.nk; ++kc) {
-          if (!mbar_wait_cluster(&empty[s], par)) {
-            raise_fault(FAULT_WAIT_EMPTY);
-            ok = false;
-            break;
-          }
+    const uint32_t full_leader = dsmem_addr(full, 0);
+    constexpr uint32_t kPairBytes = 2 * STAGE;
+    int s = 0, par = 1, issued = 0;  // slot, and parity of its last release (1: never used)
+    bool ok = true;
+    for (int t = pair; ok && t < tiles; t += pairs) {
+      int m, n;
+      tile_at(a, t, m, n);
+      const int m0 = m * BM + static_cast<int>(rank) * 128;
+      const int n0 = n * BN + static_cast<int>(rank) * 128;
+      for (int kc = 0; kc < a.nk; ++kc) {
+        if (!mbar_wait_warp(&empty[s], par)) {
+          raise_fault(FAULT_WAIT_EMPTY);
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
           uint8_t* sa = smem + s * STAGE;
           uint8_t* sb = sa + A_BYTES;
           const uint32_t bar = full_leader + 8 * s;
@@ -631,35 +647,33 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           } else {
             tma_load_2d_pair(sb, &map_b, bar, k0, n0);
           }
-          ++issued;
-          if (++s == NS) {
-            s = 0;
-            par ^= 1;
-          }
         }
-      }
-      // the last loads have landed before the CTA goes (the leader counts both CTAs')
-      par ^= 1;
-      for (int k = 0; k < NS && k < issued; ++k) {
-        if (--s < 0) {
-          s = NS - 1;
+        __syncwarp();
+        ++issued;
+        if (++s == NS) {
+          s = 0;
           par ^= 1;
         }
-        if (rank == 0 && !mbar_wait_cluster(&full[s], par)) raise_fault(FAULT_WAIT_FULL);
       }
+    }
+    // the last loads have landed before the CTA goes (the leader counts both CTAs')
+    par ^= 1;
+    for (int k = 0; k < NS && k < issued; ++k) {
+      if (--s < 0) {
+        s = NS - 1;
+        par ^= 1;
+      }
+      if (rank == 0 && !mbar_wait_cluster(&full[s], par)) raise_fault(FAULT_WAIT_FULL);
     }
   } else if (warp == 1) {
     // ---------------- MMA issuer of the pair ----------------
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
       constexpr uint32_t idesc = idesc_bf16_f32(BM, BN, A_MN, B_MN);
-      // one thread issues every product: what it computes a chunk is kept to a few
-      // additions (the descriptors' address field counts 16 bytes)
+      // descriptors' address field counts 16 bytes: slots and steps are additions
       const uint32_t base = smem_u32(smem);
       const uint64_t a_desc0 = A_MN ? sdesc_sw128(base, A_BYTES / 2, 1024) : sdesc_sw128(base, 16, 1024);
       const uint64_t b_desc0 =
           B_MN ? sdesc_sw128(base + A_BYTES, B_BYTES / 2, 1024) : sdesc_sw128(base + A_BYTES, 16, 1024);
-      uint64_t a_desc = a_desc0, b_desc = b_desc0;
-      uint32_t d = tmem;
       int s = 0, par = 0, q = 0;
       bool ok = true;
       for (int t = pair; ok && t < tiles; t += pairs) {
@@ -668,35 +682,35 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           const bool first = left == 0;
           if (first) {
             acc = q & 1;
-            d = tmem + acc * BN;
             left = min(a.seg, a.nk - kc);
-            if (q >= 2 && !mbar_wait_cluster(&t_empty[acc], ((q >> 1) - 1) & 1)) {
+            if (q >= 2 && !mbar_wait_warp(&t_empty[acc], ((q >> 1) - 1) & 1)) {
               raise_fault(FAULT_WAIT_EMPTY);
               ok = false;
               break;
             }
             ++q;
           }
-          if (!mbar_wait_cluster(&full[s], par)) {
+          if (!mbar_wait_warp(&full[s], par)) {
             raise_fault(FAULT_WAIT_FULL);
             ok = false;
             break;
           }
           tc_fence_after();
+          --left;
+          if (elect_one()) {
+            const uint64_t a_desc = a_desc0 + s * (STAGE >> 4);
+            const uint64_t b_desc = b_desc0 + s * (STAGE >> 4);
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk)
-            umma_bf16_pair(d, a_desc + kk * (A_MN ? 2048 >> 4 : 32 >> 4), b_desc + kk * (B_MN ? 2048 >> 4 : 32 >> 4),
-                           idesc, kk == 0 ? !first : 1u);
-          umma_commit_pair(&empty[s]);
-          if (--left == 0) umma_commit_pair(&t_full[acc]);
+            for (int kk = 0; kk < BK / 16; ++kk)
+              umma_bf16_pair(tmem + acc * BN, a_desc + kk * (A_MN ? 2048 >> 4 : 32 >> 4),
+                             b_desc + kk * (B_MN ? 2048 >> 4 : 32 >> 4), idesc, kk == 0 ? !first : 1u);
+            umma_commit_pair(&empty[s]);
+            if (left == 0) umma_commit_pair(&t_full[acc]);
+          }
+          __syncwarp();
           if (++s == NS) {
             s = 0;
             par ^= 1;
-            a_desc = a_desc0;
-            b_desc = b_desc0;
-          } else {
-            a_desc += STAGE >> 4;
-            b_desc += STAGE >> 4;
           }
         }
       }
