@@ -38,18 +38,19 @@ bool vec_ok(int C) { return C % 8 == 0; }
 
 // bf16 products run on the tensor cores, fp32 ones on FFMA.  Of the two tensor-core
 // kernels the one with the smaller estimate runs:
-//   CTA pairs, 256 x 256 tiles      4.5 us + 0.34 us a chunk of 64 and wave of 76 tiles
+//   CTA pairs, 256 x 256 tiles      4.5 us + 0.30 us a chunk of 64 and wave of 76 tiles
 //   split K, 128 x NT tiles         8 us + 0.28 us (NT = 128), 0.15 (64) or 0.13 a
 //                                   chunk, over the SMs
-// which are fits to both kernels timed over 14 shapes of each product.  Measured
-// (rows x K -> N, split K against pairs, us): forward 1 x 4096 -> 11008 16.6 / 42.4,
-// 128 x 4096 -> 11008 21.8 / 26.5, 256 x 4096 -> 11008 33.6 / 26.9, 512 x 4096 -> 4096
-// 20.7 / 25.9, 2048 x 2048 -> 2048 20.1 / 16.3; back 1 x 11008 -> 4096 17.7 / 59.7,
-// 1024 x 4096 -> 1024 14.7 / 25.1; weight gradient over 4096 rows, 1024 x 1024
-// 17.9 / 31.4, over 700 rows, 1792 x 448 11.4 / 10.5.
+// which are fits to both kernels timed over 21 shapes of each product; of these 63 the
+// estimate takes the slower kernel four times, by 14 % at most.  Measured
+// (rows x K -> N, split K against pairs, us): forward 1 x 4096 -> 11008 15.8 / 40.5,
+// 128 x 4096 -> 11008 21.7 / 25.1, 256 x 4096 -> 11008 32.7 / 25.3, 512 x 1024 -> 1024
+// 9.6 / 8.8, 2048 x 2048 -> 2048 19.3 / 14.8; back 33 x 11008 -> 4096 17.5 / 50.3,
+// 1024 x 4096 -> 1024 14.4 / 21.6; weight gradient over 4096 rows, 1024 x 1024
+// 16.8 / 26.1, over 700 rows, 1792 x 448 10.8 / 9.9.
 double pairs_us(const LinearArgs& a) {
   const double waves = std::ceil(static_cast<double>(cdiv(a.M, 256)) * cdiv(a.N, 256) / std::max(1, sm_count() / 2));
-  return 4.5 + 0.34 * cdiv(a.K, 64) * waves;
+  return 4.5 + 0.30 * cdiv(a.K, 64) * waves;
 }
 
 bool runs_on_pairs(const LinearArgs& a) {

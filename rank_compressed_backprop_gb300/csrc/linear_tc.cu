@@ -11,7 +11,7 @@
 // products of a single CTA's 128 x 128 tile; the fp32 accumulator is 128 lanes x
 // 256 columns of each CTA's TMEM, two of them, so that the epilogue of one tile
 // runs under the products of the next.
-//   warp 0     TMA producer: 64-deep chunks of this CTA's A and B halves into a
+//   warp 0     TMA producer (one elected lane issues): 64-deep chunks of this CTA's A and B halves into a
 //              ring; the arrivals of both CTAs are counted on the leader's
 //              barrier (the leader issues the products of both)
 //   warp 1     MMA issuer (the leader's only); commits free the stage in both CTAs
@@ -81,17 +81,6 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
     if (((++n) & 255u) == 0 && global_timer_ns() - t0 > kWaitLimitNs) return false;
   }
   return true;
-}
-
-// One lane of a converged warp.  The producer and the MMA issuer run their loops
-// with the whole warp and let one lane issue: what goes into a TMA or tensor-core
-// instruction then is uniform and stays in the warp's uniform registers.  With the
-// loop in one lane's branch each product took some 96 cycles to issue, and four of
-// them with their barrier 640 where the tensor cores need 512.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-  return p != 0;
 }
 
 // one answer for a converged warp

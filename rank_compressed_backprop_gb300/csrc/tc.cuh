@@ -95,6 +95,17 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
   return true;
 }
 
+// One lane of a converged warp.  A loop that issues TMA or tensor-core instructions
+// runs with the whole warp and lets one lane issue: what goes into the instruction
+// then is uniform and stays in the warp's uniform registers.  With the loop in one
+// lane's branch a tcgen05.mma took some 96 cycles to issue, and four of them with
+// their barrier 640 where the tensor cores need 512 (256 x 256 x 64 on a CTA pair).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // ---------------------------------------------------------------------------
 // signals between the CTAs of one launch: counters in global memory, added to
 // with release semantics after the producer's stores and read with acquire
