@@ -117,10 +117,11 @@ EncodeTiledFn encoder() {
 
 }  // namespace
 
-// tiled map with the 128-byte swizzle (bf16 unless stated); dims/strides
+// tiled map (128-byte swizzle, bf16 unless stated); dims/strides
 // innermost first
 bool instant::make_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
-                       const uint64_t* strides_bytes, const uint32_t* box, CUtensorMapDataType type) {
+                       const uint64_t* strides_bytes, const uint32_t* box, CUtensorMapDataType type,
+                       CUtensorMapSwizzle swizzle) {
   EncodeTiledFn f = encoder();
   if (!f) return false;
   cuuint64_t d[5], s[5];
@@ -132,7 +133,7 @@ bool instant::make_map(CUtensorMap* m, const void* base, int rank, const uint64_
     if (i < rank - 1) s[i] = strides_bytes[i];
   }
   return f(m, type, rank, const_cast<void*>(base), d, s, b, e,
-           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

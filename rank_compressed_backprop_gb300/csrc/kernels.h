@@ -377,10 +377,9 @@ struct TcArgs {
   const void* bias;    // [N] bf16 or null (grad_w: column scale)
   const void* res;     // [M, N] bf16 or null
   const void* out;     // null: no y
-  uint8_t *zs, *ys;    // scale bytes of the checkpoints written (null: none)
-  const int8_t* cq;    // checkpoint read
-  const uint8_t* cs;
-  int ld;              // its code pitch
+  CkptRef zk, yk;      // checkpoints written (null: none)
+  CkptRef ck;          // checkpoint read
+  int ld;              // code pitch of the checkpoints
   int accumulate;
   const void* sum_src; // [K, M] bf16 whose columns are summed on the side (grad_w), or null
   float* sum_part;     // [sum_parts, M]
@@ -405,10 +404,11 @@ struct FewArgs {
 int few_rows_tile(const LinearArgs& a);  // its row tile for this product: 16, 32, 64 or 128
 cudaError_t launch_linear_few(const LinearArgs& a, cudaStream_t st);
 
-// tiled tensor map with the 128-byte swizzle; dims/strides innermost first
+// tiled tensor map, by default with the 128-byte swizzle; dims/strides innermost first
 bool make_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
               const uint64_t* strides_bytes, const uint32_t* box,
-              CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
+              CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+              CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
 
 // host-side count of kernel launches issued by the library
 void count_launches(unsigned int n);

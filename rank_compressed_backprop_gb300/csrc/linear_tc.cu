@@ -20,7 +20,9 @@
 //              two warps on each scheduler, whose latencies showed: 12544 x 448 ->
 //              1792 with gelu and both checkpoints 53 us.)  Two groups share the 128
 //              columns of a checkpoint group and exchange the scale byte of their
-//              halves' largest magnitudes: the larger byte is the group's
+//              halves' largest magnitudes: the larger byte is the group's.
+//              12544 x 448 -> 1792 with gelu and both checkpoints 36 us, without
+//              them 25
 // The tensor cores' fp32 accumulation cuts low bits at every step, which adds
 // up over a long contraction (6e-6 of a 8192-token weight gradient).  Where the
 // output shows it (fp32 gradients, and checkpoints, whose codes flip) the
@@ -32,6 +34,8 @@
 // plain loads touches 32 lines an access and doubled the time of 12544 x 448 ->
 // 1792 -- and the results leave through the same boxes by TMA stores, which also clip ragged edges; accumulation into gw is the TMA's own add
 // (each element is added to once).
+#include <utility>
+
 #include "ckpt.cuh"
 
 namespace instant {
@@ -46,17 +50,18 @@ constexpr uint32_t STAGE = A_BYTES + B_BYTES;
 constexpr uint32_t BOX = 128 * 128;          // staging box: 128 rows x 128 bytes
 constexpr int kThreads = 640;
 // Shared memory: the ring of chunks, the boxes through which epilogue operands
-// come in and results go out (one of 64 columns for each group; where checkpoints
-// are written a pair of groups has one of codes besides, at the cost of a stage),
-// the tile's bias or column scale, scale bytes under exchange
+// come in and results go out (64 columns of 128 rows for each group; where
+// checkpoints are written, of 32 rows for each warp), the tile's bias or column
+// scale (a copy for each warp there, which takes a stage), scale bytes under exchange
 template <bool KEEP>
 struct Lay {
   static constexpr int ns = KEEP ? 4 : 5;
+  static constexpr int ins = KEEP ? 16 : 4;
   static constexpr uint32_t box = ns * STAGE;
-  static constexpr uint32_t vec = box + (KEEP ? 6 : 4) * BOX;  // 4 groups x 64 floats
-  static constexpr uint32_t code = vec + 1024;                  // 2 pairs x 2 halves x 128 bytes
-  static constexpr uint32_t bar = code + 512;
-  static constexpr uint32_t total = bar + 160;
+  static constexpr uint32_t vec = box + 4 * BOX;
+  static constexpr uint32_t code = vec + (KEEP ? 16 * 32 * 64 : 4 * 64 * 4);
+  static constexpr uint32_t bar = code + (KEEP ? 8 * 128 : 0);  // 8 pairs of warps x z, y x 2 halves x 32 bytes
+  static constexpr uint32_t total = bar + 8 * (2 * ns + 4 + ins + 1);
 };
 
 // ---- cluster-scope barriers and pair-wide tensor-core operations ----------
@@ -296,28 +301,157 @@ __device__ __forceinline__ void make_codes(uint4 (&q)[4], uint32_t code, const f
   }
 }
 
-template <int KIND, int ACT, bool KEEP>
-__device__ __forceinline__ void epilogue(const TcArgs& a, const CUtensorMap* my, const CUtensorMap* mz,
-                                         const CUtensorMap* mk, const CUtensorMap* mr, uint8_t* smem,
+// One accumulator segment after the other into v, 64 columns of a row a thread.
+// `release(acc)` hands the accumulator back; ids and count as in mbar_wait_group.
+template <typename Release>
+__device__ __forceinline__ bool sum_segments(const TcArgs& a, uint32_t tbase, uint64_t* t_full, int id, int count,
+                                             int& q, float2* v, const Release& release) {
+  for (int k0 = 0; k0 < a.nk; k0 += a.seg, ++q) {
+    const int acc = q & 1;
+    if (!mbar_wait_group(&t_full[acc], (q >> 1) & 1, id, count)) return false;
+    tc_fence_after();
+    if (k0 == 0) {
+      tmem_read<64>(tbase + acc * BN, v);
+    } else {
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        float w[16];
+        tmem_ld16(tbase + acc * BN + 16 * h, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[8 * h + j] = add2(v[8 * h + j], make_float2(w[2 * j], w[2 * j + 1]));
+      }
+    }
+    release(acc);
+  }
+  return true;
+}
+
+// Forward with checkpoints.  A warp takes 32 rows x 64 columns through on its own:
+// its own box for the residual and y, its own TMA operations; the codes, 64 bytes of
+// a row, through a second box (by plain stores, a row a thread, they took 4 us more at
+// 12544 x 448 -> 1792).  It meets only the warp with the other half
+// of its rows' checkpoint groups, twice, to exchange the bytes of their largest
+// magnitudes.  (With a pair of groups, 256 threads, in step through boxes of 128
+// rows the barriers were a third of the epilogue, and 12544 x 448 -> 1792 with gelu and
+// both checkpoints took 43 us instead of 36.)
+template <int ACT>
+__device__ __forceinline__ void epilogue_keep(const TcArgs& a, const CUtensorMap* my, const CUtensorMap* mz,
+                                              const CUtensorMap* mk, const CUtensorMap* mr, uint8_t* smem, uint32_t tmem,
+                                              uint64_t* t_full, uint64_t* in_full, uint32_t t_empty_leader,
+                                              uint32_t rank, int pair, int pairs) {
+  using L = Lay<true>;
+  const int warp = (threadIdx.x >> 5) - 4, lane = threadIdx.x & 31;
+  const int group = warp >> 2, quarter = warp & 3;  // 64 columns, 32 TMEM lanes
+  const int half = group & 1;
+  const int mate = (group >> 1) * 4 + quarter;      // the two halves of 32 rows' groups
+  const int id = 1 + mate, count = 64;
+  uint8_t* box = smem + L::box + warp * (32 * 128);
+  uint8_t* cbox = smem + L::vec + warp * (32 * 64);  // codes; before them the bias
+  float* vec = reinterpret_cast<float*>(cbox);
+  uint8_t* zcode = smem + L::code + 128 * mate;  // [half][32]
+  uint8_t* ycode = zcode + 64;
+  in_full += warp;
+  int in_par = 0, q = 0;
+  const int tiles = a.mt * a.nt;
+  const uint32_t tbase = tmem + 64 * group + (static_cast<uint32_t>(quarter * 32) << 16);
+  auto release = [&](int acc) {  // the accumulator may be overwritten
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_at(t_empty_leader + 8 * acc);
+  };
+  for (int t = pair; t < tiles; t += pairs) {
+    int m, n;
+    tile_at(a, t, m, n);
+    const int row0 = m * BM + static_cast<int>(rank) * 128 + 32 * quarter;
+    const int row = row0 + lane;
+    const int col = n * BN + 64 * group;
+    const bool on = row < a.M && col < a.N;
+    const size_t scale_at = static_cast<size_t>(col / kCkptGroup) * a.M + row;
+    if (lane == 0) {
+      tma_store_wait_read<0>();  // the boxes are free
+      if (a.res) {
+        mbar_arrive_expect_tx(in_full, 32 * 128);
+        tma_load_2d(box, mr, in_full, col, row0);
+      }
+    }
+    __syncwarp();
+    if (a.bias) {
+      const int c = col + 2 * lane;  // N is even
+      float2 b = both(0.f);
+      if (c < a.N) {
+        const uint32_t u = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.bias) + c);
+        b = make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+      }
+      *reinterpret_cast<float2*>(vec + 2 * lane) = b;
+    }
+    float2 v[32];
+    if (!sum_segments(a, tbase, t_full, id, count, q, v, release)) {
+      raise_fault(FAULT_WAIT_DONE);
+      break;
+    }
+    if (a.bias) {
+      with_row_vector<32, false>(vec, v);
+      __syncwarp();  // codes come over it
+    }
+    auto keep = [&](const CkptRef& k, const CUtensorMap* map, uint8_t* bytes, bool second) {
+      uint32_t code = half_code(v);
+      bytes[32 * half + lane] = static_cast<uint8_t>(code);
+      group_barrier(id, count);
+      code = max(code, static_cast<uint32_t>(bytes[32 * (half ^ 1) + lane]));
+      uint4 codes[4];
+      make_codes(codes, code, v);
+      if (half == 0 && on) k.s[scale_at] = static_cast<uint8_t>(code);
+      if (second) {
+        if (lane == 0) tma_store_wait_read<1>();  // z's codes have left, y may not
+        __syncwarp();
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        *reinterpret_cast<uint4*>(cbox + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = codes[c];
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (row0 < a.M && col < a.N) tma_store_2d(map, cbox, col, row0);
+        tma_store_commit();
+      }
+    };
+    if (a.zk.q) keep(a.zk, mz, zcode, false);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = act_fast<ACT>(v[j]);
+    if (a.res) {
+      if (!mbar_wait(in_full, in_par)) raise_fault(FAULT_WAIT_FULL);
+      in_par ^= 1;
+      add_bf16<32>(box, lane, 0, v);
+    }
+    if (a.out) {
+      put_bf16<32>(box, lane, 0, v);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (row0 < a.M && col < a.N) tma_store_2d(my, box, col, row0);
+        tma_store_commit();
+      }
+    }
+    if (a.yk.q) keep(a.yk, mk, ycode, true);
+  }
+  if (lane == 0) tma_store_wait_all();
+}
+
+template <int KIND, int ACT>
+__device__ __forceinline__ void epilogue(const TcArgs& a, const CUtensorMap* my, const CUtensorMap* mr, uint8_t* smem,
                                          uint32_t tmem, uint64_t* t_full, uint64_t* in_full,
                                          uint32_t t_empty_leader, uint32_t rank, int pair, int pairs) {
-  constexpr bool PAIRS = KEEP;  // two groups share the 128 columns of a checkpoint's groups
   constexpr bool CODES = KIND == BACK && ACT != INSTANT_ACT_NONE;
-  using L = Lay<KEEP>;
+  using L = Lay<false>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = (warp - 4) >> 2;        // 64 columns each
   const int r = (warp & 3) * 32 + lane;     // TMEM lane
-  const int half = group & 1;               // of a pair
-  const int id = PAIRS ? 5 + (group >> 1) : 1 + group, count = PAIRS ? 256 : 128;
-  const bool lead = r == 0 && (!PAIRS || half == 0);  // issues loads and stores
-  // a pair's boxes: codes, y's first half, y's second; a group's: y
-  uint8_t* boxes = smem + L::box + (PAIRS ? (group >> 1) * 3 : group) * BOX;
-  uint8_t* ybox = PAIRS ? boxes + (1 + half) * BOX : boxes;
-  in_full += PAIRS ? group >> 1 : group;    // epilogue operands arrived
+  const int id = 1 + group, count = 128;
+  const bool lead = r == 0;                 // issues loads and stores
+  uint8_t* box = smem + L::box + group * BOX;
+  in_full += group;                         // epilogue operands arrived
   int in_par = 0;
   float* vec = reinterpret_cast<float*>(smem + L::vec) + 64 * group;
-  uint8_t* zcode = smem + L::code + 256 * (group >> 1);                                 // [half][row]
-  uint8_t* ycode = reinterpret_cast<uint8_t*>(smem + L::vec) + 512 * (group >> 1);      // over vec
   const int tiles = a.mt * a.nt;
   const uint32_t tbase = tmem + 64 * group + (static_cast<uint32_t>((warp & 3) * 32) << 16);
   int q = 0;    // accumulators read so far
@@ -332,129 +466,44 @@ __device__ __forceinline__ void epilogue(const TcArgs& a, const CUtensorMap* my,
     const int row0 = m * BM + static_cast<int>(rank) * 128;
     const int col = n * BN + 64 * group;
     const bool on = row0 + r < a.M;
-    // the columns' bias or scale, read by the whole group (or, as ycode, pair)
-    // before a barrier that all pass before the next tile, and written before the
-    // wait below
-    const int col0 = PAIRS ? col - 64 * half : col;  // first column of the pair or group
-    const bool stores = col0 < a.N && row0 < a.M;
-    auto wait_in = [&]() {
-      if (!mbar_wait(in_full, in_par)) raise_fault(FAULT_WAIT_FULL);
-      in_par ^= 1;
-    };
-    if (lead) tma_store_wait_read<0>();  // the boxes are free
+    const bool stores = col < a.N && row0 < a.M;
+    if (lead) tma_store_wait_read<0>();  // the box is free
     if (lead && a.res) {
-      mbar_arrive_expect_tx(in_full, PAIRS ? 2 * BOX : BOX);
-      tma_load_2d(PAIRS ? boxes + BOX : boxes, mr, in_full, col0, row0);
-      if (PAIRS) tma_load_2d(boxes + 2 * BOX, mr, in_full, col0 + 64, row0);
+      mbar_arrive_expect_tx(in_full, BOX);
+      tma_load_2d(box, mr, in_full, col, row0);
     }
+    // the columns' bias or scale, read by the whole group before a barrier that all
+    // pass before the next tile, and written before the wait below
     if (a.bias && KIND != BACK && r < 64)
       vec[r] = col + r < a.N ? bf16_to_f32(static_cast<const uint16_t*>(a.bias)[col + r]) : 0.f;
-    if (KEEP || KIND == GRAD_W) {
+    if (KIND == GRAD_W) {
       float2 v[32];
-      bool ok = true;
-      for (int k0 = 0; k0 < a.nk; k0 += a.seg, ++q) {
-        const int acc = q & 1;
-        ok = mbar_wait_group(&t_full[acc], (q >> 1) & 1, id, count);
-        if (!ok) break;
-        tc_fence_after();
-        if (k0 == 0) {
-          tmem_read<64>(tbase + acc * BN, v);
-        } else {
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            float w[16];
-            tmem_ld16(tbase + acc * BN + 16 * h, w);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              v[8 * h + j] = add2(v[8 * h + j], make_float2(w[2 * j], w[2 * j + 1]));
-          }
-        }
-        release(acc);
-      }
-      if (!ok) {
+      if (!sum_segments(a, tbase, t_full, id, count, q, v, release)) {
         raise_fault(FAULT_WAIT_DONE);
         break;
       }
-      if (a.bias) with_row_vector<32, KIND == GRAD_W>(vec, v);
-      if (KIND == GRAD_W) {
-        // two boxes of 32 fp32 columns
+      if (a.bias) with_row_vector<32, true>(vec, v);
+      // two boxes of 32 fp32 columns
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (h == 1) {
-            if (lead) tma_store_wait_read<0>();
-            group_barrier(id, count);
-          }
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const float2* w = v + 16 * h + 2 * c;
-            put_piece(boxes, r, c, make_uint4(__float_as_uint(w[0].x), __float_as_uint(w[0].y),
-                                              __float_as_uint(w[1].x), __float_as_uint(w[1].y)));
-          }
-          fence_proxy_async_smem();
+      for (int h = 0; h < 2; ++h) {
+        if (h == 1) {
+          if (lead) tma_store_wait_read<0>();
           group_barrier(id, count);
-          if (lead) {
-            const int c0 = col + 32 * h;
-            if (c0 < a.N && row0 < a.M) {
-              if (a.accumulate) tma_add_2d(my, boxes, c0, row0);
-              else tma_store_2d(my, boxes, c0, row0);
-            }
-            tma_store_commit();
-          }
         }
-        continue;
-      }
-      // Forward with checkpoints: z's codes go out through box 0, y's two halves
-      // through boxes 1 and 2, then y's codes through box 0 again, made in registers
-      // while z's are read out.  Columns past the tensor's end hold zeros.
-      const size_t at = static_cast<size_t>(col0 / kCkptGroup) * a.M + row0 + r;
-      uint32_t code = 0;
-      uint4 codes[4];
-      if (a.zs) {
-        code = half_code(v);
-        zcode[128 * half + r] = static_cast<uint8_t>(code);
-      }
-      group_barrier(id, count);  // scale bytes of z there, boxes free
-      if (a.zs) {
-        code = max(code, static_cast<uint32_t>(zcode[128 * (half ^ 1) + r]));
-        make_codes(codes, code, v);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) put_piece(boxes, r, 4 * half + c, codes[c]);
-        if (half == 0 && on && col0 < a.N) a.zs[at] = static_cast<uint8_t>(code);
-      }
-#pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = act_fast<ACT>(v[j]);
-      if (a.res) {
-        wait_in();
-        add_bf16<32>(ybox, r, 0, v);
-      }
-      if (a.ys) {
-        code = half_code(v);
-        ycode[128 * half + r] = static_cast<uint8_t>(code);
-      }
-      if (a.out) put_bf16<32>(ybox, r, 0, v);
-      fence_proxy_async_smem();
-      group_barrier(id, count);  // z's codes, y and its scale bytes there
-      if (lead) {
-        if (a.zs && stores) tma_store_2d(mz, boxes, col0, row0);
-        tma_store_commit();
-        if (a.out && stores) {
-          tma_store_2d(my, boxes + BOX, col0, row0);
-          if (col0 + 64 < a.N) tma_store_2d(my, boxes + 2 * BOX, col0 + 64, row0);
+        for (int c = 0; c < 8; ++c) {
+          const float2* w = v + 16 * h + 2 * c;
+          put_piece(box, r, c, make_uint4(__float_as_uint(w[0].x), __float_as_uint(w[0].y),
+                                          __float_as_uint(w[1].x), __float_as_uint(w[1].y)));
         }
-        tma_store_commit();
-      }
-      if (a.ys) {
-        code = max(code, static_cast<uint32_t>(ycode[128 * (half ^ 1) + r]));
-        make_codes(codes, code, v);
-        if (half == 0 && on && col0 < a.N) a.ys[at] = static_cast<uint8_t>(code);
-        if (lead) tma_store_wait_read<1>();
-        group_barrier(id, count);  // box 0 free again
-#pragma unroll
-        for (int c = 0; c < 4; ++c) put_piece(boxes, r, 4 * half + c, codes[c]);
         fence_proxy_async_smem();
         group_barrier(id, count);
         if (lead) {
-          if (stores) tma_store_2d(mk, boxes, col0, row0);
+          const int c0 = col + 32 * h;
+          if (c0 < a.N && row0 < a.M) {
+            if (a.accumulate) tma_add_2d(my, box, c0, row0);
+            else tma_store_2d(my, box, c0, row0);
+          }
           tma_store_commit();
         }
       }
@@ -464,20 +513,23 @@ __device__ __forceinline__ void epilogue(const TcArgs& a, const CUtensorMap* my,
       uint4 codes[4];
       float scale = 0.f;
       if (CODES) {
-        const int8_t* p = a.cq + static_cast<size_t>(on ? row0 + r : 0) * a.ld + col;
+        const int8_t* p = a.ck.q + static_cast<size_t>(on ? row0 + r : 0) * a.ld + col;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           codes[c] = on && col + 16 * c < a.N ? *reinterpret_cast<const uint4*>(p + 16 * c)
                                               : make_uint4(0u, 0u, 0u, 0u);
         if (on && col < a.N)
-          scale = ckpt_scale(a.cs[static_cast<size_t>(col / kCkptGroup) * a.M + row0 + r]);
+          scale = ckpt_scale(a.ck.s[static_cast<size_t>(col / kCkptGroup) * a.M + row0 + r]);
       }
       const int acc = q & 1;
       if (!mbar_wait_group(&t_full[acc], (q >> 1) & 1, id, count)) {
         raise_fault(FAULT_WAIT_DONE);
         break;
       }
-      if (a.res) wait_in();
+      if (a.res) {
+        if (!mbar_wait(in_full, in_par)) raise_fault(FAULT_WAIT_FULL);
+        in_par ^= 1;
+      }
       tc_fence_after();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {  // 32 columns at a time
@@ -499,14 +551,14 @@ __device__ __forceinline__ void epilogue(const TcArgs& a, const CUtensorMap* my,
             for (int e = 0; e < 8; ++e) v[8 * c + e] = mul2(v[8 * c + e], act_slope_fast<ACT>(z[e]));
           }
         }
-        if (a.res) add_bf16<16>(ybox, r, 4 * h, v);
-        put_bf16<16>(ybox, r, 4 * h, v);
+        if (a.res) add_bf16<16>(box, r, 4 * h, v);
+        put_bf16<16>(box, r, 4 * h, v);
       }
       ++q;
       fence_proxy_async_smem();
       group_barrier(id, count);
       if (lead) {
-        if (stores) tma_store_2d(my, boxes, col0, row0);
+        if (stores) tma_store_2d(my, box, col, row0);
         tma_store_commit();
       }
     }
@@ -566,8 +618,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   uint64_t* empty = full + NS;       // each CTA's: products of a chunk done
   uint64_t* t_full = empty + NS;     // [2] each CTA's: accumulator done
   uint64_t* t_empty = t_full + 2;    // [2] leader's: accumulator read
-  uint64_t* in_full = t_empty + 2;   // [4] each CTA's: epilogue operands arrived
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(in_full + 4);
+  uint64_t* in_full = t_empty + 2;   // [L::ins] each CTA's: epilogue operands arrived
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(in_full + L::ins);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -584,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       mbar_init(&t_full[i], 1);
       mbar_init(&t_empty[i], 32);  // epilogue warps of both CTAs
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&in_full[i], 1);
+    for (int i = 0; i < L::ins; ++i) mbar_init(&in_full[i], 1);
     fence_barrier_init();
     prefetch_tmap(&map_a);
     prefetch_tmap(&map_b);
@@ -707,8 +759,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   } else if (KIND == GRAD_W && warp < 4) {
     if (a.sum_part) side_sums(a, 2 * blockIdx.x + warp - 2, 2 * gridDim.x);
   } else if (warp >= 4) {
-    epilogue<KIND, ACT, KEEP>(a, &map_y, &map_z, &map_k, &map_r, smem, tmem, t_full, in_full,
-                              dsmem_addr(t_empty, 0), rank, pair, pairs);
+    const uint32_t t_empty_leader = dsmem_addr(t_empty, 0);
+    if constexpr (KEEP)
+      epilogue_keep<ACT>(a, &map_y, &map_z, &map_k, &map_r, smem, tmem, t_full, in_full, t_empty_leader, rank, pair,
+                         pairs);
+    else
+      epilogue<KIND, ACT>(a, &map_y, &map_r, smem, tmem, t_full, in_full, t_empty_leader, rank, pair, pairs);
   }
   __syncwarp();
   tc_fence_before();
@@ -739,11 +795,12 @@ cudaError_t go_act(int act, const TcMaps& m, const TcArgs& a, cudaStream_t st) {
 }
 
 bool map2(CUtensorMap* m, const void* p, long long inner, long long outer, long long pitch_bytes,
-          int box_inner, int box_outer, CUtensorMapDataType type) {
+          int box_inner, int box_outer, CUtensorMapDataType type,
+          CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   const uint64_t d[2] = {static_cast<uint64_t>(inner), static_cast<uint64_t>(outer)};
   const uint64_t s[1] = {static_cast<uint64_t>(pitch_bytes)};
   const uint32_t b[2] = {static_cast<uint32_t>(box_inner), static_cast<uint32_t>(box_outer)};
-  return make_map(m, p, 2, d, s, b, type);
+  return make_map(m, p, 2, d, s, b, type, swizzle);
 }
 
 }  // namespace
@@ -752,7 +809,6 @@ bool map2(CUtensorMap* m, const void* p, long long inner, long long outer, long 
 // and alignment.
 cudaError_t launch_linear_tc(const LinearArgs& l, cudaStream_t st) {
   constexpr CUtensorMapDataType kBf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  constexpr CUtensorMapDataType kU8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   TcArgs a{};
   a.M = l.M;
   a.N = l.N;
@@ -767,10 +823,9 @@ cudaError_t launch_linear_tc(const LinearArgs& l, cudaStream_t st) {
   a.bias = l.bias;
   a.res = l.res;
   a.out = l.out;
-  a.zs = l.zk.s;
-  a.ys = l.yk.s;
-  a.cq = l.ck.q;
-  a.cs = l.ck.s;
+  a.zk = l.zk;
+  a.yk = l.yk;
+  a.ck = l.ck;
   a.ld = l.ld;
   a.accumulate = l.accumulate;
   a.sum_src = l.a;
@@ -789,10 +844,10 @@ cudaError_t launch_linear_tc(const LinearArgs& l, cudaStream_t st) {
   if (l.kind == GRAD_W)
     ok = ok && map2(&m.y, l.out, l.N, l.M, 4ll * l.N, 32, 128, CU_TENSOR_MAP_DATA_TYPE_FLOAT32);
   else if (l.out)
-    ok = ok && map2(&m.y, l.out, l.N, l.M, 2ll * l.N, 64, 128, kBf);
-  if (l.zk.q) ok = ok && map2(&m.z, l.zk.q, l.N, l.M, l.ld, 128, 128, kU8);
-  if (l.res) ok = ok && map2(&m.r, l.res, l.N, l.M, 2ll * l.N, 64, 128, kBf);
-  if (l.yk.q) ok = ok && map2(&m.k, l.yk.q, l.N, l.M, l.ld, 128, 128, kU8);
+    ok = ok && map2(&m.y, l.out, l.N, l.M, 2ll * l.N, 64, keep ? 32 : 128, kBf);
+  for (const auto& [map, q] : {std::make_pair(&m.z, l.zk.q), std::make_pair(&m.k, l.yk.q)})
+    if (q) ok = ok && map2(map, q, l.N, l.M, l.ld, 64, 32, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_64B);
+  if (l.res) ok = ok && map2(&m.r, l.res, l.N, l.M, 2ll * l.N, 64, keep ? 32 : 128, kBf);
   if (!ok) return cudaErrorInvalidValue;
   if (l.kind == GRAD_W) return go<GRAD_W, INSTANT_ACT_NONE, false>(m, a, st);
   if (l.kind == BACK) return go_act<BACK, false>(l.act, m, a, st);
