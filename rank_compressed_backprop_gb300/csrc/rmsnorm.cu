@@ -249,15 +249,25 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
+// barrier of the W warps that share a row, which are row slot `slot` of eight warps
+// (ids in the instructions: one in a register would reserve all of them)
+template <int W>
+__device__ __forceinline__ void row_barrier(int slot) {
+  if (W >= 8 || slot == 0) named_barrier<2>(32 * W);
+  else if (slot == 1) named_barrier<3>(32 * W);
+  else if (slot == 2) named_barrier<4>(32 * W);
+  else named_barrier<5>(32 * W);
+}
+
 // sum over the W warps of a row; `red` is a buffer of 32 floats, another one at
 // the next call
-template <int W, int THREADS>
+template <int W>
 __device__ __forceinline__ float row_sum_stream(float v, float* red, int warp) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   if (W == 1) return v;
   if ((threadIdx.x & 31) == 0) red[warp] = v;
-  named_barrier<1>(THREADS);
+  row_barrier<W>(warp / W);
   const float* p = red + warp / W * W;
   if (W == 2) return p[0] + p[1];
   float4 sum = *reinterpret_cast<const float4*>(p);
@@ -306,12 +316,18 @@ __device__ __forceinline__ void produce(const NormBackArgs& a, const StreamPlan&
   }
 }
 
-// Streaming backward.  Only the shares of ggamma live in registers across a row:
-// u and d are made twice, before and after the row's sum, from what the ring holds,
-// so that the registers allow as many CTAs as the shared memory.  A CTA's rows are
-// neighbours: their factors and scale bytes are fetched for `chunk` rows at once (a
-// plain load a row would wait behind the copies that are under way: 5 us).
-template <typename T, int W, int V, int CTAS>
+// Streaming backward.  A CTA's rows are neighbours: their factors and scale bytes are
+// fetched for `chunk` rows at once, and the copies start when the first chunk is there
+// (a plain load waits behind the copies that are under way: 5 us).  A row's two passes
+// read the ring, or what the registers hold.  The warps of a row meet at a barrier of
+// their own.  Beyond the bytes' floor it takes about 10 us whatever the size: 3 for the
+// second kernel, the rest launch, first loads and copies, and the sums at the end.
+//
+// What a consumer thread keeps in registers: its columns' shares of ggamma, gamma too,
+// or the row's values too between its two passes
+enum { HOLD_SUMS, HOLD_GAMMA, HOLD_ROW };
+
+template <typename T, int W, int V, int CTAS, int HOLD>
 __global__ void __launch_bounds__((W > 8 ? 32 * W : 256) + 32, CTAS)
     k_rms_norm_back_stream(NormBackArgs a, StreamPlan p) {
   constexpr int kWarps = W > 8 ? W : 8;
@@ -336,15 +352,9 @@ __global__ void __launch_bounds__((W > 8 ? 32 * W : 256) + 32, CTAS)
   const int lo = min(p.blocks, static_cast<int>(blockIdx.x) * p.per_cta);
   const int hi = min(p.blocks, lo + p.per_cta);
   if (warp == kWarps) {
+    if (lo < hi) named_barrier<6>(kCons + 32);  // the first chunk is there
     if ((threadIdx.x & 31) == 0) produce<T>(a, p, smem, full, empty, lo, hi);
     return;
-  }
-  // gamma into shared memory under the first copies (the first chunk's barrier
-  // below makes it visible)
-  for (int c = 8 * threadIdx.x; c < a.C; c += 8 * kCons) {
-    float2 g[4];
-    load_pairs<true>(static_cast<const T*>(a.gamma) + c, 8, g);
-    store_pairs<true>(gamma + c, 8, g);
   }
   const int t = threadIdx.x % (32 * W);  // thread within its row
   const int slot = warp / W;
@@ -362,6 +372,18 @@ __global__ void __launch_bounds__((W > 8 ? 32 * W : 256) + 32, CTAS)
     in[v] = c < a.C;
     col[v] = in[v] ? c : 0;
   }
+  constexpr bool kGamma = HOLD != HOLD_SUMS, kHold = HOLD == HOLD_ROW;
+  float2 gm[kGamma ? V : 1][4];
+  if (kGamma) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) load_pairs<true>(static_cast<const T*>(a.gamma) + col[v], 8, gm[v]);
+  } else {  // into shared memory; the first chunk's barrier makes it visible
+    for (int c = 8 * threadIdx.x; c < a.C; c += 8 * kCons) {
+      float2 g[4];
+      load_pairs<true>(static_cast<const T*>(a.gamma) + c, 8, g);
+      store_pairs<true>(gamma + c, 8, g);
+    }
+  }
   int s = 0, par = 0, it = 0;
   bool ok = true;  // after a wait that ran out no more are made: the loops stay in step
   float* sr = reinterpret_cast<float*>(smem + p.r_off);  // factors of the chunk's rows
@@ -377,7 +399,8 @@ __global__ void __launch_bounds__((W > 8 ? 32 * W : 256) + 32, CTAS)
       for (int g = warp; g < groups; g += kWarps)
         for (int i = threadIdx.x & 31; i < n; i += 32)
           ssc[g * p.chunk + i] = a.k.s[static_cast<size_t>(g) * a.rows + chunk0 + i];
-      named_barrier<1>(kCons);
+      if (b == lo) named_barrier<6>(kCons + 32);
+      else named_barrier<1>(kCons);
     }
     if (ok && !mbar_wait(&full[s], par)) {
       raise_fault(FAULT_WAIT_FULL);
@@ -398,25 +421,30 @@ __global__ void __launch_bounds__((W > 8 ? 32 * W : 256) + 32, CTAS)
       // a vector past the row's end repeats its first one with a scale of zero
       // (columns that are never written, terms of zero in the row's sum)
       float2 dot = both(0.f);
+      float2 gy[kHold ? V : 1][4], q[kHold ? V : 1][4];
+      float scale[kHold ? V : 1];
+      auto fetch = [&](int v, int at) {
+        scale[at] = in[v] ? ckpt_scale(ssc[(col[v] / kCkptGroup) * p.chunk + in_chunk + i]) : 0.f;
+        load_pairs<true>(gyr + col[v], 8, gy[at]);
+        code_pairs(*reinterpret_cast<const uint2*>(qr + col[v]), q[at]);
+        if (!kGamma) load_pairs<true>(gamma + col[v], 8, gm[0]);
+      };
       if (on) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          const float scale = in[v] ? ckpt_scale(ssc[(col[v] / kCkptGroup) * p.chunk + in_chunk + i]) : 0.f;
-          float2 gy[4], q[4], gm[4];
-          load_pairs<true>(gyr + col[v], 8, gy);
-          code_pairs(*reinterpret_cast<const uint2*>(qr + col[v]), q);
-          load_pairs<true>(gamma + col[v], 8, gm);
+          const int h = kHold ? v : 0;
+          fetch(v, h);
           float2 part = both(0.f);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float2 x = mul2(gy[e], q[e]);
-            acc[v][e] = fma2(x, both(scale), acc[v][e]);
-            part = fma2(x, gm[e], part);
+            const float2 x = mul2(gy[h][e], q[h][e]);
+            acc[v][e] = fma2(x, both(scale[h]), acc[v][e]);
+            part = fma2(x, gm[kGamma ? v : 0][e], part);
           }
-          dot = fma2(part, both(scale), dot);
+          dot = fma2(part, both(scale[h]), dot);
         }
       }
-      const float c1 = row_sum_stream<W, kCons>(dot.x + dot.y, red[it & 1], warp) * -inv_c;
+      const float c1 = row_sum_stream<W>(dot.x + dot.y, red[it & 1], warp) * -inv_c;
       if (on) {
         const float r = sr[in_chunk + i];
         const T* resr = sres + i * a.C;
@@ -424,17 +452,17 @@ __global__ void __launch_bounds__((W > 8 ? 32 * W : 256) + 32, CTAS)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           // r (gy gamma - u c) + residual
-          const float uc = (in[v] ? ckpt_scale(ssc[(col[v] / kCkptGroup) * p.chunk + in_chunk + i]) : 0.f) * c1;
-          float2 d[4], q[4], gm[4];
-          load_pairs<true>(gyr + col[v], 8, d);
-          code_pairs(*reinterpret_cast<const uint2*>(qr + col[v]), q);
-          load_pairs<true>(gamma + col[v], 8, gm);
+          const int h = kHold ? v : 0;
+          if (!kHold) fetch(v, 0);
+          const float2 uc = both(scale[h] * c1);
+          float2 d[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) d[e] = fma2(q[e], both(uc), mul2(d[e], gm[e]));
+          for (int e = 0; e < 4; ++e) d[e] = fma2(q[h][e], uc, mul2(gy[h][e], gm[kGamma ? v : 0][e]));
           if (a.res) {
-            load_pairs<true>(resr + col[v], 8, gm);
+            float2 o[4];
+            load_pairs<true>(resr + col[v], 8, o);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) d[e] = fma2(d[e], both(r), gm[e]);
+            for (int e = 0; e < 4; ++e) d[e] = fma2(d[e], both(r), o[e]);
           } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e) d[e] = mul2(d[e], both(r));
@@ -485,23 +513,29 @@ __global__ void __launch_bounds__((W > 8 ? 32 * W : 256) + 32, CTAS)
     GO(32, 4);                                           \
   } while (0)
 
-// streaming backward: warps a row, vectors a thread, CTAs an SM
+// Streaming backward: warps a row, vectors a thread, CTAs an SM, what a thread holds.
+// Whatever the registers hold a thread needs no second time from the ring, but a
+// spilled register waits behind the copies like any plain load: with the row held at
+// 8192 x 4096 (spills) 131 us instead of 46, gamma held at 8191 x 11008 291 instead of
+// 113.  Three CTAs an SM, whose registers hold only the sums, took 49 us at
+// 8192 x 4096, 29 instead of 27.5 at 16384 x 1024 and 21.6 instead of 18.7 at
+// 12544 x 448 fp32.
 #define INSTANT_STREAM_DISPATCH(C, GO)                   \
   do {                                                   \
-    if ((C) <= 256) GO(1, 1, 3);                         \
-    if ((C) <= 512) GO(2, 1, 3);                         \
-    if ((C) <= 1024) GO(4, 1, 3);                        \
-    if ((C) <= 2048) GO(8, 1, 3);                        \
-    if ((C) <= 4096) GO(8, 2, 3);                        \
-    if ((C) <= 8192) GO(8, 4, 2);                        \
-    GO(16, 3, 1);                                        \
+    if ((C) <= 256) GO(1, 1, 2, HOLD_ROW);               \
+    if ((C) <= 512) GO(2, 1, 2, HOLD_ROW);               \
+    if ((C) <= 1024) GO(4, 1, 2, HOLD_ROW);              \
+    if ((C) <= 2048) GO(8, 1, 2, HOLD_ROW);              \
+    if ((C) <= 4096) GO(8, 2, 2, HOLD_GAMMA);            \
+    if ((C) <= 8192) GO(16, 2, 1, HOLD_GAMMA);           \
+    GO(16, 3, 1, HOLD_SUMS);                             \
   } while (0)
 
 // Streaming plan; false where the direct form runs: rows too wide for a ring of
-// two, or fewer than two blocks a CTA, where its start costs more than its ring
-// gives (us, streaming / direct, bf16: 8192 x 4096 48.7 / 95.5, 8191 x 11008
-// 116 / 267, 512 x 11008 21 / 29, 16384 x 768 30 / 44; 300 x 8192 14.6 / 12.4,
-// 8192 x 64 8.7 / 8.1).  A slot holds about 16 KB, the CTAs of an SM about 220 KB.
+// two, or fewer blocks than CTAs (us, streaming / direct, bf16: 8192 x 4096 45.8 / 95.3,
+// 8191 x 11008 113 / 272, 16384 x 768 26.4 / 43, 1000 x 1024 6.8 / 7.6, 300 x 8192
+// 10.4 / 13.6; 8192 x 64 7.4 / 6.3).  A slot holds about 16 KB, the CTAs of an SM about
+// 220 KB.
 bool stream_plan(StreamPlan& p, const NormBackArgs& a, size_t elem, int w, int v, int ctas, int most_ctas) {
   const int slots = w > 8 ? 1 : 8 / w;
   const int groups = (a.C + kCkptGroup - 1) / kCkptGroup;
@@ -511,7 +545,7 @@ bool stream_plan(StreamPlan& p, const NormBackArgs& a, size_t elem, int w, int v
   p.block = static_cast<int>(slots * passes);
   p.blocks = (a.rows + p.block - 1) / p.block;
   const int full = ctas * std::min(sm_count(), kColSumSMs);
-  if (p.blocks < 2 * most_ctas * sm_count()) return false;
+  if (p.blocks < most_ctas * sm_count()) return false;
   p.grid = std::min(full, norm_back_parts(a.rows, a.C));  // the workspace's shares
   p.per_cta = (p.blocks + p.grid - 1) / p.grid;
   p.grid = (p.blocks + p.per_cta - 1) / p.per_cta;
@@ -539,14 +573,14 @@ bool stream_plan(StreamPlan& p, const NormBackArgs& a, size_t elem, int w, int v
   return p.smem <= room;
 }
 
-template <typename T, int W, int V, int CTAS>
+template <typename T, int W, int V, int CTAS, int HOLD>
 cudaError_t back_stream_go(const NormBackArgs& a, bool* done, cudaStream_t st) {
   StreamPlan p;
   *done = false;
   for (int ctas = CTAS; ctas >= 1 && !*done; --ctas)  // fewer CTAs an SM have wider rings
     *done = stream_plan(p, a, sizeof(T), W, V, ctas, CTAS);
   if (!*done) return cudaSuccess;
-  auto k = k_rms_norm_back_stream<T, W, V, CTAS>;
+  auto k = k_rms_norm_back_stream<T, W, V, CTAS, HOLD>;
   cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(k), p.smem, true);
   if (e == cudaSuccess)
     e = launch_ex(k, dim3(p.grid), dim3((W > 8 ? 32 * W : 256) + 32), p.smem, st, 1, pdl_enabled(), a, p);
@@ -556,7 +590,7 @@ cudaError_t back_stream_go(const NormBackArgs& a, bool* done, cudaStream_t st) {
 
 template <typename T>
 cudaError_t back_stream_dispatch(const NormBackArgs& a, bool* done, cudaStream_t st) {
-#define GO(W, V, CTAS) return back_stream_go<T, W, V, CTAS>(a, done, st)
+#define GO(W, V, CTAS, HOLD) return back_stream_go<T, W, V, CTAS, HOLD>(a, done, st)
   INSTANT_STREAM_DISPATCH(a.C, GO);
 #undef GO
 }
