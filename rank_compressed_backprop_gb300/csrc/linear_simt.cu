@@ -213,10 +213,19 @@ __global__ void __launch_bounds__(32 * BM / R) k_linear_simt(LinearArgs a, int s
   const int first = splits > 1 ? rank + splits * warp : warp * R;
   const int step = splits > 1 ? splits * (BM / R) : 1;
   const int last = min(splits > 1 ? BM : warp * R + R, a.M - m0);
-#pragma unroll 2
+#pragma unroll 1
   for (int i = first; i < last; i += step) {
     const int m = m0 + i;
     const size_t base = static_cast<size_t>(m) * a.N + n0 + lane;
+    // global operands are asked for before the peers' partial sums
+    const bool slopes = KIND == BACK && a.act != INSTANT_ACT_NONE;
+    float scale = 0.f, z[4], res[4];
+    if (slopes) scale = ckpt_scale(__ldg(a.ck.s + static_cast<size_t>(n0 / kCkptGroup) * a.M + m));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      z[j] = slopes && on[j] ? static_cast<float>(__ldg(a.ck.q + static_cast<size_t>(m) * a.ld + n0 + lane + 32 * j)) : 0.f;
+      res[j] = KIND != GRAD_W && a.res && on[j] ? static_cast<const float*>(a.res)[base + 32 * j] : 0.f;
+    }
     const float* src = buf + i * BN + lane;
     float v[4];
     if (splits == 1) {
@@ -255,17 +264,13 @@ __global__ void __launch_bounds__(32 * BM / R) k_linear_simt(LinearArgs a, int s
       if (a.zk.q) put_ckpt(a.zk, a.ld, a.M, m, n0, a.N, v);
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] = act_f32(v[j], a.act);
-    } else if (a.act != INSTANT_ACT_NONE) {
-      const float scale = ckpt_scale(a.ck.s[static_cast<size_t>(n0 / kCkptGroup) * a.M + m]);
-      const int8_t* q = a.ck.q + static_cast<size_t>(m) * a.ld + n0 + lane;
+    } else if (slopes) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (on[j]) v[j] *= act_slope_f32(static_cast<float>(q[32 * j]) * scale, a.act);
+      for (int j = 0; j < 4; ++j) v[j] *= act_slope_f32(z[j] * scale, a.act);
     }
     if (a.res) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (on[j]) v[j] += static_cast<const float*>(a.res)[base + 32 * j];
+      for (int j = 0; j < 4; ++j) v[j] += res[j];
     }
     if (KIND == FORWARD && a.yk.q) put_ckpt(a.yk, a.ld, a.M, m, n0, a.N, v);
     if (a.out) {
@@ -295,7 +300,7 @@ cudaError_t go(const LinearArgs& a, cudaStream_t st) {
              : launch_ex(k_linear_simt<KIND, BM, R, false>, grid, block, 0, st, splits, pdl_enabled(), a, splits, per);
 }
 
-// row tiles of 64 where the rows or the grid call for them, else 16
+// row tiles of 64, or of 16 for short batches
 template <int KIND>
 cudaError_t go_rows(const LinearArgs& a, cudaStream_t st) {
   return a.M > 32 ? go<KIND, 64, 8>(a, st) : go<KIND, 16, 4>(a, st);
