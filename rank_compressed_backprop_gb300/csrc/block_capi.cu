@@ -233,27 +233,31 @@ instant_status instant_ckpt_grad_w(const void* gy, const void* q, const void* s,
   a.ld = ckpt_ld(Cx);
   a.accumulate = accumulate != 0;
   float* part = gb ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + values_bytes(rows, Cx)) : nullptr;
-  cudaError_t e = cudaSuccess;
-  bool side = false;
-  if (bf16) {
-    // the values are exact in bf16 and every row tile of gw reads them: made once
-    a.b = ws;
+  if (!bf16) {
+    cudaError_t e = launch_linear(a, bf16, st);
+    if (e == cudaSuccess && gb)
+      e = launch_col_sum(static_cast<const float*>(gy), gb, part, rows, Cy, accumulate != 0, vec_ok(Cy), st);
+    return from_cuda(e);
+  }
+  // the values are exact in bf16 and every row tile of gw reads them: made once
+  a.b = ws;
+  // gb's shares on the side of a product long enough for the pair kernel's idle warps
+  // to read gy, which they do at about 0.8 TB/s; else in the launch that makes the values
+  int parts = 0;
+  cudaError_t e;
+  if (gb && !(runs_on_pairs(a) && 2e-6 * rows * Cy / 0.8 <= pairs_us(a))) {
+    e = launch_unpack_and_sum(a.ck, ws, rows, Cx, gy, part, Cy, &parts, st);
+  } else {
     e = launch_ckpt_unpack(a.ck, ws, rows, Cx, true, true, st);
-    // gb on the side of a product long enough for the pair kernel's idle warps to
-    // read gy, which they do at about 0.8 TB/s; else in a launch of its own
-    side = gb && runs_on_pairs(a) && 2e-6 * rows * Cy / 0.8 <= pairs_us(a);
-    if (side) {
+    if (gb) {
       a.sum_part = part;
       a.sum_parts = std::min(col_sum_parts(rows, Cy), std::max(1, 2 * kColSumSMs / cdiv(Cy, 256)));
       a.sum_per = cdiv(rows, a.sum_parts);
-      a.sum_parts = cdiv(rows, a.sum_per);
+      parts = a.sum_parts = cdiv(rows, a.sum_per);
     }
   }
   if (e == cudaSuccess) e = launch_linear(a, bf16, st);
-  if (e == cudaSuccess && side)
-    e = launch_part_sum(part, gb, a.sum_parts, Cy, accumulate != 0, st);
-  else if (e == cudaSuccess && gb)
-    e = launch_col_sum(gy, gb, part, rows, Cy, accumulate != 0, bf16, vec_ok(Cy), st);
+  if (e == cudaSuccess && gb) e = launch_part_sum(part, gb, parts, Cy, accumulate != 0, st);
   return from_cuda(e);
 }
 

@@ -58,18 +58,16 @@ __global__ void __launch_bounds__(kThreads)
 // A thread takes eight channels of a row (8 bytes in, 16 out), four rows at once;
 // a CTA `cp` neighbouring threads' channels of 256 / cp rows.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads)
-    k_ckpt_unpack(const int8_t* __restrict__ q, const uint8_t* __restrict__ s, T* __restrict__ x,
-                  int rows, int C, int ld, int cp, int per) {
-  pdl_launch_dependents();
-  pdl_wait();
+__device__ __forceinline__ void unpack_rows(const int8_t* __restrict__ q, const uint8_t* __restrict__ s,
+                                            T* __restrict__ x, int rows, int C, int ld, int cp, int per,
+                                            int column, int share) {
   constexpr int kUnroll = 4;
-  const int c = 8 * (blockIdx.x * cp + (threadIdx.x & (cp - 1)));
+  const int c = 8 * (column * cp + (threadIdx.x & (cp - 1)));
   if (c >= C) return;
   const int step = kThreads / cp;
   const uint8_t* sg = s + static_cast<size_t>(c / kCkptGroup) * rows;
-  const int r1 = min(rows, (static_cast<int>(blockIdx.y) + 1) * per);
-  for (int r0 = blockIdx.y * per + static_cast<int>(threadIdx.x) / cp; r0 < r1; r0 += kUnroll * step) {
+  const int r1 = min(rows, (share + 1) * per);
+  for (int r0 = share * per + static_cast<int>(threadIdx.x) / cp; r0 < r1; r0 += kUnroll * step) {
     uint2 w[kUnroll];
     float scale[kUnroll];
 #pragma unroll
@@ -91,18 +89,25 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads)
+    k_ckpt_unpack(const int8_t* __restrict__ q, const uint8_t* __restrict__ s, T* __restrict__ x,
+                  int rows, int C, int ld, int cp, int per) {
+  pdl_launch_dependents();
+  pdl_wait();
+  unpack_rows<T, VEC>(q, s, x, rows, C, ld, cp, per, blockIdx.x, blockIdx.y);
+}
+
 // Column sums in two fixed-order stages (no atomics: the same bits on every
 // call).  Stage 1: a CTA sums `per` rows of 8 x 32 columns, eight warps taking
 // the rows in turn; stage 2 adds the row shares.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads, 3)
-    k_col_sum(const T* __restrict__ x, float* __restrict__ part, int rows, int C, int per) {
+__device__ __forceinline__ void sum_rows(const T* __restrict__ x, float* __restrict__ part, int rows, int C, int per,
+                                         int strip, int share) {
   __shared__ float red[8][kThreads];
-  pdl_launch_dependents();
-  pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x * 256 + 8 * lane;
-  const int r0 = blockIdx.y * per;
+  const int c = strip * 256 + 8 * lane;
+  const int r0 = share * per;
   const int r1 = min(rows, r0 + per);
   float2 sum2[4];
 #pragma unroll
@@ -136,8 +141,29 @@ __global__ void __launch_bounds__(kThreads, 3)
   float sum = 0.f;
 #pragma unroll
   for (int w = 0; w < 8; ++w) sum += red[w][threadIdx.x];
-  const int col = blockIdx.x * 256 + threadIdx.x;
-  if (col < C) part[static_cast<size_t>(blockIdx.y) * C + col] = sum;
+  const int col = strip * 256 + threadIdx.x;
+  if (col < C) part[static_cast<size_t>(share) * C + col] = sum;
+}
+
+template <bool VEC>
+__global__ void __launch_bounds__(kThreads, 3)
+    k_col_sum(const float* __restrict__ x, float* __restrict__ part, int rows, int C, int per) {
+  pdl_launch_dependents();
+  pdl_wait();
+  sum_rows<float, VEC>(x, part, rows, C, per, blockIdx.x, blockIdx.y);
+}
+
+// Stage 1 of a bias gradient beside the checkpoint's values for the weight gradient,
+// in one launch: the CTAs from `sums` on sum x, the others unpack
+__global__ void __launch_bounds__(kThreads, 3)
+    k_unpack_and_sum(const int8_t* __restrict__ q, const uint8_t* __restrict__ s, uint16_t* __restrict__ v, int C,
+                     int ld, int cp, int per, int columns, const uint16_t* __restrict__ x, float* __restrict__ part,
+                     int Cx, int sum_per, int strips, int sums, int rows) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int b = blockIdx.x;
+  if (b < sums) unpack_rows<uint16_t, true>(q, s, v, rows, C, ld, cp, per, b % columns, b / columns);
+  else sum_rows<uint16_t, true>(x, part, rows, Cx, sum_per, (b - sums) % strips, (b - sums) / strips);
 }
 
 // out[c] (+)= sum_p part[p][c]: eight columns a CTA (a 32-byte sector of each
@@ -200,16 +226,25 @@ cudaError_t launch_ckpt_pack(const void* x, const CkptRef& k, int rows, int C, b
              : go(k_ckpt_pack<float, false>, static_cast<const float*>(x));
 }
 
+// how the CTAs of an unpacking divide [rows, C]
+struct UnpackPlan {
+  int cp, columns, per, shares;
+  UnpackPlan(int rows, int C) {
+    const int chunks = (C + 7) / 8;
+    cp = pow2_up(chunks, kThreads);
+    columns = (chunks + cp - 1) / cp;
+    per = rows_per_cta(rows, columns, 4 * kThreads / cp, 16 * sm_count());
+    shares = (rows + per - 1) / per;
+  }
+};
+
 cudaError_t launch_ckpt_unpack(const CkptRef& k, void* x, int rows, int C, bool bf16, bool vec,
                                cudaStream_t st) {
-  const int chunks = (C + 7) / 8;
-  const int cp = pow2_up(chunks, kThreads);
-  const int columns = (chunks + cp - 1) / cp;
-  const int per = rows_per_cta(rows, columns, 4 * kThreads / cp, 16 * sm_count());
-  const dim3 grid(columns, (rows + per - 1) / per);
-  auto go = [&](auto kernel, auto* p) {
-    return launch_ex(kernel, grid, dim3(kThreads), 0, st, 1, pdl_enabled(), static_cast<const int8_t*>(k.q),
-                     static_cast<const uint8_t*>(k.s), p, rows, C, ckpt_ld(C), cp, per);
+  const UnpackPlan p(rows, C);
+  auto go = [&](auto kernel, auto* dst) {
+    return launch_ex(kernel, dim3(p.columns, p.shares), dim3(kThreads), 0, st, 1, pdl_enabled(),
+                     static_cast<const int8_t*>(k.q), static_cast<const uint8_t*>(k.s), dst, rows, C, ckpt_ld(C), p.cp,
+                     p.per);
   };
   if (bf16) return go(k_ckpt_unpack<uint16_t, true>, static_cast<uint16_t*>(x));
   return vec ? go(k_ckpt_unpack<float, true>, static_cast<float*>(x))
@@ -230,20 +265,31 @@ cudaError_t launch_part_sum(const float* part, float* out, int parts, int C, int
                    parts, C, accumulate);
 }
 
-cudaError_t launch_col_sum(const void* x, float* out, float* part, int rows, int C, int accumulate,
-                           bool bf16, bool vec, cudaStream_t st) {
+cudaError_t launch_col_sum(const float* x, float* out, float* part, int rows, int C, int accumulate, bool vec,
+                           cudaStream_t st) {
   int parts = col_sum_parts(rows, C);
   const int per = (rows + parts - 1) / parts;
   parts = (rows + per - 1) / per;
-  const dim3 grid((C + 255) / 256, parts);
-  auto go = [&](auto kernel, auto* p) {
-    return launch_ex(kernel, grid, dim3(kThreads), 0, st, 1, pdl_enabled(), p, part, rows, C, per);
-  };
-  const cudaError_t e = bf16 ? go(k_col_sum<uint16_t, true>, static_cast<const uint16_t*>(x))
-                        : vec ? go(k_col_sum<float, true>, static_cast<const float*>(x))
-                              : go(k_col_sum<float, false>, static_cast<const float*>(x));
-  if (e != cudaSuccess) return e;
-  return launch_part_sum(part, out, parts, C, accumulate, st);
+  const cudaError_t e = launch_ex(vec ? k_col_sum<true> : k_col_sum<false>, dim3((C + 255) / 256, parts),
+                                  dim3(kThreads), 0, st, 1, pdl_enabled(), x, part, rows, C, per);
+  return e != cudaSuccess ? e : launch_part_sum(part, out, parts, C, accumulate, st);
+}
+
+// bf16 values of a checkpoint of [rows, C] and the shares of the column sums of x
+// [rows, Cx], whose number it returns; launch_part_sum adds them
+cudaError_t launch_unpack_and_sum(const CkptRef& k, void* values, int rows, int C, const void* x, float* part, int Cx,
+                                  int* parts, cudaStream_t st) {
+  const UnpackPlan p(rows, C);
+  const int per = (rows + col_sum_parts(rows, Cx) - 1) / col_sum_parts(rows, Cx);
+  *parts = (rows + per - 1) / per;
+  const int strips = (Cx + 255) / 256;
+  const long long unpacks = static_cast<long long>(p.columns) * p.shares;
+  const long long all = unpacks + static_cast<long long>(strips) * *parts;
+  if (all > 0x7fffffffll) return cudaErrorInvalidValue;
+  return launch_ex(k_unpack_and_sum, dim3(static_cast<unsigned>(all)), dim3(kThreads), 0, st, 1, pdl_enabled(),
+                   static_cast<const int8_t*>(k.q), static_cast<const uint8_t*>(k.s), static_cast<uint16_t*>(values), C,
+                   ckpt_ld(C), p.cp, p.per, p.columns, static_cast<const uint16_t*>(x), part, Cx, per, strips,
+                   static_cast<int>(unpacks), rows);
 }
 
 }  // namespace instant

@@ -360,10 +360,12 @@ cudaError_t launch_ckpt_pack(const void* x, const CkptRef& k, int rows, int C, b
                              cudaStream_t st);
 cudaError_t launch_ckpt_unpack(const CkptRef& k, void* x, int rows, int C, bool bf16, bool vec,
                                cudaStream_t st);
+cudaError_t launch_unpack_and_sum(const CkptRef& k, void* values, int rows, int C, const void* x, float* part, int Cx,
+                                  int* parts, cudaStream_t st);
 cudaError_t launch_part_sum(const float* part, float* out, int parts, int C, int accumulate,
                             cudaStream_t st);
-cudaError_t launch_col_sum(const void* x, float* out, float* part, int rows, int C, int accumulate,
-                           bool bf16, bool vec, cudaStream_t st);
+cudaError_t launch_col_sum(const float* x, float* out, float* part, int rows, int C, int accumulate, bool vec,
+                           cudaStream_t st);
 cudaError_t launch_rms_norm(const NormArgs& a, bool bf16, cudaStream_t st);
 cudaError_t launch_rms_norm_back(const NormBackArgs& a, bool bf16, cudaStream_t st);
 cudaError_t launch_linear_simt(const LinearArgs& a, cudaStream_t st);  // fp32

@@ -11,9 +11,9 @@
 // products of a single CTA's 128 x 128 tile; the fp32 accumulator is 128 lanes x
 // 256 columns of each CTA's TMEM, two of them, so that the epilogue of one tile
 // runs under the products of the next.
-//   warp 0     TMA producer (one elected lane issues): 64-deep chunks of this CTA's A and B halves into a
-//              ring; the arrivals of both CTAs are counted on the leader's
-//              barrier (the leader issues the products of both)
+//   warp 0     TMA producer (one elected lane issues): 64-deep chunks of this CTA's
+//              A and B halves into a ring; the arrivals of both CTAs are counted on
+//              the leader's barrier (the leader issues the products of both)
 //   warp 1     MMA issuer (the leader's only); commits free the stage in both CTAs
 //   warps 4-19  epilogue: four groups of four warps, each 64 columns of the
 //              accumulator, a thread a row.  (Two groups of 128 columns a thread left
@@ -21,19 +21,22 @@
 //              1792 with gelu and both checkpoints 53 us.)  Two groups share the 128
 //              columns of a checkpoint group and exchange the scale byte of their
 //              halves' largest magnitudes: the larger byte is the group's.
-//              12544 x 448 -> 1792 with gelu and both checkpoints 36 us, without
-//              them 25
 // The tensor cores' fp32 accumulation cuts low bits at every step, which adds
 // up over a long contraction (6e-6 of a 8192-token weight gradient).  Where the
 // output shows it (fp32 gradients, and checkpoints, whose codes flip) the
 // accumulator holds `seg` chunks at a time and the epilogue threads add the
 // segments into registers in ordinary fp32, under the products of the next.
-// Operands contracted over their rows (w in back, gy and v in grad_w)
-// are MN-major operands read from their natural layout.  The residual
-// comes by TMA into swizzled boxes while the products run -- a thread's own row by
-// plain loads touches 32 lines an access and doubled the time of 12544 x 448 ->
-// 1792 -- and the results leave through the same boxes by TMA stores, which also clip ragged edges; accumulation into gw is the TMA's own add
-// (each element is added to once).
+// Operands contracted over their rows (w in back, gy and v in grad_w) are MN-major
+// operands read from their natural layout.  The residual comes by TMA into swizzled
+// boxes while the products run -- a thread's own row by plain loads touches 32 lines an
+// access and doubled the time of 12544 x 448 -> 1792 -- and the results leave through
+// the same boxes by TMA stores, which also clip ragged edges; accumulation into gw is
+// the TMA's own add (each element is added to once).
+//
+// Bound: at 8192 x 11008 -> 4096 the tensor cores (393 us, 1.88 PFLOP/s; sustained 444,
+// 1.66 PFLOP/s, under the power limit, like a library matrix product of these sizes);
+// at 12544 x 448 -> 1792 the epilogue's instructions (17 us plain, 25 with gelu, 36 with
+// both checkpoints, for 11 us of products).
 #include <utility>
 
 #include "ckpt.cuh"
