@@ -488,7 +488,8 @@ instant_status instant_linear_act_grad(const void* gy, const void* w, const void
  *   gw [Cy, Cx] fp32, gb [Cy] fp32 or NULL (written, or added to)
  *   ws  device scratch of instant_ckpt_grad_w_workspace_bytes(rows, Cx, Cy)
  *       bytes, 16-byte aligned (f32: may be NULL without gb); contents are
- *       overwritten.  Its larger part holds v in bf16 during the call
+ *       overwritten.  It holds v in bf16, shares of gb's sums and,
+ *       where the rows are shared out, partial products of gw
  * The sums over rows are taken in a fixed order.
  */
 instant_status instant_ckpt_grad_w(const void* gy, const void* q, const void* s, const void* col_scale,

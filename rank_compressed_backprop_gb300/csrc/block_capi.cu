@@ -36,6 +36,40 @@ CkptRef ref(const void* q, const void* s) {
 bool align_ok(instant_dtype dt, int C) { return dt == INSTANT_F32 || C % 8 == 0; }
 bool vec_ok(int C) { return C % 8 == 0; }
 
+// pieces of 256 x 256 x 64 chunks on the CTA pairs
+double pairs_us(double pieces, int chunks, int sms) {
+  return 4.5 + 0.30 * chunks * std::ceil(pieces / std::max(1, sms / 2));
+}
+
+// the partial products' way to memory and back through launch_split_sum
+double split_sum_us(int splits, int M, int N) {
+  return splits > 1 ? 3.0 + 4e-6 * splits * M * N / 4.0 : 0.0;
+}
+
+// Shares of the rows into which the pair kernel cuts a weight gradient [M, N] over K
+// rows: its tiles are few (14 at 1792 x 448) and its rows many, so that without them
+// most pairs stand idle (us, without shares and the split-K kernel in their place / with:
+// 12544 x 448 x 1792 33.7 / 24.3, 16384 x 768 x 768 28 / 25.3, 9728 x 448 x 2048 24.9 /
+// 23).  A gain of less than a tenth is left: at 16384 x 4096 x 4096 the estimate saw 1 %
+// in two shares and they took 348 instead of 340.  Counted from the SMs of the one device
+// this library is built for: the workspace's size needs no device.
+int grad_w_splits(int M, int N, int K) {
+  const double tiles = static_cast<double>(cdiv(M, 256)) * cdiv(N, 256);
+  const int chunks = cdiv(K, 64);
+  int best = 1;
+  double best_us = 0.9 * pairs_us(tiles, chunks, kColSumSMs);
+  for (int n = 2; n <= kMaxSplits; ++n) {
+    const int per = cdiv(chunks, n);
+    if (cdiv(chunks, per) != n) continue;  // an empty share
+    const double us = pairs_us(tiles * n, per, kColSumSMs) + split_sum_us(n, M, N);
+    if (us < best_us) {
+      best = n;
+      best_us = us;
+    }
+  }
+  return best;
+}
+
 // bf16 products run on the tensor cores, fp32 ones on FFMA.  Of the two tensor-core
 // kernels the one with the smaller estimate runs:
 //   CTA pairs, 256 x 256 tiles      4.5 us + 0.30 us a chunk of 64 and wave of 76 tiles
@@ -49,8 +83,10 @@ bool vec_ok(int C) { return C % 8 == 0; }
 // 1024 x 4096 -> 1024 14.4 / 21.6; weight gradient over 4096 rows, 1024 x 1024
 // 16.8 / 26.1, over 700 rows, 1792 x 448 10.8 / 9.9.
 double pairs_us(const LinearArgs& a) {
-  const double waves = std::ceil(static_cast<double>(cdiv(a.M, 256)) * cdiv(a.N, 256) / std::max(1, sm_count() / 2));
-  return 4.5 + 0.30 * cdiv(a.K, 64) * waves;
+  const int splits = std::max(1, a.splits);
+  return pairs_us(static_cast<double>(cdiv(a.M, 256)) * cdiv(a.N, 256) * splits, cdiv(cdiv(a.K, 64), splits),
+                  sm_count()) +
+         split_sum_us(splits, a.M, a.N);
 }
 
 bool runs_on_pairs(const LinearArgs& a) {
@@ -203,9 +239,17 @@ static size_t values_bytes(int rows, int Cx) {
   return (static_cast<size_t>(rows) * Cx * 2 + 255) & ~static_cast<size_t>(255);
 }
 
+static size_t sums_bytes(int rows, int Cy) {
+  return (static_cast<size_t>(col_sum_parts(rows, Cy)) * Cy * sizeof(float) + 255) & ~static_cast<size_t>(255);
+}
+static size_t splits_bytes(int rows, int Cx, int Cy) {
+  const int splits = grad_w_splits(Cy, Cx, rows);
+  return splits > 1 ? static_cast<size_t>(splits) * cdiv(Cy, 256) * 256 * Cx * sizeof(float) : 0;
+}
+
 size_t instant_ckpt_grad_w_workspace_bytes(int rows, int Cx, int Cy) {
   if (!extent_ok(rows, Cx) || !extent_ok(rows, Cy)) return 0;
-  return values_bytes(rows, Cx) + static_cast<size_t>(col_sum_parts(rows, Cy)) * Cy * sizeof(float);
+  return values_bytes(rows, Cx) + sums_bytes(rows, Cy) + splits_bytes(rows, Cx, Cy);
 }
 
 instant_status instant_ckpt_grad_w(const void* gy, const void* q, const void* s, const void* col_scale,
@@ -241,11 +285,15 @@ instant_status instant_ckpt_grad_w(const void* gy, const void* q, const void* s,
   }
   // the values are exact in bf16 and every row tile of gw reads them: made once
   a.b = ws;
+  a.splits = grad_w_splits(Cy, Cx, rows);
+  a.split_part =
+      reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + values_bytes(rows, Cx) + sums_bytes(rows, Cy));
+  const bool pairs = runs_on_pairs(a);
   // gb's shares on the side of a product long enough for the pair kernel's idle warps
   // to read gy, which they do at about 0.8 TB/s; else in the launch that makes the values
   int parts = 0;
   cudaError_t e;
-  if (gb && !(runs_on_pairs(a) && 2e-6 * rows * Cy / 0.8 <= pairs_us(a))) {
+  if (gb && !(pairs && 2e-6 * rows * Cy / 0.8 <= pairs_us(a))) {
     e = launch_unpack_and_sum(a.ck, ws, rows, Cx, gy, part, Cy, &parts, st);
   } else {
     e = launch_ckpt_unpack(a.ck, ws, rows, Cx, true, true, st);
@@ -257,6 +305,8 @@ instant_status instant_ckpt_grad_w(const void* gy, const void* q, const void* s,
     }
   }
   if (e == cudaSuccess) e = launch_linear(a, bf16, st);
+  if (e == cudaSuccess && pairs && a.splits > 1)
+    e = launch_split_sum(a.split_part, a.splits, gw, col_scale, Cy, Cx, accumulate != 0, st);
   if (e == cudaSuccess && gb) e = launch_part_sum(part, gb, parts, Cy, accumulate != 0, st);
   return from_cuda(e);
 }

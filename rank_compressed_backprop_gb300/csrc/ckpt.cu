@@ -208,7 +208,56 @@ int rows_per_cta(int rows, int columns, int pass, int ctas) {
   return static_cast<int>((per + pass - 1) / pass * pass);
 }
 
+// Sum of the partial products of a weight gradient, in the order of the shares of the
+// rows; four columns a thread
+__global__ void __launch_bounds__(kThreads)
+    k_split_sum(const float* __restrict__ part, float* __restrict__ out, const uint16_t* __restrict__ scale,
+                long long n, long long pitch, int N, int splits, int accumulate) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const long long i = 4 * (static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x);
+  if (i >= n) return;
+  float4 v[kMaxSplits];
+#pragma unroll
+  for (int s = 0; s < kMaxSplits; ++s)
+    if (s < splits) v[s] = *reinterpret_cast<const float4*>(part + s * pitch + i);
+#pragma unroll
+  for (int s = 1; s < kMaxSplits; ++s)
+    if (s < splits) {
+      v[0].x += v[s].x;
+      v[0].y += v[s].y;
+      v[0].z += v[s].z;
+      v[0].w += v[s].w;
+    }
+  if (scale) {
+    const uint2 w = *reinterpret_cast<const uint2*>(scale + i % N);
+    v[0].x *= __uint_as_float(w.x << 16);
+    v[0].y *= __uint_as_float(w.x & 0xffff0000u);
+    v[0].z *= __uint_as_float(w.y << 16);
+    v[0].w *= __uint_as_float(w.y & 0xffff0000u);
+  }
+  float4* dst = reinterpret_cast<float4*>(out + i);
+  if (accumulate) {
+    const float4 o = *dst;
+    v[0].x += o.x;
+    v[0].y += o.y;
+    v[0].z += o.z;
+    v[0].w += o.w;
+  }
+  *dst = v[0];
+}
+
 }  // namespace
+
+cudaError_t launch_split_sum(const float* part, int splits, float* out, const void* scale, int M, int N,
+                             int accumulate, cudaStream_t st) {
+  const long long n = static_cast<long long>(M) * N;  // N is a multiple of 8
+  const long long pitch = (static_cast<long long>(M) + 255) / 256 * 256 * N;
+  const long long ctas = (n / 4 + kThreads - 1) / kThreads;
+  if (ctas > 0x7fffffffll || splits > kMaxSplits) return cudaErrorInvalidValue;
+  return launch_ex(k_split_sum, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, st, 1, pdl_enabled(), part, out,
+                   static_cast<const uint16_t*>(scale), n, pitch, N, splits, accumulate);
+}
 
 cudaError_t launch_ckpt_pack(const void* x, const CkptRef& k, int rows, int C, bool bf16, bool vec,
                              cudaStream_t st) {

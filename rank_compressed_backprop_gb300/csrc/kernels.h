@@ -349,6 +349,8 @@ struct LinearArgs {
   int accumulate;      // kind 2
   float* sum_part;     // kind 2, pair kernel: shares of the column sums of a, or null
   int sum_parts, sum_per;  // how many, rows of a share
+  float* split_part;   // kind 2, pair kernel: partial products [splits][M to 256][N] where splits > 1
+  int splits;
 };
 
 // shares of a column reduction are counted from the SMs of the one device this
@@ -386,11 +388,16 @@ struct TcArgs {
   const void* sum_src; // [K, M] bf16 whose columns are summed on the side (grad_w), or null
   float* sum_part;     // [sum_parts, M]
   int sum_parts, sum_per;
+  int splits, per;     // shares of K (grad_w), chunks of a share
 };
 struct TcMaps {
   CUtensorMap a, b, y, z, k, r;
 };
 cudaError_t launch_linear_tc(const LinearArgs& a, cudaStream_t st);
+constexpr int kMaxSplits = 8;
+// out [M, N] (+)= (sum of the partial products) * scale per column (bf16, or null)
+cudaError_t launch_split_sum(const float* part, int splits, float* out, const void* scale, int M, int N,
+                             int accumulate, cudaStream_t st);
 
 // the same for outputs of few tiles (linear_few.cu)
 struct FewArgs {

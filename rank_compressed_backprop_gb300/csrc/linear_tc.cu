@@ -205,6 +205,22 @@ __device__ __forceinline__ void tile_at(const TcArgs& a, int t, int& m, int& n) 
   n = r / gsz;
 }
 
+// piece t of the work: an output tile, and in grad_w a share of its chunks
+template <int KIND>
+__device__ __forceinline__ void work_at(const TcArgs& a, int t, int& m, int& n, int& share, int& k_lo, int& nk) {
+  share = 0;
+  k_lo = 0;
+  nk = a.nk;
+  if (KIND == GRAD_W && a.splits > 1) {
+    const int tiles = a.mt * a.nt;
+    share = t / tiles;
+    t -= share * tiles;
+    k_lo = share * a.per;
+    nk = min(a.per, a.nk - k_lo);
+  }
+  tile_at(a, t, m, n);
+}
+
 // 32 columns of this warp's 32 lanes, no wait
 __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t* r) {
   asm volatile(
@@ -307,9 +323,9 @@ __device__ __forceinline__ void make_codes(uint4 (&q)[4], uint32_t code, const f
 // One accumulator segment after the other into v, 64 columns of a row a thread.
 // `release(acc)` hands the accumulator back; ids and count as in mbar_wait_group.
 template <typename Release>
-__device__ __forceinline__ bool sum_segments(const TcArgs& a, uint32_t tbase, uint64_t* t_full, int id, int count,
+__device__ __forceinline__ bool sum_segments(const TcArgs& a, int nk, uint32_t tbase, uint64_t* t_full, int id, int count,
                                              int& q, float2* v, const Release& release) {
-  for (int k0 = 0; k0 < a.nk; k0 += a.seg, ++q) {
+  for (int k0 = 0; k0 < nk; k0 += a.seg, ++q) {
     const int acc = q & 1;
     if (!mbar_wait_group(&t_full[acc], (q >> 1) & 1, id, count)) return false;
     tc_fence_after();
@@ -388,7 +404,7 @@ __device__ __forceinline__ void epilogue_keep(const TcArgs& a, const CUtensorMap
       *reinterpret_cast<float2*>(vec + 2 * lane) = b;
     }
     float2 v[32];
-    if (!sum_segments(a, tbase, t_full, id, count, q, v, release)) {
+    if (!sum_segments(a, a.nk, tbase, t_full, id, count, q, v, release)) {
       raise_fault(FAULT_WAIT_DONE);
       break;
     }
@@ -455,7 +471,7 @@ __device__ __forceinline__ void epilogue(const TcArgs& a, const CUtensorMap* my,
   in_full += group;                         // epilogue operands arrived
   int in_par = 0;
   float* vec = reinterpret_cast<float*>(smem + L::vec) + 64 * group;
-  const int tiles = a.mt * a.nt;
+  const int tiles = a.mt * a.nt * (KIND == GRAD_W ? a.splits : 1);
   const uint32_t tbase = tmem + 64 * group + (static_cast<uint32_t>((warp & 3) * 32) << 16);
   int q = 0;    // accumulators read so far
   auto release = [&](int acc) {  // the accumulator may be overwritten
@@ -464,8 +480,8 @@ __device__ __forceinline__ void epilogue(const TcArgs& a, const CUtensorMap* my,
     if (lane == 0) mbar_arrive_at(t_empty_leader + 8 * acc);
   };
   for (int t = pair; t < tiles; t += pairs) {
-    int m, n;
-    tile_at(a, t, m, n);
+    int m, n, share, k_lo, nk;
+    work_at<KIND>(a, t, m, n, share, k_lo, nk);
     const int row0 = m * BM + static_cast<int>(rank) * 128;
     const int col = n * BN + 64 * group;
     const bool on = row0 + r < a.M;
@@ -481,7 +497,7 @@ __device__ __forceinline__ void epilogue(const TcArgs& a, const CUtensorMap* my,
       vec[r] = col + r < a.N ? bf16_to_f32(static_cast<const uint16_t*>(a.bias)[col + r]) : 0.f;
     if (KIND == GRAD_W) {
       float2 v[32];
-      if (!sum_segments(a, tbase, t_full, id, count, q, v, release)) {
+      if (!sum_segments(a, nk, tbase, t_full, id, count, q, v, release)) {
         raise_fault(FAULT_WAIT_DONE);
         break;
       }
@@ -504,8 +520,9 @@ __device__ __forceinline__ void epilogue(const TcArgs& a, const CUtensorMap* my,
         if (lead) {
           const int c0 = col + 32 * h;
           if (c0 < a.N && row0 < a.M) {
+            // the shares' products lie one after the other, padded to whole tiles
             if (a.accumulate) tma_add_2d(my, box, c0, row0);
-            else tma_store_2d(my, box, c0, row0);
+            else tma_store_2d(my, box, c0, share * a.mt * BM + row0);
           }
           tma_store_commit();
         }
@@ -628,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   const int lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  const int tiles = a.mt * a.nt;
+  const int tiles = a.mt * a.nt * (KIND == GRAD_W ? a.splits : 1);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
@@ -663,11 +680,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     int s = 0, par = 1, issued = 0;  // slot, and parity of its last release (1: never used)
     bool ok = true;
     for (int t = pair; ok && t < tiles; t += pairs) {
-      int m, n;
-      tile_at(a, t, m, n);
+      int m, n, share, k_lo, nk;
+      work_at<KIND>(a, t, m, n, share, k_lo, nk);
       const int m0 = m * BM + static_cast<int>(rank) * 128;
       const int n0 = n * BN + static_cast<int>(rank) * 128;
-      for (int kc = 0; kc < a.nk; ++kc) {
+      for (int kc = 0; kc < nk; ++kc) {
         if (!mbar_wait_warp(&empty[s], par)) {
           raise_fault(FAULT_WAIT_EMPTY);
           ok = false;
@@ -677,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           uint8_t* sa = smem + s * STAGE;
           uint8_t* sb = sa + A_BYTES;
           const uint32_t bar = full_leader + 8 * s;
-          const int k0 = kc * BK;
+          const int k0 = (k_lo + kc) * BK;
           if (rank == 0) mbar_arrive_expect_tx(&full[s], kPairBytes);
           if (A_MN) {  // stored [K, M]: two boxes of 64 M x 64 K rows
             tma_load_2d_pair(sa, &map_a, bar, m0, k0);
@@ -721,12 +738,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       int s = 0, par = 0, q = 0;
       bool ok = true;
       for (int t = pair; ok && t < tiles; t += pairs) {
+        int m, n, share, k_lo, nk;
+        work_at<KIND>(a, t, m, n, share, k_lo, nk);
         int left = 0, acc = 0;  // chunks left of the accumulator's segment
-        for (int kc = 0; kc < a.nk; ++kc) {
+        for (int kc = 0; kc < nk; ++kc) {
           const bool first = left == 0;
           if (first) {
             acc = q & 1;
-            left = min(a.seg, a.nk - kc);
+            left = min(a.seg, nk - kc);
             if (q >= 2 && !mbar_wait_warp(&t_empty[acc], ((q >> 1) - 1) & 1)) {
               raise_fault(FAULT_WAIT_EMPTY);
               ok = false;
@@ -781,7 +800,7 @@ cudaError_t go(const TcMaps& m, const TcArgs& a, cudaStream_t st) {
   auto k = k_linear_tc<KIND, ACT, KEEP>;
   const cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(k), bytes);
   if (e != cudaSuccess) return e;
-  const long long tiles = static_cast<long long>(a.mt) * a.nt;
+  const long long tiles = static_cast<long long>(a.mt) * a.nt * (KIND == GRAD_W ? a.splits : 1);
   const int pairs = static_cast<int>(tiles < sm_count() / 2 ? tiles : sm_count() / 2);
   return launch_ex(k, dim3(2 * pairs), dim3(kThreads), bytes, st, 1, pdl_enabled(), m.a, m.b, m.y, m.z,
                    m.k, m.r, a);
@@ -822,7 +841,9 @@ cudaError_t launch_linear_tc(const LinearArgs& l, cudaStream_t st) {
   a.group = 8;
   const bool keep = l.zk.q || l.yk.q;
   a.seg = l.kind == GRAD_W ? 16 : keep ? 8 : a.nk;
-  if (static_cast<long long>(a.mt) * a.nt > 0x7fffffffll - 4096) return cudaErrorInvalidValue;
+  a.splits = l.kind == GRAD_W && l.splits > 1 ? l.splits : 1;
+  a.per = (a.nk + a.splits - 1) / a.splits;
+  if (static_cast<long long>(a.mt) * a.nt * a.splits > 0x7fffffffll - 4096) return cudaErrorInvalidValue;
   a.bias = l.bias;
   a.res = l.res;
   a.out = l.out;
@@ -831,6 +852,11 @@ cudaError_t launch_linear_tc(const LinearArgs& l, cudaStream_t st) {
   a.ck = l.ck;
   a.ld = l.ld;
   a.accumulate = l.accumulate;
+  if (a.splits > 1) {  // launch_split_sum scales, and adds to gw
+    a.bias = nullptr;
+    a.out = l.split_part;
+    a.accumulate = 0;
+  }
   a.sum_src = l.a;
   a.sum_part = l.sum_part;
   a.sum_parts = l.sum_parts;
@@ -845,7 +871,8 @@ cudaError_t launch_linear_tc(const LinearArgs& l, cudaStream_t st) {
     ok = map2(&m.a, l.a, l.M, l.K, 2ll * l.M, 64, BK, kBf) && map2(&m.b, l.b, l.N, l.K, 2ll * l.N, 64, BK, kBf);
   }
   if (l.kind == GRAD_W)
-    ok = ok && map2(&m.y, l.out, l.N, l.M, 4ll * l.N, 32, 128, CU_TENSOR_MAP_DATA_TYPE_FLOAT32);
+    ok = ok && map2(&m.y, a.out, l.N, a.splits > 1 ? static_cast<long long>(a.splits) * a.mt * BM : l.M, 4ll * l.N, 32,
+                    128, CU_TENSOR_MAP_DATA_TYPE_FLOAT32);
   else if (l.out)
     ok = ok && map2(&m.y, l.out, l.N, l.M, 2ll * l.N, 64, keep ? 32 : 128, kBf);
   for (const auto& [map, q] : {std::make_pair(&m.z, l.zk.q), std::make_pair(&m.k, l.yk.q)})

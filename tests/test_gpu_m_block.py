@@ -314,7 +314,7 @@ def test_linear_grad(torch, dtype, rows, Cy, Cx, act, res):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("rows,Cx,Cy", SHAPES + [(1571, 776, 768), (5000, 136, 264)])
+@pytest.mark.parametrize("rows,Cx,Cy", SHAPES + [(1571, 776, 768), (5000, 136, 264), (9001, 440, 1000), (12544, 448, 1792)])
 @pytest.mark.parametrize("scale", [False, True])
 def test_grad_w(torch, dtype, rows, Cx, Cy, scale):
     api = _api()
