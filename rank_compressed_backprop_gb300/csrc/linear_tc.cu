@@ -23,8 +23,8 @@
 //              halves' largest magnitudes: the larger byte is the group's.
 // The tensor cores' fp32 accumulation cuts low bits at every step, which adds
 // up over a long contraction (6e-6 of a 8192-token weight gradient).  Where the
-// output shows it (fp32 gradients, and checkpoints, whose codes flip) the
-// accumulator holds `seg` chunks at a time and the epilogue threads add the
+// output shows it (fp32 gradients: 16 chunks; and checkpoints, whose codes flip: see
+// kShortK) the accumulator holds `seg` chunks at a time and the epilogue threads add the
 // segments into registers in ordinary fp32, under the products of the next.
 // Operands contracted over their rows (w in back, gy and v in grad_w) are MN-major
 // operands read from their natural layout.  The residual comes by TMA into swizzled
@@ -35,7 +35,7 @@
 //
 // Bound: at 8192 x 11008 -> 4096 the tensor cores (393 us, 1.88 PFLOP/s; sustained 444,
 // 1.66 PFLOP/s, under the power limit, like a library matrix product of these sizes);
-// at 12544 x 448 -> 1792 the epilogue's instructions (17 us plain, 25 with gelu, 36 with
+// at 12544 x 448 -> 1792 the epilogue's instructions (18 us plain, 28 with gelu, 37 with
 // both checkpoints, for 11 us of products).
 #include <utility>
 
@@ -52,6 +52,13 @@ enum { FORWARD = 0, BACK = 1, GRAD_W = 2 };
 constexpr uint32_t STAGE = A_BYTES + B_BYTES;
 constexpr uint32_t BOX = 128 * 128;          // staging box: 128 rows x 128 bytes
 constexpr int kThreads = 640;
+// Chunks of a short contraction.  Its forward sums segments of four with or without
+// checkpoints, in the same code: both give the same bits, and the checkpoints' codes are
+// as near to exact sums as those after fp32 sums in order (12544 x 448 -> 1792, values
+// 9e-5 off with one segment of seven, 6e-5 either way else).  That costs 2 us of 26 to
+// 36 there.  Longer ones sum segments of eight, and only with checkpoints: fours took
+// 74 us instead of 60 at 8192 x 1024 -> 4096.
+constexpr int kShortK = 8;
 // Shared memory: the ring of chunks, the boxes through which epilogue operands
 // come in and results go out (64 columns of 128 rows for each group; where
 // checkpoints are written, of 32 rows for each warp), the tile's bias or column
@@ -345,7 +352,7 @@ __device__ __forceinline__ bool sum_segments(const TcArgs& a, int nk, uint32_t t
   return true;
 }
 
-// Forward with checkpoints.  A warp takes 32 rows x 64 columns through on its own:
+// Forward with checkpoints, or over a short contraction.  A warp takes 32 rows x 64 columns through on its own:
 // its own box for the residual and y, its own TMA operations; the codes, 64 bytes of
 // a row, through a second box (by plain stores, a row a thread, they took 4 us more at
 // 12544 x 448 -> 1792).  It meets only the warp with the other half
@@ -839,8 +846,8 @@ cudaError_t launch_linear_tc(const LinearArgs& l, cudaStream_t st) {
   a.nt = (l.N + BN - 1) / BN;
   a.nk = (l.K + BK - 1) / BK;
   a.group = 8;
-  const bool keep = l.zk.q || l.yk.q;
-  a.seg = l.kind == GRAD_W ? 16 : keep ? 8 : a.nk;
+  const bool keep = l.kind == FORWARD && (l.zk.q || l.yk.q || a.nk <= kShortK);
+  a.seg = l.kind == GRAD_W ? 16 : !keep ? a.nk : a.nk <= kShortK ? 4 : 8;
   a.splits = l.kind == GRAD_W && l.splits > 1 ? l.splits : 1;
   a.per = (a.nk + a.splits - 1) / a.splits;
   if (static_cast<long long>(a.mt) * a.nt * a.splits > 0x7fffffffll - 4096) return cudaErrorInvalidValue;
