@@ -61,7 +61,9 @@ constexpr int kThreads = 640;
 constexpr int kShortK = 8;
 // Shared memory: the ring of chunks, the boxes through which epilogue operands
 // come in and results go out (64 columns of 128 rows for each group, or of 32 rows
-// for each warp that goes through on its own), the tile's bias or column scale (a copy for each warp there, which takes a stage), scale bytes under exchange
+// for each warp that goes through on its own), the tile's bias or column scale, and
+// where checkpoints are written, at the cost of a stage, a box of codes for each warp
+// and scale bytes under exchange
 template <bool KEEP>
 struct Lay {
   static constexpr int ns = KEEP ? 4 : 5;
