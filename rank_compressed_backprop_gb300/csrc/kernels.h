@@ -377,7 +377,7 @@ struct TcArgs {
   int M, N, K;
   int mt, nt, nk;      // 256 x 256 tiles, 64-deep chunks
   int group;           // m tiles per rasterization group
-  int seg;             // chunks an accumulator holds before it is added up in registers
+  int seg, seg01;      // chunks an accumulator holds before it is added up in registers; a tile's first two
   const void* bias;    // [N] bf16 or null (grad_w: column scale)
   const void* res;     // [M, N] bf16 or null
   const void* out;     // null: no y

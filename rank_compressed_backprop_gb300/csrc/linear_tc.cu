@@ -56,9 +56,15 @@ constexpr int kThreads = 640;
 // checkpoints, in the same code: both give the same bits, and the checkpoints' codes are
 // as near to exact sums as those after fp32 sums in order (12544 x 448 -> 1792, values
 // 9e-5 off with one segment of seven, 6e-5 either way else).  That costs 2 us of 26 to
-// 36 there.  Longer ones sum segments of eight, and only with checkpoints: fours took
-// 74 us instead of 60 at 8192 x 1024 -> 4096.
+// 36 there.  Longer ones sum segments of six, from 17 chunks on eight, and only with
+// checkpoints: at 8192 x 1024 -> 4096 fours took 74 us, sixes 66, eights 60, with codes
+// up to 1.7 times as far off as fp32 sums where sixes are 1.5 (576 channels).
 constexpr int kShortK = 8;
+// Over a long one the first two segments, whose products run under the epilogue of the
+// tile before, are sixteens: with eights that epilogue (7 us) outlasted them and the
+// tensor cores stood (8192 x 4096 -> 11008 with gelu and both checkpoints 510 us instead of
+// 478, 4096 x 4096 -> 4096 103 instead of 99).
+constexpr int kLongK = 64;
 // Shared memory: the ring of chunks, the boxes through which epilogue operands
 // come in and results go out (64 columns of 128 rows for each group, or of 32 rows
 // for each warp that goes through on its own), the tile's bias or column scale, and
@@ -229,6 +235,9 @@ __device__ __forceinline__ void work_at(const TcArgs& a, int t, int& m, int& n, 
   tile_at(a, t, m, n);
 }
 
+// chunks of a tile's i-th segment: the first two run under the epilogue of the tile before
+__device__ __forceinline__ int segment(const TcArgs& a, int i) { return i < 2 ? a.seg01 : a.seg; }
+
 // 32 columns of this warp's 32 lanes, no wait
 __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t* r) {
   asm volatile(
@@ -333,7 +342,7 @@ __device__ __forceinline__ void make_codes(uint4 (&q)[4], uint32_t code, const f
 template <typename Release>
 __device__ __forceinline__ bool sum_segments(const TcArgs& a, int nk, uint32_t tbase, uint64_t* t_full, int id, int count,
                                              int& q, float2* v, const Release& release) {
-  for (int k0 = 0; k0 < nk; k0 += a.seg, ++q) {
+  for (int i = 0, k0 = 0; k0 < nk; k0 += segment(a, i), ++i, ++q) {
     const int acc = q & 1;
     if (!mbar_wait_group(&t_full[acc], (q >> 1) & 1, id, count)) return false;
     tc_fence_after();
@@ -756,12 +765,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       for (int t = pair; ok && t < tiles; t += pairs) {
         int m, n, share, k_lo, nk;
         work_at<KIND>(a, t, m, n, share, k_lo, nk);
-        int left = 0, acc = 0;  // chunks left of the accumulator's segment
+        int left = 0, acc = 0, i = 0;  // chunks left of the accumulator's segment, segments begun
         for (int kc = 0; kc < nk; ++kc) {
           const bool first = left == 0;
           if (first) {
             acc = q & 1;
-            left = min(a.seg, nk - kc);
+            left = min(segment(a, i++), nk - kc);
             if (q >= 2 && !mbar_wait_warp(&t_empty[acc], ((q >> 1) - 1) & 1)) {
               raise_fault(FAULT_WAIT_EMPTY);
               ok = false;
@@ -856,7 +865,8 @@ cudaError_t launch_linear_tc(const LinearArgs& l, cudaStream_t st) {
   a.nk = (l.K + BK - 1) / BK;
   a.group = 8;
   const bool keep = l.kind == FORWARD && (l.zk.q || l.yk.q || a.nk <= kShortK);
-  a.seg = l.kind == GRAD_W ? 16 : !keep ? a.nk : a.nk <= kShortK ? 4 : 8;
+  a.seg = l.kind == GRAD_W ? 16 : !keep ? a.nk : a.nk <= kShortK ? 4 : a.nk <= 2 * kShortK ? 6 : 8;
+  a.seg01 = keep && a.nk >= kLongK ? 2 * a.seg : a.seg;
   a.splits = l.kind == GRAD_W && l.splits > 1 ? l.splits : 1;
   a.per = (a.nk + a.splits - 1) / a.splits;
   if (static_cast<long long>(a.mt) * a.nt * a.splits > 0x7fffffffll - 4096) return cudaErrorInvalidValue;
