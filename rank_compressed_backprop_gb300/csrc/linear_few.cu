@@ -159,7 +159,8 @@ __global__ void __launch_bounds__(kThreads)
   constexpr bool A_MN = KIND != FORWARD, B_MN = KIND == GRAD_W;
   constexpr int NS = stages_of(NT);
   constexpr uint32_t STAGE = stage_of(NT);
-  constexpr int COLS = NT < 32 ? 32 : NT;  // TMEM columns (a power of two, 32 at least)
+  constexpr int COLS = NT <= 16 ? 64 : 128;  // TMEM columns
+  constexpr int ACCS = COLS / NT;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -175,6 +176,9 @@ __global__ void __launch_bounds__(kThreads)
   const int rank = blockIdx.z;      // == rank in the cluster (1 x 1 x splits)
   const int k_begin = rank * a.per;
   const int nk = max(0, min(a.nk - k_begin, a.per));
+  // segments of at least four chunks, each in an accumulator of its own: the tensor
+  // cores' sums cut low bits at every step, and the segments are added in fp32
+  const int seg = max(4, (nk + ACCS - 1) / ACCS);
 
   auto load_a = [&](uint8_t* dst, int k0, uint64_t* bar) {
     if (A_MN) {  // stored [K, N]: two boxes of 64 channels x 64 K rows
@@ -253,7 +257,7 @@ __global__ void __launch_bounds__(kThreads)
     const uint32_t base = smem_u32(smem);
     const uint64_t a_desc0 = A_MN ? sdesc_sw128(base, A_BYTES / 2, 1024) : sdesc_sw128(base, 16, 1024);
     const uint64_t b_desc0 = B_MN ? sdesc_sw128(base + A_BYTES, 64 * BK * 2, 1024) : sdesc_sw128(base + A_BYTES, 16, 1024);
-    int s = 0, par = 0;
+    int s = 0, par = 0, acc = 0, left = seg;  // accumulator and what its segment lacks
     for (int i = 0; i < nk; ++i) {
       if (!__all_sync(0xffffffffu, mbar_wait(&full[s], par))) {
         raise_fault(FAULT_WAIT_FULL);
@@ -263,12 +267,16 @@ __global__ void __launch_bounds__(kThreads)
       if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < BK / 16; ++kk)
-          umma_bf16(tmem, a_desc0 + s * (STAGE >> 4) + kk * (A_MN ? 2048 >> 4 : 32 >> 4),
-                    b_desc0 + s * (STAGE >> 4) + kk * (B_MN ? 2048 >> 4 : 32 >> 4), idesc, (i | kk) != 0);
+          umma_bf16(tmem + acc * NT, a_desc0 + s * (STAGE >> 4) + kk * (A_MN ? 2048 >> 4 : 32 >> 4),
+                    b_desc0 + s * (STAGE >> 4) + kk * (B_MN ? 2048 >> 4 : 32 >> 4), idesc, left != seg || kk != 0);
         umma_commit(&empty[s]);
         if (i == nk - 1) umma_commit(done);
       }
       __syncwarp();
+      if (--left == 0) {
+        ++acc;
+        left = seg;
+      }
       if (++s == NS) {
         s = 0;
         par ^= 1;
@@ -288,11 +296,14 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll 1
     for (int j0 = 16 * (warp >> 2); j0 < NT; j0 += 32) {
       float v[16];
-      if (nk > 0) {
-        tmem_ld16(taddr + j0, v);
-      } else {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = 0.f;
+      for (int j = 0; j < 16; ++j) v[j] = 0.f;
+#pragma unroll 1
+      for (int acc = 0; acc * seg < nk; ++acc) {
+        float w[16];
+        tmem_ld16(taddr + acc * NT + j0, w);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] += w[j];
       }
 #pragma unroll
       for (int j = 0; j < 16; ++j) red[(j0 + j) * LD + ch] = v[j];
@@ -381,7 +392,10 @@ cudaError_t go_rows(int nt, const CUtensorMap& ma, const CUtensorMap& mb, const 
 
 int few_rows_tile(const LinearArgs& l) {
   int nt = l.kind == GRAD_W ? 64 : 16;  // an MN-major operand comes in 64-wide boxes
-  while (nt < 128 && nt < l.M) nt *= 2;
+  // checkpoints, whose codes show the sums' low bits: two accumulators of 64 rows rather
+  // than one of 128
+  const int most = l.zk.q || l.yk.q ? 64 : 128;
+  while (nt < most && nt < l.M) nt *= 2;
   return nt;
 }
 

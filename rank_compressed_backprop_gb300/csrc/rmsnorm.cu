@@ -109,7 +109,8 @@ __global__ void __launch_bounds__(W > 8 ? 32 * W : 256)
     }
     add_squares(h[v], ss);
   }
-  const float r = rsqrtf(row_sum<W>(ss.x + ss.y, red, warp) / static_cast<float>(a.C) + a.eps);
+  // correctly rounded: an error of r shifts the whole row, and codes near the middle of two flip
+  const float r = __frsqrt_rn(row_sum<W>(ss.x + ss.y, red, warp) / static_cast<float>(a.C) + a.eps);
   if (!on) return;  // a whole warp at a time
   norm_outputs<T, W, V, VEC>(a, h, r, row, t, [&](int v, float2* g) {
     const int c = 8 * (v * 32 * W + t);
