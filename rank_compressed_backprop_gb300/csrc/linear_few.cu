@@ -256,7 +256,8 @@ __global__ void __launch_bounds__(kThreads)
     constexpr uint32_t idesc = idesc_bf16_f32(BM, NT, A_MN, B_MN);
     const uint32_t base = smem_u32(smem);
     const uint64_t a_desc0 = A_MN ? sdesc_sw128(base, A_BYTES / 2, 1024) : sdesc_sw128(base, 16, 1024);
-    const uint64_t b_desc0 = B_MN ? sdesc_sw128(base + A_BYTES, 64 * BK * 2, 1024) : sdesc_sw128(base + A_BYTES, 16, 1024);
+    const uint64_t b_desc0 =
+        B_MN ? sdesc_sw128(base + A_BYTES, 64 * BK * 2, 1024) : sdesc_sw128(base + A_BYTES, 16, 1024);
     int s = 0, par = 0, acc = 0, left = seg;  // accumulator and what its segment lacks
     for (int i = 0; i < nk; ++i) {
       if (!__all_sync(0xffffffffu, mbar_wait(&full[s], par))) {

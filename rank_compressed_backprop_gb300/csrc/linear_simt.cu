@@ -219,11 +219,12 @@ __global__ void __launch_bounds__(32 * BM / R) k_linear_simt(LinearArgs a, int s
     const size_t base = static_cast<size_t>(m) * a.N + n0 + lane;
     // global operands are asked for before the peers' partial sums
     const bool slopes = KIND == BACK && a.act != INSTANT_ACT_NONE;
+    const int8_t* q = a.ck.q + static_cast<size_t>(m) * a.ld + n0 + lane;
     float scale = 0.f, z[4], res[4];
     if (slopes) scale = ckpt_scale(__ldg(a.ck.s + static_cast<size_t>(n0 / kCkptGroup) * a.M + m));
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      z[j] = slopes && on[j] ? static_cast<float>(__ldg(a.ck.q + static_cast<size_t>(m) * a.ld + n0 + lane + 32 * j)) : 0.f;
+      z[j] = slopes && on[j] ? static_cast<float>(__ldg(q + 32 * j)) : 0.f;
       res[j] = KIND != GRAD_W && a.res && on[j] ? static_cast<const float*>(a.res)[base + 32 * j] : 0.f;
     }
     const float* src = buf + i * BN + lane;

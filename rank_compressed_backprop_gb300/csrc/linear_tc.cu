@@ -20,7 +20,7 @@
 //              two warps on each scheduler, whose latencies showed: 12544 x 448 ->
 //              1792 with gelu and both checkpoints 53 us.)  Two groups share the 128
 //              columns of a checkpoint group and exchange the scale byte of their
-//              halves' largest magnitudes: the larger byte is the group's.
+//              halves' largest magnitudes: the larger byte is the group's
 // The tensor cores' fp32 accumulation cuts low bits at every step, which adds
 // up over a long contraction (6e-6 of a 8192-token weight gradient).  Where the
 // output shows it (fp32 gradients: 16 chunks; and checkpoints, whose codes flip: see
@@ -55,7 +55,7 @@ constexpr int kThreads = 640;
 // Chunks of a short contraction.  Its forward sums segments of four with or without
 // checkpoints, in the same code: both give the same bits, and the checkpoints' codes are
 // as near to exact sums as those after fp32 sums in order (12544 x 448 -> 1792, values
-// 9e-5 off with one segment of seven, 6e-5 either way else).  That costs 2 us of 26 to
+// 9e-5 off with one segment of seven, 6e-5 with these and after fp32 sums).  That costs 2 us of 26 to
 // 36 there.  Longer ones sum segments of six, from 17 chunks on eight, and only with
 // checkpoints: at 8192 x 1024 -> 4096 fours took 74 us, sixes 66, eights 60, with codes
 // up to 1.7 times as far off as fp32 sums where sixes are 1.5 (576 channels).
@@ -340,8 +340,8 @@ __device__ __forceinline__ void make_codes(uint4 (&q)[4], uint32_t code, const f
 // One accumulator segment after the other into v, 64 columns of a row a thread.
 // `release(acc)` hands the accumulator back; ids and count as in mbar_wait_group.
 template <typename Release>
-__device__ __forceinline__ bool sum_segments(const TcArgs& a, int nk, uint32_t tbase, uint64_t* t_full, int id, int count,
-                                             int& q, float2* v, const Release& release) {
+__device__ __forceinline__ bool sum_segments(const TcArgs& a, int nk, uint32_t tbase, uint64_t* t_full, int id,
+                                             int count, int& q, float2* v, const Release& release) {
   for (int i = 0, k0 = 0; k0 < nk; k0 += segment(a, i), ++i, ++q) {
     const int acc = q & 1;
     if (!mbar_wait_group(&t_full[acc], (q >> 1) & 1, id, count)) return false;
