@@ -35,7 +35,7 @@
 //
 // Bound: at 8192 x 11008 -> 4096 the tensor cores (393 us, 1.88 PFLOP/s; sustained 444,
 // 1.66 PFLOP/s, under the power limit, like a library matrix product of these sizes);
-// at 12544 x 448 -> 1792 the epilogue's instructions (18 us plain, 28 with gelu, 37 with
+// at 12544 x 448 -> 1792 the epilogue's instructions (20 us plain, 34 with gelu, 42 with
 // both checkpoints, for 11 us of products).
 #include <utility>
 
@@ -52,13 +52,14 @@ enum { FORWARD = 0, BACK = 1, GRAD_W = 2 };
 constexpr uint32_t STAGE = A_BYTES + B_BYTES;
 constexpr uint32_t BOX = 128 * 128;          // staging box: 128 rows x 128 bytes
 constexpr int kThreads = 640;
-// Chunks of a short contraction.  Its forward sums segments of four with or without
-// checkpoints, in the same code: both give the same bits, and the checkpoints' codes are
-// as near to exact sums as those after fp32 sums in order (12544 x 448 -> 1792, values
-// 9e-5 off with one segment of seven, 6e-5 with these and after fp32 sums).  That costs 2 us of 26 to
-// 36 there.  Longer ones sum segments of six, from 17 chunks on eight, and only with
-// checkpoints: at 8192 x 1024 -> 4096 fours took 74 us, sixes 66, eights 60, with codes
-// up to 1.7 times as far off as fp32 sums where sixes are 1.5 (576 channels).
+// Chunks of a short contraction.  Its forward sums segments of three with or without
+// checkpoints, in the same code: both give the same bits, and as few of the checkpoints'
+// codes differ from those of exact sums as after fp32 sums in order (of the 22 million of
+// 12544 x 448 -> 1792 82 to 104, after fp32 sums 78 to 87; with fours 112 to 141).  That
+// costs 4 us of 37 against fours there, and 8 of 26 without checkpoints against one
+// segment.  Longer ones sum segments of six, from 17 chunks on eight, and only with
+// checkpoints: at 8192 x 1024 -> 4096 fours took 74 us, sixes 66, eights 60, with values
+// up to 1.7 times as far off as after fp32 sums where sixes are 1.5 (576 channels).
 constexpr int kShortK = 8;
 // Over a long one the first two segments, whose products run under the epilogue of the
 // tile before, are sixteens: with eights that epilogue (7 us) outlasted them and the
@@ -865,7 +866,7 @@ cudaError_t launch_linear_tc(const LinearArgs& l, cudaStream_t st) {
   a.nk = (l.K + BK - 1) / BK;
   a.group = 8;
   const bool keep = l.kind == FORWARD && (l.zk.q || l.yk.q || a.nk <= kShortK);
-  a.seg = l.kind == GRAD_W ? 16 : !keep ? a.nk : a.nk <= kShortK ? 4 : a.nk <= 2 * kShortK ? 6 : 8;
+  a.seg = l.kind == GRAD_W ? 16 : !keep ? a.nk : a.nk <= kShortK ? 3 : a.nk <= 2 * kShortK ? 6 : 8;
   a.seg01 = keep && a.nk >= kLongK ? 2 * a.seg : a.seg;
   a.splits = l.kind == GRAD_W && l.splits > 1 ? l.splits : 1;
   a.per = (a.nk + a.splits - 1) / a.splits;
