@@ -439,7 +439,11 @@ __device__ __forceinline__ void epilogue_keep(const TcArgs& a, const CUtensorMap
       make_codes(codes, code, v);
       if (half == 0 && on) k.s[scale_at] = static_cast<uint8_t>(code);
       if (second) {
-        if (lane == 0) tma_store_wait_read<1>();  // z's codes have left, y may not
+        // z's codes have left; y, whose store came after theirs, may not
+        if (lane == 0) {
+          if (a.out) tma_store_wait_read<1>();
+          else tma_store_wait_read<0>();
+        }
         __syncwarp();
       }
 #pragma unroll

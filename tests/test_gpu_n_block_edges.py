@@ -1,0 +1,56 @@
+"""MLP-block operators at the edges of what their header promises: outputs left
+out, scratch on side streams, very many rows, tails and infinities of the
+activations, long sums, and calls that are refused."""
+
+import numpy as np
+import pytest
+
+from gpu_util import nan_like, rng, stored, to_dev, to_np, torch_or_skip
+from oracle import block_oracle as O
+from oracle import decode
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def torch():
+    return torch_or_skip()
+
+
+def _api():
+    from rank_compressed_backprop_gb300 import api
+
+    return api
+
+
+def blank_ckpt(torch, rows, C):
+    q, s = _api().ckpt_buffers(rows, C, "cuda")
+    return q.fill_(77), s.fill_(3)
+
+
+# ---------------------------------------------------------------------------
+# outputs left out: the same bits in what is asked for
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("rows,Cx,Cy", [(8192, 448, 1792), (4096, 1024, 1288), (20000, 64, 136), (33, 264, 448)])
+@pytest.mark.parametrize("act,res", [("none", True), ("none", False), ("gelu", True), ("relu", False)])
+def test_outputs_left_out(torch, rows, Cx, Cy, act, res):
+    """y may be left out when its checkpoint is asked for, and each checkpoint too."""
+    api = _api()
+    gen = torch.Generator("cuda").manual_seed(rows + Cx)
+    rn = lambda *s: torch.randn(*s, generator=gen, device="cuda").bfloat16()  # noqa: E731
+    x, w, b = rn(rows, Cx), rn(Cy, Cx) * Cx ** -0.5, rn(Cy)
+    kw = dict(bias=b, act=act, residual=rn(rows, Cy) if res else None)
+    y = nan_like(torch, (rows, Cy), torch.bfloat16)
+    z0, y0 = blank_ckpt(torch, rows, Cy), blank_ckpt(torch, rows, Cy)
+    api.linear_act(x, w, y, zq=z0[0], zs=z0[1], yq=y0[0], ys=y0[1], **kw)
+    for with_y, with_z, with_yk in [(False, True, True)] * 4 + [(False, False, True), (True, True, False),
+                                                              (True, False, True)]:
+        out = nan_like(torch, (rows, Cy), torch.bfloat16) if with_y else None
+        z1, y1 = blank_ckpt(torch, rows, Cy), blank_ckpt(torch, rows, Cy)
+        got = api.linear_act(x, w, out, zq=z1[0] if with_z else None, zs=z1[1] if with_z else None,
+                             yq=y1[0] if with_yk else None, ys=y1[1] if with_yk else None, **kw)
+        assert got is out and (out is None or torch.equal(out, y))
+        for asked, a, k in ((with_z, z0, z1), (with_yk, y0, y1)):
+            if asked:
+                assert torch.equal(a[0][:, :Cy], k[0][:, :Cy]) and torch.equal(a[1], k[1])
+    assert api.device_status() == 0
