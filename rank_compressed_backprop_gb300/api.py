@@ -88,6 +88,13 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+def _on_stream(stream):
+    """Context in which torch allocates for the stream that a call runs on."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return torch.cuda.stream(stream)
+    return torch.cuda.stream(torch.cuda.ExternalStream(int(stream)))
+
+
 def _same_dtype(dt, *pairs):
     for name, t in pairs:
         if t.dtype != dt:
@@ -700,10 +707,10 @@ def ckpt_grad_w(g_y: torch.Tensor, q: torch.Tensor, s: torch.Tensor, gw: torch.T
                 ("col_scale", col_scale, (Cx,), dt), ("gb", gb, (Cy,), f32),
                 ckpts=[(q, s, rows, Cx, ("q", "s"))])
     if ws is None and dt == torch.bfloat16:
-        ws = ckpt_grad_w_workspace(rows, Cx, Cy, g_y.device)
-        if stream is not None:
-            ws.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                             else torch.cuda.ExternalStream(int(stream)))
+        # from the pool of the stream that uses it: a block freed on another stream may
+        # still be in use there
+        with _on_stream(stream):
+            ws = ckpt_grad_w_workspace(rows, Cx, Cy, g_y.device)
     check(lib().instant_ckpt_grad_w(*p, int(accumulate), None if ws is None else _dev(ws, "ws"),
                                     0 if ws is None else ws.numel() * ws.element_size(), rows, Cx, Cy,
                                     dtype_code(dt), _stream(stream)), "instant_ckpt_grad_w")

@@ -54,3 +54,36 @@ def test_outputs_left_out(torch, rows, Cx, Cy, act, res):
             if asked:
                 assert torch.equal(a[0][:, :Cy], k[0][:, :Cy]) and torch.equal(a[1], k[1])
     assert api.device_status() == 0
+
+
+# ---------------------------------------------------------------------------
+# streams
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("handle", [False, True])
+def test_own_workspace_on_a_side_stream(torch, handle):
+    """A call that allocates its workspace does so on the stream it runs on: a block
+    that the current stream has freed but not yet finished with stays as it is."""
+    api = _api()
+    rows, Cx, Cy = 4096, 512, 256
+    gen = torch.Generator("cuda").manual_seed(5)
+    g = torch.randn(rows, Cy, generator=gen, device="cuda").bfloat16()
+    x = torch.randn(rows, Cx, generator=gen, device="cuda").bfloat16()
+    q, s = blank_ckpt(torch, rows, Cx)
+    api.ckpt_pack(x, q, s)
+    want = nan_like(torch, (Cy, Cx), torch.float32)
+    api.ckpt_grad_w(g, q, s, want)
+    n = api.ckpt_grad_w_workspace(rows, Cx, Cy, "cuda").numel()
+    kept = torch.empty(n, dtype=torch.uint8, device="cuda")
+    got = nan_like(torch, (Cy, Cx), torch.float32)
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    block = torch.full((n,), 7, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)          # some 50 ms
+    kept.copy_(block)
+    del block                               # free for the current stream, its copy still to come
+    api.ckpt_grad_w(g, q, s, got, stream=st.cuda_stream if handle else st)
+    torch.cuda.synchronize()
+    assert bool((kept == 7).all())
+    assert torch.equal(got, want)
