@@ -91,6 +91,7 @@ double pairs_us(const LinearArgs& a) {
 
 bool runs_on_pairs(const LinearArgs& a) {
   const int nt = few_rows_tile(a);
+  if (cdiv(a.M, nt) > kFewMaxRowTiles) return true;  // narrow products of millions of rows
   const double chunk_us = nt == 128 ? 0.28 : nt == 64 ? 0.15 : 0.13;
   return pairs_us(a) <= 8.0 + chunk_us * cdiv(a.K, 64) * cdiv(a.N, 128) * cdiv(a.M, nt) / sm_count();
 }

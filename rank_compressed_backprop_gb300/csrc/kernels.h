@@ -410,6 +410,7 @@ struct FewArgs {
   CkptRef zk, yk, ck;
   int ld, act, accumulate;
 };
+constexpr int kFewMaxRowTiles = 65535;   // they lie on the grid's second axis
 int few_rows_tile(const LinearArgs& a);  // its row tile for this product: 16, 32, 64 or 128
 cudaError_t launch_linear_few(const LinearArgs& a, cudaStream_t st);
 

@@ -416,7 +416,7 @@ cudaError_t launch_linear_few(const LinearArgs& l, cudaStream_t st) {
   a.act = l.act;
   a.accumulate = l.accumulate;
   const int nt = few_rows_tile(l);
-  if ((l.M + nt - 1) / nt > 65535) return cudaErrorInvalidValue;
+  if ((l.M + nt - 1) / nt > kFewMaxRowTiles) return cudaErrorInvalidValue;
   CUtensorMap ma, mb;
   auto map = [](CUtensorMap* m, const void* p, long long inner, long long outer, int box_outer) {
     const uint64_t d[2] = {static_cast<uint64_t>(inner), static_cast<uint64_t>(outer)};

@@ -87,3 +87,36 @@ def test_own_workspace_on_a_side_stream(torch, handle):
     torch.cuda.synchronize()
     assert bool((kept == 7).all())
     assert torch.equal(got, want)
+
+
+# ---------------------------------------------------------------------------
+# narrow products of more row tiles than a grid has in y
+# ---------------------------------------------------------------------------
+def test_narrow_products_of_very_many_rows(torch):
+    """8.4 million rows of 64 channels: over 65535 tiles of 128 rows."""
+    api = _api()
+    rows, C = 65535 * 128 + 8, 64
+    gen = torch.Generator("cuda").manual_seed(3)
+    x = torch.randint(-3, 4, (rows, C), generator=gen, device="cuda").bfloat16()
+    w = torch.randint(-2, 3, (C, C), generator=gen, device="cuda").bfloat16()
+    some = torch.tensor([0, 1, rows // 2, 65535 * 128 - 1, 65535 * 128, rows - 2, rows - 1], device="cuda")
+    y = nan_like(torch, (rows, C), torch.bfloat16)
+    api.linear_act(x, w, y)                 # whole numbers of up to 384: exact in fp32, rounded once
+    assert torch.equal(y[some].double(), (x[some].double() @ w.double().t()).bfloat16().double())
+    assert not bool(y.isnan().any())
+    y.fill_(float("nan"))
+    api.linear_act_grad(x, w, y)
+    assert torch.equal(y[some].double(), (x[some].double() @ w.double()).bfloat16().double())
+    assert not bool(y.isnan().any())
+    del y
+    # a layer of that many outputs: its weight gradient over 64 rows
+    g = x.view(C, rows)                     # [64, rows]
+    t = torch.randint(-3, 4, (C, C), generator=gen, device="cuda").bfloat16()
+    q, s = blank_ckpt(torch, C, C)
+    api.ckpt_pack(t, q, s)
+    gw, gb = nan_like(torch, (rows, C), torch.float32), nan_like(torch, (rows,), torch.float32)
+    api.ckpt_grad_w(g, q, s, gw, api.ckpt_grad_w_workspace(C, C, rows, "cuda"), gb=gb)
+    assert torch.equal(gw[some].double(), g[:, some].double().t() @ t.double())
+    assert torch.equal(gb[some].double(), g[:, some].double().sum(0))
+    assert not bool(gw.isnan().any()) and not bool(gb.isnan().any())
+    assert api.device_status() == 0
