@@ -120,3 +120,27 @@ def test_narrow_products_of_very_many_rows(torch):
     assert torch.equal(gb[some].double(), g[:, some].double().sum(0))
     assert not bool(gw.isnan().any()) and not bool(gb.isnan().any())
     assert api.device_status() == 0
+
+
+# ---------------------------------------------------------------------------
+# tails and infinities of the activations
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,Cy", [(32, 128), (320, 128), (32, 2048)])
+def test_gelu_slope_in_its_negative_tail(torch, dtype, rows, Cy):
+    """gelu'(z) = Phi(z) + z phi(z) keeps its relative accuracy down to z = -10.
+
+    Bound: both terms hold exp(-z^2 / 2), whose argument has two roundings: up to
+    2^-23 z^2 / 2, at most 6e-6 of the term, and 1e-6 for the functions themselves;
+    the terms differ in sign and add up to at most 1.6 times the slope from -2 on."""
+    api = _api()
+    z = np.sort(-2 - 8 * np.linspace(0, 1, 32 * 128)).reshape(32, 128)
+    wq, wsc = (np.ascontiguousarray(np.tile(a, t)) for a, t in
+               zip(O.ckpt_encode(z), ((rows // 32, 1), (1, rows // 32))))
+    q, s = torch.from_numpy(wq).cuda(), torch.from_numpy(wsc).cuda()
+    eye, one = (to_dev(stored(a, dtype)) for a in (np.eye(Cy, 128), np.ones((rows, Cy))))
+    gx = torch.full((rows, 128), float("nan"), dtype=one.dtype, device="cuda")
+    api.linear_act_grad(one, eye, gx, act="gelu", zq=q, zs=s)
+    want = O.act_slope(O.ckpt_decode(wq, wsc, 128), "gelu")
+    err = np.abs(to_np(gx) - want) / np.abs(want)
+    assert err.max() <= (2.0 ** -8 if dtype == "bf16" else 2.0 ** -24) + 2.0 ** -15
