@@ -193,10 +193,9 @@ __device__ __forceinline__ float act_slope_f32(float z, int act) {
 // with M(t) = erfcx(t / sqrt 2) / 2, which falls smoothly from 1/2 like 1 / t; M is
 // a degree-8 polynomial in 1 / (1 + 0.235 t) without constant term, fitted by
 // weighted least squares on [0, 16] to 1.2e-7 relative (5e-7 evaluated in fp32), so
-// the negative tail keeps its relative accuracy.  t is cut at 40, where Phi(-t) is 0 in fp32, so that an
-// infinite z meets no 0 * inf.  Error with the approximate exponential and
-// reciprocal: gelu 8e-6 relative at z = -13, where the roundings of z^2 / 2 count most,
-// 1.5e-6 from -4 on; gelu' 6e-7, below -1 relative like gelu.
+// the negative tail keeps its relative accuracy.  Error with the approximate
+// exponential and reciprocal: gelu 8e-6 relative at z = -13, where the roundings of
+// z^2 / 2 count most, 1.5e-6 from -4 on; gelu' 6e-7, below -1 relative like gelu.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float rcp_approx(float x) {
   float r;
@@ -236,10 +235,9 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-// t = min(|z|, 40), e = exp(-z^2 / 2), Phi(-t)
-__device__ __forceinline__ float2 normal_tail(float2 z, float2& t, float2& e) {
-  t = make_float2(fminf(fabsf(z.x), 40.f), fminf(fabsf(z.y), 40.f));
-  const float2 s = make_float2(rcp_approx(fmaf(0.235f, t.x, 1.f)), rcp_approx(fmaf(0.235f, t.y, 1.f)));
+// Phi(-|z|), and e = exp(-z^2 / 2)
+__device__ __forceinline__ float2 normal_tail(float2 z, float2& e) {
+  const float2 s = make_float2(rcp_approx(fmaf(0.235f, fabsf(z.x), 1.f)), rcp_approx(fmaf(0.235f, fabsf(z.y), 1.f)));
   float2 m = fma2(both(-0.064109147f), s, both(0.21002914f));
   m = fma2(m, s, both(-0.14554477f));
   m = fma2(m, s, both(0.17967278f));
@@ -256,9 +254,12 @@ template <int ACT>
 __device__ __forceinline__ float2 act_fast(float2 z) {
   if (ACT == INSTANT_ACT_RELU) return make_float2(z.x < 0.f ? 0.f : z.x, z.y < 0.f ? 0.f : z.y);
   if (ACT == INSTANT_ACT_GELU) {
-    float2 t, e;
-    const float2 p = normal_tail(z, t, e);
-    return make_float2(fmaf(-t.x, p.x, fmaxf(z.x, 0.f)), fmaf(-t.y, p.y, fmaxf(z.y, 0.f)));
+    float2 e;
+    const float2 p = normal_tail(z, e);
+    // -|z|, cut at -40 above zero, where the tail is 0 in fp32: plus infinity then meets no
+    // 0 * inf, and minus infinity does, as in the formula
+    const float2 n = make_float2(fminf(z.x, fmaxf(-z.x, -40.f)), fminf(z.y, fmaxf(-z.y, -40.f)));
+    return make_float2(fmaf(n.x, p.x, fmaxf(z.x, 0.f)), fmaf(n.y, p.y, fmaxf(z.y, 0.f)));
   }
   if (ACT == INSTANT_ACT_SILU) {
     const float2 x = mul2(z, both(-1.44269504f));
@@ -275,8 +276,8 @@ __device__ __forceinline__ float2 act_slope_fast(float2 z) {
   if (ACT == INSTANT_ACT_GELU) {
     // Phi(z) and z times the density.  Below zero Phi(z) is the tail itself: one minus
     // it and back would leave nothing of it (gelu'(-5.5) was 3 % off)
-    float2 t, e;
-    const float2 p = normal_tail(z, t, e);
+    float2 e;
+    const float2 p = normal_tail(z, e);
     const float2 h = fma2(p, both(-1.f), both(1.f));
     const float2 c = make_float2(z.x < 0.f ? p.x : h.x, z.y < 0.f ? p.y : h.y);
     return fma2(mul2(z, both(0.39894228f)), e, c);

@@ -144,3 +144,26 @@ def test_gelu_slope_in_its_negative_tail(torch, dtype, rows, Cy):
     want = O.act_slope(O.ckpt_decode(wq, wsc, 128), "gelu")
     err = np.abs(to_np(gx) - want) / np.abs(want)
     assert err.max() <= (2.0 ** -8 if dtype == "bf16" else 2.0 ** -24) + 2.0 ** -15
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,Cx", [(6, 64), (300, 64), (6, 2048)])
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "silu"])
+def test_activations_of_infinities(torch, dtype, rows, Cx, act):
+    """act(+-inf) and act(NaN) are what the formula says, whatever the type and size:
+    relu(-inf) is 0, z Phi(z) and z / (1 + exp(-z)) have no value at -inf."""
+    api = _api()
+    x = np.ones((rows, Cx))
+    x[[1, 2, 4], 5] = [np.inf, -np.inf, np.nan]
+    w = np.full((256, Cx), 1 / Cx)
+    y = nan_like(torch, (rows, 256), torch.float32 if dtype == "f32" else torch.bfloat16).fill_(3)
+    yq, ys = blank_ckpt(torch, rows, 256)
+    for kw in (dict(), dict(yq=yq, ys=ys)):
+        api.linear_act(to_dev(stored(x, dtype)), to_dev(stored(w, dtype)), y, act=act, **kw)
+        with np.errstate(invalid="ignore", over="ignore"):
+            want = O.act(x @ w.T, act)
+        assert np.array_equal(np.isnan(to_np(y)), np.isnan(want))
+        assert np.array_equal(np.isinf(to_np(y)), np.isinf(want))
+        assert np.abs(to_np(y)[0] - want[0]).max() <= 2.0 ** -8
+    bad = ~np.isfinite(want[:, 0])
+    assert np.array_equal(np.isnan(O.ckpt_decode(yq.cpu().numpy(), ys.cpu().numpy(), 256)).all(1), bad)
