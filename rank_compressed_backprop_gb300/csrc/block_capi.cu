@@ -74,14 +74,15 @@ int grad_w_splits(int M, int N, int K) {
 // kernels the one with the smaller estimate runs:
 //   CTA pairs, 256 x 256 tiles      4.5 us + 0.30 us a chunk of 64 and wave of 76 tiles
 //   split K, 128 x NT tiles         8 us + 0.28 us (NT = 128), 0.15 (64) or 0.13 a
-//                                   chunk, over the SMs
-// which are fits to both kernels timed over 21 shapes of each product; of these 63 the
-// estimate takes the slower kernel four times, by 14 % at most.  Measured
+//                                   chunk, over the SMs; weight gradients: few_grad_w_us
+// which are fits to both kernels timed over 21 shapes of forward and of back and 29 of the
+// weight gradient.  Measured
 // (rows x K -> N, split K against pairs, us): forward 1 x 4096 -> 11008 15.8 / 40.5,
 // 128 x 4096 -> 11008 21.7 / 25.1, 256 x 4096 -> 11008 32.7 / 25.3, 512 x 1024 -> 1024
 // 9.6 / 8.8, 2048 x 2048 -> 2048 19.3 / 14.8; back 33 x 11008 -> 4096 17.5 / 50.3,
-// 1024 x 4096 -> 1024 14.4 / 21.6; weight gradient over 4096 rows, 1024 x 1024
-// 16.8 / 26.1, over 700 rows, 1792 x 448 10.8 / 9.9.
+// 1024 x 4096 -> 1024 14.4 / 21.6; weight gradient with the unpacking before it
+// over 700 rows, 1792 x 448 8.4 / 9.8, over 8192, 256 x 256 11.4 / 13.7, 768 x 768 20 / 20,
+// 4096 x 1024 84 / 48.
 double pairs_us(const LinearArgs& a) {
   const int splits = std::max(1, a.splits);
   return pairs_us(static_cast<double>(cdiv(a.M, 256)) * cdiv(a.N, 256) * splits, cdiv(cdiv(a.K, 64), splits),
@@ -92,6 +93,7 @@ double pairs_us(const LinearArgs& a) {
 bool runs_on_pairs(const LinearArgs& a) {
   const int nt = few_rows_tile(a);
   if (cdiv(a.M, nt) > kFewMaxRowTiles) return true;  // narrow products of millions of rows
+  if (a.kind == 2) return pairs_us(a) <= few_grad_w_us(a, nt);
   const double chunk_us = nt == 128 ? 0.28 : nt == 64 ? 0.15 : 0.13;
   return pairs_us(a) <= 8.0 + chunk_us * cdiv(a.K, 64) * cdiv(a.N, 128) * cdiv(a.M, nt) / sm_count();
 }
@@ -291,10 +293,12 @@ instant_status instant_ckpt_grad_w(const void* gy, const void* q, const void* s,
       reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + values_bytes(rows, Cx) + sums_bytes(rows, Cy));
   const bool pairs = runs_on_pairs(a);
   // gb's shares on the side of a product long enough for the pair kernel's idle warps
-  // to read gy, which they do at about 0.8 TB/s; else in the launch that makes the values
+  // to read gy, which they do at about 0.8 TB/s over all pairs (32768 rows, 64 x 64, on 8 of
+  // the 76: 45 us instead of 25); else in the launch that makes the values
   int parts = 0;
   cudaError_t e;
-  if (gb && !(pairs && 2e-6 * rows * Cy / 0.8 <= pairs_us(a))) {
+  const double busy = std::min(1.0, static_cast<double>(cdiv(Cy, 256)) * cdiv(Cx, 256) * a.splits / (kColSumSMs / 2));
+  if (gb && !(pairs && 2e-6 * rows * Cy / (0.8 * busy) <= pairs_us(a))) {
     e = launch_unpack_and_sum(a.ck, ws, rows, Cx, gy, part, Cy, &parts, st);
   } else {
     e = launch_ckpt_unpack(a.ck, ws, rows, Cx, true, true, st);

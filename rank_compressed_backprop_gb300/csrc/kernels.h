@@ -412,6 +412,7 @@ struct FewArgs {
 };
 constexpr int kFewMaxRowTiles = 65535;   // they lie on the grid's second axis
 int few_rows_tile(const LinearArgs& a);  // its row tile for this product: 16, 32, 64 or 128
+double few_grad_w_us(const LinearArgs& a, int row_tile);  // its time for a weight gradient, an estimate
 cudaError_t launch_linear_few(const LinearArgs& a, cudaStream_t st);
 
 // tiled tensor map, by default with the 128-byte swizzle; dims/strides innermost first

@@ -167,3 +167,71 @@ def test_activations_of_infinities(torch, dtype, rows, Cx, act):
         assert np.abs(to_np(y)[0] - want[0]).max() <= 2.0 ** -8
     bad = ~np.isfinite(want[:, 0])
     assert np.array_equal(np.isnan(O.ckpt_decode(yq.cpu().numpy(), ys.cpu().numpy(), 256)).all(1), bad)
+
+
+# ---------------------------------------------------------------------------
+# long sums: what the tensor cores cut off must not add up
+# ---------------------------------------------------------------------------
+def in_order(torch, a, b):
+    """a^T b over the first axis, one fp32 addition a term (products of bf16 are exact)."""
+    out = torch.zeros(a.shape[1], b.shape[1], device="cuda")
+    for k in range(a.shape[0]):
+        out.addcmul_(a[k, :, None], b[k])
+    return out
+
+
+@pytest.mark.parametrize("rows,Cx,Cy", [(8192, 1152, 4096), (8192, 2432, 2048), (32768, 128, 11008),
+                                        (16384, 256, 1024), (32768, 64, 64), (4096, 1024, 1024)])
+def test_weight_gradient_over_many_rows(torch, rows, Cx, Cy):
+    """An accumulator takes 16 chunks of 64 rows, in 64 steps that cut off at most 2^-23
+    of the sum so far: 33 2^-23 of a segment of positive terms.  Up to 32 segments are
+    added in fp32, at most 2^-24 each."""
+    api = _api()
+    gen = torch.Generator("cuda").manual_seed(rows + Cx)
+    rn = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    for positive in (False, True):
+        g, x = rn(rows, Cy), rn(rows, Cx)
+        if positive:
+            g, x = g.abs() + 0.5, x.abs() + 0.5
+        g = g.bfloat16()
+        q, s = blank_ckpt(torch, rows, Cx)
+        api.ckpt_pack(x, q, s)
+        v = torch.empty(rows, Cx, device="cuda")
+        api.ckpt_unpack(q, s, v)
+        gw = nan_like(torch, (Cy, Cx), torch.float32)
+        api.ckpt_grad_w(g, q, s, gw)
+        want = g.double().t() @ v.double()
+        if positive:
+            assert float(((gw.double() - want).abs() / want).max()) <= (33 + 16) * 2.0 ** -23
+        elif rows * Cx * Cy < 1e11:   # random signs: no farther than twice what sums in order are
+            off = (in_order(torch, g.float(), v).double() - want).norm()
+            assert float((gw.double() - want).norm()) <= 2 * float(off)
+
+
+def rounded(torch, t):
+    """What the checkpoint of t (float64) stands for."""
+    rows, C = t.shape
+    g = torch.nn.functional.pad(t, (0, -C % 128)).view(rows, -1, 128)
+    m, e = torch.frexp(g.abs().amax(-1, keepdim=True))
+    step = torch.exp2((e - 7 + (m > 127 / 128)).clamp(-120, 121).double())
+    return ((g / step).round().clamp(-127, 127) * step).view(rows, -1)[:, :C]
+
+
+@pytest.mark.parametrize("rows,Cx,Cy", [(128, 4096, 11008), (100, 11008, 4096), (4096, 576, 4096), (12544, 448, 1792),
+                                        (2048, 1536, 4096)])
+def test_checkpoint_of_a_product(torch, rows, Cx, Cy):
+    """Codes that differ from those of exact sums: an error of the sums flips a code that
+    lies within it of the middle of two, so their number goes with the error.  Twice
+    what fp32 sums in order flip, and half as many again for chance."""
+    api = _api()
+    gen = torch.Generator("cuda").manual_seed(rows + Cx)
+    rn = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    x, w = rn(rows, Cx).bfloat16(), (rn(Cy, Cx) * Cx ** -0.5).bfloat16()
+    y = nan_like(torch, (rows, Cy), torch.bfloat16)
+    q, s = blank_ckpt(torch, rows, Cy)
+    api.linear_act(x, w, y, zq=q, zs=s)
+    v = nan_like(torch, (rows, Cy), torch.float32)
+    api.ckpt_unpack(q, s, v)
+    want = rounded(torch, x.double() @ w.double().t())
+    ordered = rounded(torch, in_order(torch, x.float().t().contiguous(), w.float().t().contiguous()).double())
+    assert int((v.double() != want).sum()) <= 3 * int((ordered != want).sum()) + 10
