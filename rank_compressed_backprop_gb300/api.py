@@ -515,6 +515,15 @@ def _ptr(t, shape, dt):
     return -1
 
 
+def _matrix(where: str, name: str, t):
+    """Shape of a matrix; anything else is refused."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{where}: {name} must be a matrix [rows, channels], got {list(t.shape)}")
+    return t.shape
+
+
 def _refuse(where: str, *wanted, ckpts=()):
     """Raises for the first of ``(name, tensor, shape, dtype)`` that is not what
     it should be: shapes and dtypes first, then device and layout."""
@@ -573,7 +582,7 @@ def ckpt_buffers(rows: int, C: int, device):
 
 def ckpt_pack(x: torch.Tensor, q: torch.Tensor, s: torch.Tensor, stream=None):
     """The 8-bit checkpoint of x ``[rows, C]``; q, s from :func:`ckpt_buffers`."""
-    rows, C = shape = x.shape
+    rows, C = shape = _matrix("ckpt_pack", "x", x)
     px = _ptr(x, shape, x.dtype)
     pq, ps = _ckpt_ptrs(rows, C, q, s)
     if -1 in (px, pq, ps):
@@ -585,7 +594,7 @@ def ckpt_pack(x: torch.Tensor, q: torch.Tensor, s: torch.Tensor, stream=None):
 
 def ckpt_unpack(q: torch.Tensor, s: torch.Tensor, x: torch.Tensor, stream=None) -> torch.Tensor:
     """The values a checkpoint stands for, into x ``[rows, C]`` (exact in bf16)."""
-    rows, C = shape = x.shape
+    rows, C = shape = _matrix("ckpt_unpack", "x", x)
     px = _ptr(x, shape, x.dtype)
     pq, ps = _ckpt_ptrs(rows, C, q, s)
     if -1 in (px, pq, ps):
@@ -602,7 +611,7 @@ def rms_norm(x: torch.Tensor, gamma: torch.Tensor, y: torch.Tensor | None, *,
     """``h = x + residual``, ``r = rsqrt(mean(h^2) + eps)``, ``u = h r``,
     ``y = u gamma``; q, s take the 8-bit checkpoint of u and r ``[rows]`` fp32
     the factor (both for :func:`rms_norm_backward`).  Returns y."""
-    rows, C = shape = x.shape
+    rows, C = shape = _matrix("rms_norm", "x", x)
     dt = x.dtype
     p = (_ptr(x, shape, dt), _ptr(residual, shape, dt), _ptr(gamma, (C,), dt), _ptr(h, shape, dt),
          _ptr(y, shape, dt), *_ckpt_ptrs(rows, C, q, s), _ptr(r, (rows,), torch.float32))
@@ -626,7 +635,7 @@ def rms_norm_backward(g_y: torch.Tensor, q: torch.Tensor, s: torch.Tensor, r: to
     """Gradient of :func:`rms_norm` from the checkpoint of u: ``gx`` (with the
     gradient ``residual`` that bypassed the norm added) and ``ggamma`` ``[C]``
     fp32 (added to with ``accumulate``).  Returns ``(gx, ggamma)``."""
-    rows, C = shape = g_y.shape
+    rows, C = shape = _matrix("rms_norm_backward", "g_y", g_y)
     dt, f32 = g_y.dtype, torch.float32
     p = (_ptr(g_y, shape, dt), *_ckpt_ptrs(rows, C, q, s), _ptr(r, (rows,), f32), _ptr(gamma, (C,), dt),
          _ptr(residual, shape, dt), _ptr(gx, shape, dt), _ptr(ggamma, (C,), f32))
@@ -648,8 +657,8 @@ def linear_act(x: torch.Tensor, w: torch.Tensor, y: torch.Tensor | None, *,
     """``z = x w^T + bias``, ``y = act(z) + residual``: x ``[rows, Cx]``, w ``[Cy, Cx]``,
     y ``[rows, Cy]``; zq, zs take the 8-bit checkpoint of z, yq, ys that of y.
     act: "none", "relu", "gelu" (erf form) or "silu".  Returns y."""
-    rows, Cx = shape = x.shape
-    Cy = w.shape[0]
+    rows, Cx = shape = _matrix("linear_act", "x", x)
+    Cy = _matrix("linear_act", "w", w)[0]
     dt = x.dtype
     out = (rows, Cy)
     p = (_ptr(x, shape, dt), _ptr(w, (Cy, Cx), dt), _ptr(bias, (Cy,), dt), _ptr(residual, out, dt),
@@ -668,8 +677,8 @@ def linear_act_grad(g_y: torch.Tensor, w: torch.Tensor, gx: torch.Tensor, *, act
                     residual: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """``gx = (g_y w) act'(z) + residual``: g_y ``[rows, Cy]``, w ``[Cy, Cx]``, gx
     ``[rows, Cx]``; zq, zs is the checkpoint of the activation's input z."""
-    rows, Cy = shape = g_y.shape
-    Cx = w.shape[1] if w.dim() == 2 else -1
+    rows, Cy = shape = _matrix("linear_act_grad", "g_y", g_y)
+    Cx = _matrix("linear_act_grad", "w", w)[1]
     dt = g_y.dtype
     out = (rows, Cx)
     p = (_ptr(g_y, shape, dt), _ptr(w, (Cy, Cx), dt), *_ckpt_ptrs(rows, Cx, zq, zs),
@@ -695,8 +704,8 @@ def ckpt_grad_w(g_y: torch.Tensor, q: torch.Tensor, s: torch.Tensor, gw: torch.T
     ``[Cy, Cx]`` fp32, gb ``[Cy]`` fp32 (needs ws).  ws from
     :func:`ckpt_grad_w_workspace`; without gb it may be left out, and bf16 calls
     then allocate it.  Returns ``(gw, gb)``."""
-    rows, Cy = shape = g_y.shape
-    Cx = gw.shape[1] if gw.dim() == 2 else -1
+    rows, Cy = shape = _matrix("ckpt_grad_w", "g_y", g_y)
+    Cx = _matrix("ckpt_grad_w", "gw", gw)[1]
     dt, f32 = g_y.dtype, torch.float32
     if gb is not None and ws is None:
         raise ValueError("ckpt_grad_w: gb needs a workspace")
