@@ -9,8 +9,10 @@ the forward are scratch.  The backward reads nothing else: the norm's gradient
 and w1's take u (w1's input was u gamma, so its gradient is scaled by gamma per
 column), w2's takes a, and z gives the activation's slope.
 
-The block holds its buffers and gradients; torch only owns memory, every
-arithmetic step runs in the CUDA library.
+The block holds its buffers and gradients, and the checkpoints of one forward: the
+next one overwrites them.  Several batches under way at once take a block each
+(the weights may be shared).  Torch only owns memory, every arithmetic step runs
+in the CUDA library.
 """
 
 from __future__ import annotations
@@ -37,6 +39,8 @@ class CheckpointedMLP:
         self.z = api.ckpt_buffers(rows, H, dev)
         self.a = api.ckpt_buffers(rows, H, dev)
         self.r = torch.empty(rows, dtype=f32, device=dev)
+        # forwards since the backward before them, and whether their last one has been used
+        self._forwards, self._used = 0, False
         # scratch of one pass
         self.h = torch.empty(rows, C, dtype=dt, device=dev)
         self.n = torch.empty(rows, C, dtype=dt, device=dev)
@@ -57,15 +61,19 @@ class CheckpointedMLP:
 
     def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None,
                 y: torch.Tensor | None = None) -> torch.Tensor:
-        """The training forward: y ``[rows, C]``; leaves the checkpoints for
-        :meth:`backward`."""
+        """The training forward of x ``[rows, C]``: y ``[rows, C]``; leaves the
+        checkpoints for :meth:`backward`, over those of the forward before."""
         y = torch.empty_like(x) if y is None else y
         h = x if residual is None else self.h
         api.rms_norm(x, self.gamma, self.n, residual=residual, h=None if residual is None else h,
                      q=self.u[0], s=self.u[1], r=self.r, eps=self.eps)
+        before = 0 if self._used else self._forwards
+        self._forwards = 0   # until all of the checkpoints are there
         api.linear_act(self.n, self.w1, self.wide, bias=self.b1, act=self.act, zq=self.z[0],
                        zs=self.z[1], yq=self.a[0], ys=self.a[1])
-        return api.linear_act(self.wide, self.w2, y, bias=self.b2, residual=h)
+        api.linear_act(self.wide, self.w2, y, bias=self.b2, residual=h)
+        self._forwards, self._used = before + 1, False
+        return y
 
     def generate(self, x: torch.Tensor, residual: torch.Tensor | None = None) -> torch.Tensor:
         """The forward without checkpoints, for any number of tokens (one and up)."""
@@ -79,8 +87,17 @@ class CheckpointedMLP:
 
     def backward(self, g_y: torch.Tensor, gx: torch.Tensor | None = None,
                  accumulate: bool = False) -> torch.Tensor:
-        """Gradient of the block's input (x and residual alike); the parameters'
-        gradients go to (or are added to) ``ggamma``, ``gw1``, ``gb1``, ``gw2``, ``gb2``."""
+        """Gradient of the block's input (x and residual alike) at the last forward;
+        the parameters' gradients go to (or are added to) ``ggamma``, ``gw1``, ``gb1``,
+        ``gw2``, ``gb2``.
+
+        Without a forward there is nothing to read, and two forwards followed by two
+        backwards have lost the first one's checkpoints: both are refused."""
+        if self._forwards == 0:
+            raise RuntimeError("CheckpointedMLP.backward: no forward has left its checkpoints")
+        if self._used and self._forwards > 1:
+            raise RuntimeError(f"CheckpointedMLP.backward: {self._forwards} forwards in a row, and only the last "
+                               "one's checkpoints are kept: use a block for each batch under way")
         gx = torch.empty_like(g_y) if gx is None else gx
         api.ckpt_grad_w(g_y, *self.a, self.gw2, self.ws_w2, gb=self.gb2, accumulate=accumulate)
         gz = api.linear_act_grad(g_y, self.w2, self.wide, act=self.act, zq=self.z[0], zs=self.z[1])
@@ -89,4 +106,5 @@ class CheckpointedMLP:
         gn = api.linear_act_grad(gz, self.w1, self.n)
         api.rms_norm_backward(gn, *self.u, self.r, self.gamma, gx, self.ggamma, self.ws_norm,
                               residual=g_y, accumulate=accumulate)
+        self._used = True
         return gx

@@ -235,3 +235,50 @@ def test_checkpoint_of_a_product(torch, rows, Cx, Cy):
     want = rounded(torch, x.double() @ w.double().t())
     ordered = rounded(torch, in_order(torch, x.float().t().contiguous(), w.float().t().contiguous()).double())
     assert int((v.double() != want).sum()) <= 3 * int((ordered != want).sum()) + 10
+
+
+# ---------------------------------------------------------------------------
+# the block
+# ---------------------------------------------------------------------------
+def small_mlp(torch, rows, C=64, H=136):
+    from rank_compressed_backprop_gb300 import CheckpointedMLP
+
+    gen = torch.Generator("cuda").manual_seed(11)
+    rn = lambda *s: torch.randn(*s, generator=gen, device="cuda").bfloat16()  # noqa: E731
+    mlp = CheckpointedMLP(1 + 0.1 * rn(C), rn(H, C) * C ** -0.5, rn(H), rn(C, H) * H ** -0.5, rn(C), rows)
+    return mlp, rn
+
+
+def test_block_keeps_one_forward(torch):
+    """A backward whose checkpoints are not there, or are another batch's, is refused;
+    everything else runs: a forward that nobody went back through, two gradients at
+    one forward, any number of steps."""
+    mlp, rn = small_mlp(torch, 33)
+    a, b, g = rn(33, 64), rn(33, 64), rn(33, 64)
+    with pytest.raises(RuntimeError, match="no forward"):
+        mlp.backward(g)
+    mlp.forward(a)
+    first = mlp.backward(g).clone()
+    assert torch.equal(mlp.backward(g), first)      # twice at one forward
+    for _ in range(2):                              # steps, one forward of them left unused
+        mlp.forward(b)
+        mlp.forward(a)
+        assert torch.equal(mlp.backward(g), first)
+        mlp.forward(a)
+        assert torch.equal(mlp.backward(g), first)
+    mlp.forward(a)                                  # two batches under way in one block
+    mlp.forward(b)
+    mlp.backward(g)
+    with pytest.raises(RuntimeError, match="2 forwards in a row"):
+        mlp.backward(g)
+    mlp.forward(a)
+    assert torch.equal(mlp.backward(g), first)
+    with pytest.raises(ValueError, match="x must be a matrix"):
+        mlp.forward(a.view(3, 11, 64))
+    with pytest.raises(ValueError):
+        mlp.forward(a[:5])                          # another number of rows than the block's
+    assert torch.equal(mlp.backward(g), first)      # a refused forward has left them alone
+    with pytest.raises(ValueError, match="y must be"):
+        mlp.forward(b, y=a[:5])                     # refused at its end, over what was kept
+    with pytest.raises(RuntimeError, match="no forward"):
+        mlp.backward(g)
