@@ -282,3 +282,115 @@ def test_block_keeps_one_forward(torch):
         mlp.forward(b, y=a[:5])                     # refused at its end, over what was kept
     with pytest.raises(RuntimeError, match="no forward"):
         mlp.backward(g)
+
+
+# ---------------------------------------------------------------------------
+# captured in a graph, and called from several threads
+# ---------------------------------------------------------------------------
+def test_block_in_a_graph(torch):
+    """A captured step (forward and backward, a weight gradient with scratch of its own)
+    replayed over other inputs gives what the calls by themselves give."""
+    api = _api()
+    mlp, rn = small_mlp(torch, 300, 264, 1032)
+    x, r, g = rn(300, 264), rn(300, 264), rn(300, 264)
+    y, gx, gw = torch.empty_like(x), torch.empty_like(x), torch.empty(1032, 264, device="cuda")
+
+    def step():
+        mlp.forward(x, r, y)
+        mlp.backward(g, gx)
+        api.ckpt_grad_w(mlp.wide, *mlp.u, gw)
+
+    names = ("gw1", "gb1", "gw2", "gb2", "ggamma")
+    results = lambda: [t.clone() for t in (y, gx, gw, *(getattr(mlp, n) for n in names))]  # noqa: E731
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(3):
+        for t in (x, r, g):
+            t.copy_(rn(300, 264))
+        step()
+        want = results()
+        for t in (y, gx, gw, *(getattr(mlp, n) for n in names)):
+            t.fill_(float("nan"))
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(results(), want))
+    assert api.device_status() == 0
+
+
+def test_blocks_of_several_threads(torch):
+    """Four host threads, a block and a stream each, at the same time."""
+    import threading
+
+    jobs = []
+    for i, (rows, C, H) in enumerate([(1, 264, 520), (700, 448, 1792), (129, 1024, 2048), (2600, 64, 328)]):
+        mlp, rn = small_mlp(torch, rows, C, H)
+        x, g = rn(rows, C), rn(rows, C)
+        y = mlp.forward(x)
+        jobs.append((mlp, x, g, y.clone(), mlp.backward(g).clone(), mlp.gw1.clone(), mlp.ggamma.clone()))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(mlp, x, g, y, gx, gw1, gg):
+        try:
+            st = torch.cuda.Stream()
+            with torch.cuda.stream(st):
+                for _ in range(20):
+                    a = mlp.forward(x)
+                    b = mlp.backward(g)
+                    if not (torch.equal(a, y) and torch.equal(b, gx) and torch.equal(mlp.gw1, gw1)
+                            and torch.equal(mlp.ggamma, gg)):
+                        wrong.append(x.shape)
+        except Exception as e:  # noqa: BLE001
+            wrong.append(e)
+
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+    assert _api().device_status() == 0
+
+
+# ---------------------------------------------------------------------------
+# the norm's gradient over wide rows, more of them than CTAs
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,C,res", [(700, 12296, True), (1300, 16384, True), (650, 32768, False)])
+def test_norm_backward_of_wide_rows(torch, dtype, rows, C, res):
+    """Bounds as for the narrow ones: C products a row, rows products a column, each sum
+    off by at most 2^-23 of its terms' magnitudes a step."""
+    api = _api()
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    gen = torch.Generator("cuda").manual_seed(rows + C)
+    rn = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    h, gamma = rn(rows, C).to(dt), (1 + 0.1 * rn(C)).to(dt)
+    q, s = blank_ckpt(torch, rows, C)
+    r = torch.empty(rows, device="cuda")
+    api.rms_norm(h, gamma, None, q=q, s=s, r=r)
+    gy = (rn(rows, C) * 1e-2).to(dt)
+    bypass = (rn(rows, C) * 1e-2).to(dt) if res else None
+    gx, gg = nan_like(torch, (rows, C), dt), nan_like(torch, (C,), torch.float32)
+    ws = api.rms_norm_backward_workspace(rows, C, "cuda")
+    api.rms_norm_backward(gy, q, s, r, gamma, gx, gg, ws, residual=bypass)
+    u = torch.empty(rows, C, device="cuda")
+    api.ckpt_unpack(q, s, u)
+    u, d = u.double(), gy.double() * gamma.double()
+    c, ca = (d * u).mean(1, keepdim=True), (d * u).abs().mean(1, keepdim=True)
+    want = r.double()[:, None] * (d - u * c) + (bypass.double() if res else 0)
+    e = r.double()[:, None] * (2.0 ** -21 * (d.abs() + u.abs() * ca) + u.abs() * ca * C * 2.0 ** -23)
+    ulp = 2.0 ** -24 if dtype == "f32" else 2.0 ** -8
+    assert bool(((gx.double() - want).abs() <= want.abs() * (ulp + 2.0 ** -22) + e).all())
+    p = gy.double() * u
+    assert bool(((gg.double() - p.sum(0)).abs() <= p.abs().sum(0) * (rows + 8) * 2.0 ** -23).all())
+    first = gg.clone()
+    api.rms_norm_backward(gy, q, s, r, gamma, gx, gg, ws, residual=bypass, accumulate=True)
+    assert bool(((gg.double() - 2 * p.sum(0)).abs() <= 2 * p.abs().sum(0) * (rows + 8) * 2.0 ** -23
+                 + p.sum(0).abs() * 2.0 ** -22).all())
+    api.rms_norm_backward(gy, q, s, r, gamma, gx, gg, ws, residual=bypass)
+    assert torch.equal(gg, first)
