@@ -53,13 +53,17 @@ constexpr uint32_t STAGE = A_BYTES + B_BYTES;
 constexpr uint32_t BOX = 128 * 128;          // staging box: 128 rows x 128 bytes
 constexpr int kThreads = 640;
 // Chunks of a short contraction.  Its forward sums segments of three with or without
-// checkpoints, in the same code: both give the same bits, and as few of the checkpoints'
+// checkpoints, in the same code, so that in this kernel both give the same bits (longer
+// contractions and linear_few.cu promise no such thing), and as few of the checkpoints'
 // codes differ from those of exact sums as after fp32 sums in order (of the 22 million of
 // 12544 x 448 -> 1792 82 to 104, after fp32 sums 78 to 87; with fours 112 to 141).  That
 // costs 4 us of 37 against fours there, and 8 of 26 without checkpoints against one
 // segment.  Longer ones sum segments of six, from 17 chunks on eight, and only with
-// checkpoints: at 8192 x 1024 -> 4096 fours took 74 us, sixes 66, eights 60, with values
-// up to 1.7 times as far off as after fp32 sums where sixes are 1.5 (576 channels).
+// checkpoints.  Values are then up to 1.4 (sixes, 576 to 1024 channels) and 1.5 times
+// (eights, 1536; 1.2 at 4096) as far from those of exact sums as after fp32 sums, which is
+// a hundredth of the codes' own rounding.  Fours up to 1024 channels, 1.0 to 1.3 times,
+// took 74 us instead of 67 at 8192 x 1024 -> 4096 and 20.6 instead of 19.4 at 8192 x 576 ->
+// 1024, sixes above, 1.1 times, 86 instead of 81 at 8192 x 1536 -> 4096.
 constexpr int kShortK = 8;
 // Over a long one the first two segments, whose products run under the epilogue of the
 // tile before, are sixteens: with eights that epilogue (7 us) outlasted them and the
