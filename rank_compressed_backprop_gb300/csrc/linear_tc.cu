@@ -35,7 +35,7 @@
 //
 // Bound: at 8192 x 11008 -> 4096 the tensor cores (393 us, 1.88 PFLOP/s; sustained 444,
 // 1.66 PFLOP/s, under the power limit, like a library matrix product of these sizes);
-// at 12544 x 448 -> 1792 the epilogue's instructions (20 us plain, 34 with gelu, 42 with
+// at 12544 x 448 -> 1792 the epilogue's instructions (20 us plain, 35 with gelu, 42 with
 // both checkpoints, for 11 us of products).
 #include <utility>
 
