@@ -58,12 +58,12 @@ constexpr int kThreads = 640;
 // codes differ from those of exact sums as after fp32 sums in order (of the 22 million of
 // 12544 x 448 -> 1792 82 to 104, after fp32 sums 78 to 87; with fours 112 to 141).  That
 // costs 4 us of 37 against fours there, and 8 of 26 without checkpoints against one
-// segment.  Longer ones sum segments of six, from 17 chunks on eight, and only with
-// checkpoints.  Values are then up to 1.4 (sixes, 576 to 1024 channels) and 1.5 times
-// (eights, 1536; 1.2 at 4096) as far from those of exact sums as after fp32 sums, which is
-// a hundredth of the codes' own rounding.  Fours up to 1024 channels, 1.0 to 1.3 times,
-// took 74 us instead of 67 at 8192 x 1024 -> 4096 and 20.6 instead of 19.4 at 8192 x 576 ->
-// 1024, sixes above, 1.1 times, 86 instead of 81 at 8192 x 1536 -> 4096.
+// segment.  Longer ones sum even segments of six at most, and only with checkpoints.
+// Values are then 1.2 to 1.4 times (576 to 1024 channels) and 1.0 to 1.2 times (above) as far
+// from those of exact sums as after fp32 sums, which is a hundredth of the codes' own
+// rounding.  Fours up to 1024 channels, 1.0 to 1.3 times, took 74 us instead of 67 at
+// 8192 x 1024 -> 4096 and 20.6 instead of 19.4 at 8192 x 576 -> 1024; eights above, up to 1.5
+// times, 80 instead of 85 at 8192 x 1536 -> 4096.
 constexpr int kShortK = 8;
 // Over a long one the first two segments, whose products run under the epilogue of the
 // tile before, are sixteens: with eights that epilogue (7 us) outlasted them and the
@@ -874,8 +874,10 @@ cudaError_t launch_linear_tc(const LinearArgs& l, cudaStream_t st) {
   a.nk = (l.K + BK - 1) / BK;
   a.group = 8;
   const bool keep = l.kind == FORWARD && (l.zk.q || l.yk.q || a.nk <= kShortK);
-  a.seg = l.kind == GRAD_W ? 16 : !keep ? a.nk : a.nk <= kShortK ? 3 : a.nk <= 2 * kShortK ? 6 : 8;
-  a.seg01 = keep && a.nk >= kLongK ? 2 * a.seg : a.seg;
+  const int most = a.nk <= kShortK ? 3 : 6;  // of a forward's segments, which are as even as that allows
+  const int segments = (a.nk + most - 1) / most;
+  a.seg = l.kind == GRAD_W ? 16 : !keep ? a.nk : (a.nk + segments - 1) / segments;
+  a.seg01 = keep && a.nk >= kLongK ? 16 : a.seg;
   a.splits = l.kind == GRAD_W && l.splits > 1 ? l.splits : 1;
   a.per = (a.nk + a.splits - 1) / a.splits;
   if (static_cast<long long>(a.mt) * a.nt * a.splits > 0x7fffffffll - 4096) return cudaErrorInvalidValue;

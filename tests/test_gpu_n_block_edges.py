@@ -394,3 +394,22 @@ def test_norm_backward_of_wide_rows(torch, dtype, rows, C, res):
                  + p.sum(0).abs() * 2.0 ** -22).all())
     api.rms_norm_backward(gy, q, s, r, gamma, gx, gg, ws, residual=bypass)
     assert torch.equal(gg, first)
+
+
+@pytest.mark.parametrize("rows,Cx,Cy", [(16384, 576, 4096), (8192, 1536, 4096), (8192, 2048, 4096)])
+def test_checkpoints_over_some_hundred_channels(torch, rows, Cx, Cy):
+    """Over 30 million values and more, with a few channels twenty times larger, at most
+    twice the codes that fp32 sums in order flip (some 200 to 600: chance is a tenth)."""
+    api = _api()
+    gen = torch.Generator("cuda").manual_seed(rows + Cx)
+    rn = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    x = rn(rows, Cx)
+    x[:, ::256] *= 20
+    x, w = x.bfloat16(), (rn(Cy, Cx) * Cx ** -0.5).bfloat16()
+    q, s = blank_ckpt(torch, rows, Cy)
+    api.linear_act(x, w, None, yq=q, ys=s)
+    v = nan_like(torch, (rows, Cy), torch.float32)
+    api.ckpt_unpack(q, s, v)
+    want = rounded(torch, x.double() @ w.double().t())
+    ordered = rounded(torch, in_order(torch, x.float().t().contiguous(), w.float().t().contiguous()).double())
+    assert int((v.double() != want).sum()) <= 2 * int((ordered != want).sum())
