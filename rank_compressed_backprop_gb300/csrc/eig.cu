@@ -8,9 +8,10 @@
 // (round-robin parallel) Jacobi method on the whole matrix in shared memory.
 // Larger L: block subspace iteration with a Rayleigh-Ritz step every
 // iteration, as one cluster launch where the rows fit (k_solve_cluster below),
-// otherwise as a host loop whose iterations are five launches:
+// otherwise as a host loop of launches:
 //   orth   (1 CTA)  T = D W_G Lambda_G^(-1/2) from the Gram matrix of Z
 //   apply  (grid)   V = Z T                         (orthonormal basis)
+//   gram, orth, apply once more on V where a pivot of the first pass was small
 //   cv     (grid)   Y = C V / n,  H += V^T Y
 //   rr     (1 CTA)  H = W Theta W^T  (Jacobi, sorted descending)
 //   ritz   (grid)   U = V W, Z = Y W = C U / n, G += Z^T Z, res_j += |Z_j - theta_j U_j|^2
@@ -365,14 +366,17 @@ __global__ void k_sub_init(int L, int m, const void* seed, int n_seed, int seed_
   }
 }
 
-// G += Z[rows]^T Z[rows]
-__global__ void k_sub_gram(int L, int m, SolverWs w) {
+// G += X[rows]^T X[rows]; second: only where the first pass was weak
+__global__ void k_sub_gram(const float* X, int second, int L, int m, SolverWs w) {
+  pdl_launch_dependents();
+  pdl_wait();
+  if (second && !w.res->weak) return;
   extern __shared__ float zs[];  // [kRows][m]
   const int i0 = blockIdx.x * kRows;
   const int nr = min(kRows, L - i0);
   for (int idx = threadIdx.x; idx < kRows * m; idx += blockDim.x) {
     const int r = idx / m;
-    zs[idx] = r < nr ? w.Z[(i0 + r) * m + (idx - r * m)] : 0.f;
+    zs[idx] = r < nr ? X[(i0 + r) * m + (idx - r * m)] : 0.f;
   }
   __syncthreads();
   for (int idx = threadIdx.x; idx < m * m; idx += blockDim.x) {
@@ -385,6 +389,12 @@ __global__ void k_sub_gram(int L, int m, SolverWs w) {
   }
 }
 
+// A pivot of the normalised Gram matrix is what is left of a column's squared norm beside
+// the columns before it, and the fp32 Gram matrix has it to some 1e-7: a basis from pivots
+// down to p is orthonormal to 1e-7 / p.  Below this one it is taken once more, from its own
+// Gram matrix (Ritz vectors of a spectrum without zeros keep their pivots near 1).
+constexpr float kWeakPivot = 0.05f;
+
 // T with Z T orthonormal, from the Gram matrix G = Z^T Z (m x m, row stride
 // ldg), written to T (row stride ldt); the whole CTA takes part.
 // Columns are first normalised (D = diag(G)^(-1/2)); the normalised Gram
@@ -395,13 +405,16 @@ __global__ void k_sub_gram(int L, int m, SolverWs w) {
 // Returns false when that Jacobi solve hit its sweep cap.  G before the first Cholesky step and T is written last, so G and
 // T may share storage.
 __device__ bool orth_core(const float* G, int ldg, int m, int max_sweeps, JacSmem s, float* T,
-                          int ldt, float* dsc, float* pv, int* deficient) {
+                          int ldt, float* dsc, float* pv, int* deficient, float* least = nullptr) {
   const int ld = m + 1;
   for (int i = threadIdx.x; i < m; i += blockDim.x) {
     const float g = G[i * ldg + i];
     dsc[i] = g > 0.f ? 1.f / sqrtf(g) : 0.f;
   }
-  if (threadIdx.x == 0) *deficient = 0;
+  if (threadIdx.x == 0) {
+    *deficient = 0;
+    if (least) *least = 1.f;
+  }
   __syncthreads();
   for (int idx = threadIdx.x; idx < m * m; idx += blockDim.x) {
     const int i = idx / m, j = idx - (idx / m) * m;
@@ -419,6 +432,7 @@ __device__ bool orth_core(const float* G, int ldg, int m, int max_sweeps, JacSme
   __syncthreads();
   for (int k = 0; k < m; ++k) {
     const float d = Lc[k * ld + k];
+    if (least && threadIdx.x == 0) *least = d > 1e-6f ? fminf(*least, d) : 0.f;
     if (!(d > 1e-6f)) {
       if (threadIdx.x == 0) *deficient = 1;
       break;
@@ -475,30 +489,45 @@ __device__ bool orth_core(const float* G, int ldg, int m, int max_sweeps, JacSme
 }
 
 // 1 CTA: T from the Gram matrix G (see orth_core); zeroes G for the next step
-__global__ void __launch_bounds__(kJacThreads) k_sub_orth(int m, int max_sweeps, SolverWs w) {
+__global__ void __launch_bounds__(kJacThreads) k_sub_orth(int second, int m, int max_sweeps, SolverWs w) {
   pdl_launch_dependents();
   pdl_wait();
+  if (second && !w.res->weak) return;
   extern __shared__ uint8_t smem[];
   JacSmem s = jac_carve(smem, m);
   __shared__ float dsc[kMaxBlock];
   __shared__ float pv[kMaxBlock];
   __shared__ int deficient;
-  const bool ok = orth_core(w.G, m, m, max_sweeps, s, w.T, m, dsc, pv, &deficient);
+  __shared__ float least;
+  const bool ok = orth_core(w.G, m, m, max_sweeps, s, w.T, m, dsc, pv, &deficient, &least);
   for (int idx = threadIdx.x; idx < m * m; idx += blockDim.x) w.G[idx] = 0.f;
-  if (threadIdx.x == 0 && !ok) w.res->jacobi_failed = 1;
+  if (threadIdx.x == 0) {
+    if (!ok) w.res->jacobi_failed = 1;
+    if (!second) w.res->weak = least < kWeakPivot;
+  }
 }
 
-// out[rows] = in[rows] * M   (M m x m), rows of kRows per CTA
-__global__ void k_sub_apply(const float* __restrict__ in, const float* __restrict__ M, float* out,
-                            float* zero_rows, int L, int m) {
+// out[rows] = in[rows] * M   (M m x m), rows of kRows per CTA, which has read its rows
+// before it writes them (out may be in).  second: only where the first pass was weak.
+// There it has put pseudo-random columns in the place of those that M leaves out (the
+// directions that a rank-deficient block lacks), which the second orthonormalises.
+__global__ void k_sub_apply(const float* in, const float* __restrict__ M, float* out, float* zero_rows,
+                            const int* weak, int second, int L, int m) {
   pdl_launch_dependents();
   pdl_wait();
+  const bool refill = *weak != 0;
+  if (second && !refill) return;
   extern __shared__ float sm[];
   float* Ms = sm;            // [m][m]
   float* rs = sm + m * m;    // [kRows][m]
+  __shared__ int lacking[kMaxBlock];
   const int i0 = blockIdx.x * kRows;
   const int nr = min(kRows, L - i0);
   for (int idx = threadIdx.x; idx < m * m; idx += blockDim.x) Ms[idx] = M[idx];
+  for (int j = threadIdx.x; j < m; j += blockDim.x) {
+    lacking[j] = refill && !second;
+    for (int k = 0; k < m && lacking[j]; ++k) lacking[j] = M[k * m + j] == 0.f;
+  }
   for (int idx = threadIdx.x; idx < kRows * m; idx += blockDim.x) {
     const int r = idx / m;
     rs[idx] = r < nr ? in[(i0 + r) * m + (idx - r * m)] : 0.f;
@@ -508,7 +537,7 @@ __global__ void k_sub_apply(const float* __restrict__ in, const float* __restric
     const int r = idx / m, j = idx - (idx / m) * m;
     float acc = 0.f;
     for (int k = 0; k < m; ++k) acc = fmaf(rs[r * m + k], Ms[k * m + j], acc);
-    out[(i0 + r) * m + j] = acc;
+    out[(i0 + r) * m + j] = lacking[j] ? hash_uniform(i0 + r, j) : acc;
     if (zero_rows) zero_rows[(i0 + r) * m + j] = 0.f;
   }
 }
@@ -679,7 +708,8 @@ __device__ int k_rule(const double* theta, int m, double target) {
 // below kRitzRelTol * theta_i, or -- at the rounding floor of the fp32 C V
 // product, which can lie above that for small theta_i -- when it is below
 // tol * theta_1 and no longer shrinking (at least half the previous check's
-// squared residual).
+// squared residual; in the multi-launch loop, whose sums vary, half the smallest so
+// far: many pairs at the floor would hardly ever all miss a downward swing at once).
 constexpr double kRitzRelTol = 1e-3;
 
 __host__ __device__ inline bool ritz_converged(double r2, double r2_prev, double th_i, double th_1,
@@ -704,7 +734,7 @@ __global__ void k_sub_check(int L, int m, double eps, int p, int r_override, dou
   const double th1 = r->theta[0];
   for (int i = 0; i < R && i < m && conv; ++i)
     if (!ritz_converged(r->res2[i], r->res2_prev[i], r->theta[i], th1, tol)) conv = 0;
-  for (int i = 0; i < m; ++i) r->res2_prev[i] = r->res2[i];
+  for (int i = 0; i < m; ++i) r->res2_prev[i] = fminf(r->res2_prev[i], r->res2[i]);
   r->converged = conv;
 }
 
@@ -1720,7 +1750,7 @@ cudaError_t launch_subspace_init(int L, int m, const void* seed, int n_seed, int
                                  SolverWs w, cudaStream_t st) {
   k_sub_init<<<64, 256, 0, st>>>(L, m, seed, n_seed, seed_bf16, w);
   const size_t gb = sizeof(float) * kRows * m;
-  k_sub_gram<<<(L + kRows - 1) / kRows, 256, gb, st>>>(L, m, w);
+  k_sub_gram<<<(L + kRows - 1) / kRows, 256, gb, st>>>(w.Z, 0, L, m, w);
   count_launches(2);
   return cudaGetLastError();
 }
@@ -1741,12 +1771,17 @@ cudaError_t launch_subspace_iteration(const float* C, int L, int m, double inv_n
   const int jt = jac_threads(m);
   const bool pdl = pdl_enabled();
   const float fn = static_cast<float>(inv_n);
-  if ((e = launch_ex(k_sub_orth, dim3(1), dim3(jt), jb, st, 1, pdl, m, max_sweeps, w)) != cudaSuccess)
-    return e;
-  if ((e = launch_ex(k_sub_apply, dim3(nb), dim3(256), ab, st, 1, pdl,
-                     static_cast<const float*>(w.Z), static_cast<const float*>(w.T), w.V, w.Y, L,
-                     m)) != cudaSuccess)
-    return e;
+  for (int second = 0; second < 2; ++second) {
+    if (second && (e = launch_ex(k_sub_gram, dim3(nb), dim3(256), sizeof(float) * kRows * m, st, 1, pdl,
+                                 static_cast<const float*>(w.V), 1, L, m, w)) != cudaSuccess)
+      return e;
+    if ((e = launch_ex(k_sub_orth, dim3(1), dim3(jt), jb, st, 1, pdl, second, m, max_sweeps, w)) != cudaSuccess)
+      return e;
+    if ((e = launch_ex(k_sub_apply, dim3(nb), dim3(256), ab, st, 1, pdl,
+                       static_cast<const float*>(second ? w.V : w.Z), static_cast<const float*>(w.T), w.V, w.Y,
+                       static_cast<const int*>(&w.res->weak), second, L, m)) != cudaSuccess)
+      return e;
+  }
   {
     const int JB = L >= 1024 ? 256 : (L >= 256 ? 64 : 32);
     const size_t cvb = sizeof(float) * (kCvRows * (JB + 1) + JB * m);

@@ -219,7 +219,7 @@ struct SolverResult {      // lives at the start of the solver workspace
   float scale;
   int jacobi_failed;       // a Jacobi solve hit its sweep cap
   int block_short;         // k + p does not fit the block
-  int pad_;
+  int weak;                // the last orthonormalisation needs a second pass
   double theta[128];       // Ritz values (descending)
   float res2[128];         // squared residual norms of the Ritz vectors
   float res2_prev[128];    // the same at the previous convergence check
