@@ -7,8 +7,9 @@
 //
 // Both are bound by HBM: the forward reads the logits once, a thread keeping the
 // running maximum and sums of its vectors; the gradient reads them once and writes
-// once.  Exponents are those of differences to the maximum, so that a row of large
-// logits keeps its accuracy and one of the type's lowest values does not overflow.
+// once.  Exponents are those of differences to the maximum, taken in one of two forms by
+// its size (Part), so that a row of large logits keeps its accuracy and one that is masked
+// whole, by whatever value, is a uniform one.
 //
 // A row belongs to one CTA, or to a cluster of up to kMaxShares when rows are few;
 // its CTAs' results meet in shared memory of the first.
@@ -119,8 +120,8 @@ __device__ __forceinline__ float batch_max(const uint4 (&u)[kBatch], float) {
   return m;
 }
 
-// values below -1e37 as -1e37: their weight is 0 beside a maximum of at least -1e36 (with
-// c >= 1e-30), and the product with their exponent (at least -1e38) is no NaN
+// values below -1e37 as -1e37: their weight is 0 beside a maximum m with |m c| <= 2^20 (with
+// c >= 1e-30, x c is -1e7), and the product with their exponent (at least -1e38) is no NaN
 __device__ __forceinline__ uint4 not_below(const uint4& u, uint16_t) {
   uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -151,21 +152,25 @@ __device__ __forceinline__ float key_value(uint64_t key) {
 __device__ __forceinline__ uint32_t key_index(uint64_t key) { return ~static_cast<uint32_t>(key); }
 
 // Running maximum and sums of a part of a row.  An exponent is taken as w = x c - mc with
-// c = scale log2 e and mc = m c rounded, one FMA; what the rounding of mc shifts all of
-// them by is put right in the row's log S.  Where that could leave the range of fp32 (a
-// row of the type's lowest values, very large or small scales) it is (x - m) c instead.
+// c = scale log2 e and mc = m c rounded, one FMA; rest = m c - mc, by which the rounding
+// shifts all of them, is put right in the row's log S.  That is so while |m c| is at most
+// kNear, where the rest is below 2^-5; from 2^31 on 2^rest itself would leave the range of
+// fp32.  Larger maxima (a row masked whole by some -1e10, one of the type's lowest values)
+// and very large or small scales take w as (x - m) c instead.
 struct Part {
+  static constexpr float kNear = 1048576.f;  // 2^20
   float m, s, a;  // max, sum 2^w, sum w 2^w
   __device__ __forceinline__ static bool careful(float m, float c) {
-    return !(fabsf(m) <= 1e36f && c >= 1e-30f && c <= 10.f);
+    return !(fabsf(m) * c <= kNear && c >= 1e-30f && c <= 10.f);
   }
-  // what is taken from x c; 0 for a part of nothing but minus infinities
-  __device__ __forceinline__ static float ref(float m, float c) { return m == -inf_f() ? 0.f : m * c; }
-  // moves the sums to another maximum (at least m, or a NaN)
+  __device__ __forceinline__ static float ref(float m, float c) { return __fmul_rn(m, c); }  // mc, in no FMA
+  __device__ __forceinline__ static float rest(float m, float c) { return careful(m, c) ? 0.f : fmaf(m, c, -ref(m, c)); }
+  // Moves the sums to another maximum (at least m, or a NaN), from the one form of an exponent
+  // to the other where that changes.  s is finite, at most the number of its elements and 2^(2^-5).
   template <bool ENT>
   __device__ __forceinline__ void move(float m1, float c) {
-    const bool far = careful(m, c) || careful(m1, c);
-    const float t = far ? (m - m1) * c : ref(m, c) - ref(m1, c);
+    float t = ref(m, c) - ref(m1, c);
+    if (__builtin_expect(careful(m, c) || careful(m1, c), 0)) t = fmaf(m - m1, c, rest(m1, c) - rest(m, c));
     const float f = m == -inf_f() ? 0.f : ex2_approx(t);
     if (ENT) a = f == 0.f ? 0.f : f * fmaf(t, s, a);  // t may be huge where f is 0
     s = f * s;
@@ -179,10 +184,9 @@ struct Part {
     s += o.s;
     a += o.a;
   }
-  // log S from s: S = s 2^(mc - m c)
+  // log S from s: S = s 2^-rest
   __device__ __forceinline__ float log_sum(float c) const {
-    if (m == -inf_f()) return m;
-    return careful(m, c) ? logf(s) : fmaf(-kLn2, fmaf(m, c, -ref(m, c)), logf(s));
+    return m == -inf_f() ? m : fmaf(-kLn2, rest(m, c), logf(s));
   }
 };
 
@@ -641,7 +645,7 @@ __global__ void __launch_bounds__(NT, CTAS) k_logprobs(const __grid_constant__ L
   if (edge) {
     Part e;
     e.m = xe;
-    const float w = Part::careful(e.m, c) ? e.m - e.m : fmaf(e.m, c, -Part::ref(e.m, c));  // NaN for an infinity
+    const float w = Part::careful(e.m, c) ? e.m - e.m : Part::rest(e.m, c);  // NaN for an infinity
     e.s = e.m == -inf_f() ? 0.f : ex2_approx(w);
     e.a = e.m == -inf_f() ? 0.f : w * e.s;
     p.join<ENT>(e, c);

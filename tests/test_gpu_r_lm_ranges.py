@@ -1,0 +1,97 @@
+"""The operators at the ends of a language model over the whole range of their values and
+sizes: finite masks of any size, logits around the bound between the two forms of an
+exponent."""
+
+import numpy as np
+import pytest
+
+from gpu_util import rng, stored, torch_or_skip
+from test_gpu_p_lm import check_logprobs, check_logprobs_grad
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def torch():
+    return torch_or_skip()
+
+
+# ---------------------------------------------------------------------------
+# finite masks and large logits
+# ---------------------------------------------------------------------------
+FILLS = [1e4, 1e6, 1e9, 1e10, 1e12, 1e15, 1e20, 1e30, 1e36, 2e36, 1e38]
+KINDS = ["whole", "few", "front", "back", "edge", "some", "large", "peak", "rising", "falling", "border", "minus_border"]
+
+
+def masked_row(g, kind, fill, V, scale):
+    """Ordinary logits of which some are -fill (kinds up to "some"), or logits as large as fill, or
+    ones that lie around the 2^20 / (scale log2 e) beyond which an exponent is a difference's."""
+    x = g.standard_normal(V) * 2.5
+    if kind == "whole":
+        x[:] = -fill
+    elif kind == "few":            # constrained decoding: some tokens allowed
+        keep = g.integers(0, V, 5)
+        x, ordinary = np.full(V, -fill), x
+        x[keep] = ordinary[keep]
+    elif kind == "front":
+        x[:V - V // 3] = -fill
+    elif kind == "back":
+        x[V // 3:] = -fill
+    elif kind == "edge":           # outside the vectors, where the row is not aligned
+        x[[0, -1]] = -fill
+    elif kind == "some":
+        x[g.random(V) < 0.2] = -fill
+    elif kind == "large":
+        x[:] = fill
+    elif kind == "peak":
+        x[g.integers(0, V, 3)] = fill
+    elif kind in ("rising", "falling"):
+        x = np.linspace(-fill, fill, V)[::1 if kind == "rising" else -1]
+    else:
+        x = x + 2 ** 20 / (scale * np.log2(np.e))
+        x = x if kind == "border" else -x
+    return x
+
+
+def masked_rows(rows, V, scale, dtype):
+    g = rng(rows + V)
+    each = [(k, f) for f in FILLS for k in KINDS]
+    # 59 has no factor with the 132 combinations: any number of rows takes fills and kinds of all sorts
+    return stored(np.array([masked_row(g, *each[59 * i % len(each)], V, scale) for i in range(rows)]), dtype)
+
+
+MASKED = [(132, 9001), (70, 30523), (16, 70001), (330, 4203), (660, 4203), (1320, 4201)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,V", MASKED)
+@pytest.mark.parametrize("scale", [0.7, 1.0, 1.5])
+def test_finite_masks_and_large_logits(torch, dtype, rows, V, scale):
+    """Clusters of several sizes and every size of a CTA; rows of odd length that start anywhere."""
+    x = masked_rows(rows, V, scale, dtype)
+    tok = rng(V).integers(0, V, rows)
+    k = (1, 5, 20)[V % 3]
+    check_logprobs(torch, x, V, tok, scale, k, dtype)
+    check_logprobs(torch, x, V, tok, scale, 0, dtype)
+    check_logprobs_grad(torch, x, V, tok, scale, dtype, "both")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", KINDS)
+def test_finite_masks_in_one_row_over_a_cluster(torch, dtype, kind):
+    """A generated token's row, a call for each size of the mask."""
+    g, V = rng(17), 128000
+    for fill in FILLS:
+        x = stored(masked_row(g, kind, fill, V, 1.25)[None], dtype)
+        check_logprobs(torch, x, V, np.array([g.integers(0, V)]), 1.25, 20, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [1, 2, 9, 255])
+def test_finite_masks_in_short_rows(torch, dtype, V):
+    """Rows of no or few vectors: most of their elements are edges."""
+    g = rng(V)
+    x = stored(np.array([masked_row(g, k, f, V, 1.0) for f in FILLS for k in KINDS]), dtype)
+    tok = g.integers(0, V, len(x))
+    check_logprobs(torch, x, V, tok, 1.0, 1, dtype)
+    check_logprobs_grad(torch, x, V, tok, 1.0, dtype, "logp")
