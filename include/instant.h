@@ -584,8 +584,9 @@ instant_status instant_token_logprobs_grad(const void* x, const void* tokens, in
  *   ws     device scratch of instant_grad_clip_workspace_bytes(count) bytes, 16-byte
  *          aligned; contents are overwritten
  * An N that is not finite in fp32 clips nothing (f = 1), and the caller sees it.  The
- * sums are taken in a fixed order, in fp32 over at most a few hundred values and in 64 bits
- * from there on.  With every out its g and scale f = 1 nothing is written.
+ * sums are taken in a fixed order: squares of values between 2^-50 and 2^40 in fp32 over
+ * at most 65 and in two fp32 words (some 48 bits) from there on, others in 64 bits.  With
+ * every out its g and scale f = 1 nothing is written.
  * No output may overlap another tensor; max_norm > 0 (infinity: the norm alone), scale
  * finite and positive.  The list is read before the call returns.
  */

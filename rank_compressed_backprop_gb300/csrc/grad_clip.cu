@@ -4,14 +4,14 @@
 // Bound by HBM: each gradient is read once for the norm and once more to be scaled,
 // the second time from L2 as far as it holds them, and written once.  The tensors are
 // cut into chunks of kBytes that the CTAs take in turn, so the list may mix matrices with
-// scalars.  k_grad_norm leaves a partial sum of squares a CTA, in 64
-// bits; every CTA of k_grad_clip adds them in the same order and gets the same factor.
+// scalars.  k_grad_norm leaves a partial sum of squares a CTA (ClipPart); every CTA of
+// k_grad_clip adds them in the same order and gets the same factor.
 // The pointers travel in the launch's parameters: nothing is copied to the device, and
 // a captured graph holds its own list.
 //
-// Squares are added in fp32 within a chunk, in two fp32 words over a CTA's and in 64 bits from
-// there on; vectors of very large or very small values in 64 bits at once, so that no
-// gradient leaves the range of fp32.
+// Squares are added in fp32 within a chunk (65 of a thread's at most) and in two fp32 words over
+// a CTA's chunks and over the CTAs; vectors of very large or very small values in 64 bits
+// throughout.  The two sums meet in 64 bits, before the root.
 #include <algorithm>
 
 #include "ckpt.cuh"
@@ -107,7 +107,9 @@ struct ChunkAt {
   __device__ __forceinline__ long long at(long long v) const { return head + v * kPer<T>; }
 };
 
-constexpr float kLarge = 1125899906842624.f;       // 2^50
+// Bounds of the values whose squares are added in fp32: 2^31 chunks of 2^14 values are 2^45 squares
+// of at most 2^80, and their sum stays below 2^128
+constexpr float kLarge = 1099511627776.f;          // 2^40
 constexpr float kSmall = 8.8817841970012523e-16f;  // 2^-50
 
 // Adds the squares of a thread's values to a sum in fp32 while the largest of them lies

@@ -1,12 +1,12 @@
 """The operators at the ends of a language model over the whole range of their values and
 sizes: finite masks of any size, logits around the bound between the two forms of an
-exponent."""
+exponent, gradients around the bounds between the sums of their squares."""
 
 import numpy as np
 import pytest
 
-from gpu_util import rng, stored, torch_or_skip
-from test_gpu_p_lm import check_logprobs, check_logprobs_grad
+from gpu_util import nan_like, rng, stored, torch_or_skip
+from test_gpu_p_lm import H, U, check_clip, check_logprobs, check_logprobs_grad, close
 
 pytestmark = pytest.mark.gpu
 
@@ -14,6 +14,12 @@ pytestmark = pytest.mark.gpu
 @pytest.fixture(scope="module")
 def torch():
     return torch_or_skip()
+
+
+def _api():
+    from rank_compressed_backprop_gb300 import api
+
+    return api
 
 
 # ---------------------------------------------------------------------------
@@ -95,3 +101,33 @@ def test_finite_masks_in_short_rows(torch, dtype, V):
     tok = g.integers(0, V, len(x))
     check_logprobs(torch, x, V, tok, 1.0, 1, dtype)
     check_logprobs_grad(torch, x, V, tok, 1.0, dtype, "logp")
+
+
+# ---------------------------------------------------------------------------
+# the norm's range
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("size", [1.1 * 2.0 ** 39, 1.9 * 2.0 ** 39, 1.1 * 2.0 ** 40, 1.9 * 2.0 ** 49, 1.1 * 2.0 ** 50, 2.0 ** 63])
+def test_the_norm_of_many_large_gradients(torch, size):
+    """2^29 bf16 values whose squares add up to more than 2^128, or 2^30 below it: the norm is finite
+    in fp32, and clips."""
+    api = _api()
+    n = 1 << 29
+    g = torch.full((n,), size, device="cuda", dtype=torch.bfloat16)
+    v = float(g[0])
+    norm = nan_like(torch, (2,), torch.float32)
+    api.grad_clip([g], 2.0 ** 40, norm)
+    want = v * n ** 0.5
+    f = min(1.0, 2.0 ** 40 / want)
+    # as for other lists: 65 squares of a chunk in fp32, then the root, the quotient and the product
+    close(norm, [want, f], np.array([want, f]) * 36 * U, "norm")
+    lo, hi = torch.aminmax(g)
+    assert float(lo) == float(hi) and abs(float(hi) - v * f) <= v * f * (36 * U + 1.01 * H["bf16"])
+
+
+@pytest.mark.parametrize("size", [2.0 ** -50, 2.0 ** -49, 2.0 ** 39, 2.0 ** 40, 2.0 ** 49, 2.0 ** 50])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gradients_about_the_bounds_of_plain_squares(torch, size, dtype):
+    """Values on both sides of the bounds between sums in fp32 and in 64 bits."""
+    g = rng(6)
+    a = stored(size * np.exp2(g.uniform(-2, 2, 70001)) * g.choice([-1, 1], 70001), dtype)
+    check_clip(torch, [a, stored(size * g.standard_normal(333), dtype)], [dtype] * 2, size)
