@@ -131,3 +131,36 @@ def test_gradients_about_the_bounds_of_plain_squares(torch, size, dtype):
     g = rng(6)
     a = stored(size * np.exp2(g.uniform(-2, 2, 70001)) * g.choice([-1, 1], 70001), dtype)
     check_clip(torch, [a, stored(size * g.standard_normal(333), dtype)], [dtype] * 2, size)
+
+
+@pytest.mark.parametrize("count", [32, 33, 120, 121, 128, 129, 400, 401, 512, 513, 940, 941, 1880, 1881])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_as_many_gradients_as_a_launch_takes_and_one_more(torch, count, in_place):
+    g = rng(count)
+    dtypes = ["bf16" if i % 4 == 0 else "f32" for i in range(count)]
+    check_clip(torch, [stored(g.standard_normal(1 + (i * 37) % 300), d) for i, d in enumerate(dtypes)], dtypes, 1.0,
+               in_place=in_place)
+
+
+@pytest.mark.parametrize("count", [20, 100, 500, 900, 1000])
+@pytest.mark.parametrize("in_place,scale", [(False, 1.0), (True, 0.5)])
+def test_long_lists_of_many_tensors(torch, count, in_place, scale):
+    """More than 64 MB in lists of every size, of two launches too: a CTA a chunk where they are written."""
+    api = _api()
+    gen = torch.Generator("cuda").manual_seed(count)
+    sizes = [40_000_000 // count + (i * 977) % 5000 for i in range(count)]
+    g = [torch.randn(n, generator=gen, device="cuda") for n in sizes]
+    for i in range(0, count, 3):
+        g[i] = g[i].bfloat16()
+    keep = [t.clone() for t in g]
+    outs = g if in_place else [nan_like(torch, t.shape, t.dtype) for t in g]
+    norm = nan_like(torch, (2,), torch.float32)
+    api.GradClip(g, None if in_place else outs)(1.0, norm, scale=scale)
+    n = scale * float(torch.sqrt(sum(t.double().square().sum() for t in keep)))
+    close(norm, [n, 1 / n], np.array([n, 1 / n]) * 36 * U, "norm")
+    for o, k in zip(outs, keep):
+        want = k.double() * (scale / n)
+        h = H["bf16" if o.dtype == torch.bfloat16 else "f32"]
+        assert bool(((o.double() - want).abs() <= want.abs() * (36 * U + 1.01 * h)).all())
+    if not in_place:
+        assert all(torch.equal(a, b) for a, b in zip(g, keep))
