@@ -7,7 +7,8 @@
 // Both are bound by HBM.  The gradient's sums are taken in fp32 in the order of i, the
 // same bits on every call: the positions are sorted by token (stably), and
 //   k_embed_sort  up to kSortMax positions in one cluster, in shared memory; more go through
-//                 k_sort_count and k_sort_move, eight bits of the token at a time
+//                 k_sort_count, k_sort_scan (of many) and k_sort_move, eight bits of the
+//                 token at a time
 //   k_embed_zero  zeros over the table's gradient, while the cluster sorts; up to kSortAlone
 //                 positions one CTA sorts, and others of its launch write the zeros
 //   k_embed_sum   a warp sums kSegment neighbouring positions of the sorted order in its
@@ -311,14 +312,19 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_zero(float* p, size_t n,
 }
 
 // --- more positions than a cluster holds: tiles of 1024 to 16384 positions, a CTA each, and
-// eight bits in two launches: the tiles' counts of each digit, and the move to where they say
+// eight bits in two launches: the tiles' counts of each digit, and the move to where they say.
+// A CTA of the move adds up the counts of all tiles, work that grows with their square: from
+// kScanTiles tiles on k_sort_scan does that between the two, for a launch (us without / with it over
+// 50000 x 8: 128 tiles 35.6 / 39.0, 196 54 / 54, 256 64.0 / 58.4, 512 1375 / 1338; over 60000 x 8, 8192
+// tiles 30.5 / 24.3 ms).
 constexpr int kTileItems = 16;  // positions a thread, at most
+constexpr int kScanTiles = 200;
 struct SortPass {
   const void* tokens;       // first pass: the tokens, else null
   int wide, V, n, bit, tiles, items;
   const uint32_t *key0, *pos0;
   uint32_t *key, *pos;
-  uint32_t* count;          // [tiles][kDigits]
+  uint32_t* count;          // [tiles][kDigits], and of kScanTiles tiles or more another row
 };
 
 __device__ __forceinline__ uint32_t pass_key(const SortPass& p, int i) {
@@ -339,6 +345,39 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_count(const __grid_consta
   if (threadIdx.x < kDigits) p.count[static_cast<size_t>(blockIdx.x) * kDigits + threadIdx.x] = count[threadIdx.x];
 }
 
+// The counts of a digit become the sums over the tiles before, and those over all go to a row
+// behind them, so that k_sort_move reads two rows.  A CTA takes 32
+// digits, a warp of it neighbouring tiles, each twice.
+__global__ void __launch_bounds__(kSortThreads) k_sort_scan(const __grid_constant__ SortPass p) {
+  __shared__ uint32_t sum[kSortWarps][32];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int each = (p.tiles + kSortWarps - 1) / kSortWarps;
+  const int t0 = min(p.tiles, warp * each), t1 = min(p.tiles, t0 + each);
+  uint32_t* count = p.count + blockIdx.x * 32 + lane;
+  uint32_t at = 0;
+#pragma unroll 8
+  for (int t = t0; t < t1; ++t) at += count[static_cast<size_t>(t) * kDigits];
+  sum[warp][lane] = at;
+  __syncthreads();
+  at = 0;
+  for (int w = 0; w < warp; ++w) at += sum[w][lane];
+  if (warp == kSortWarps - 1) count[static_cast<size_t>(p.tiles) * kDigits] = at + sum[warp][lane];
+  for (int t = t0; t < t1; t += 8) {
+    uint32_t c[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = t + i < t1 ? count[static_cast<size_t>(t + i) * kDigits] : 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (t + i < t1) count[static_cast<size_t>(t + i) * kDigits] = at;
+      at += c[i];
+    }
+  }
+}
+
+// SCANNED: k_sort_scan has been over the counts
+template <bool SCANNED>
 __global__ void __launch_bounds__(kSortThreads) k_sort_move(const __grid_constant__ SortPass p) {
   __shared__ uint32_t counts[kSortWarps][kDigits];
   __shared__ uint32_t lower[4][kDigits], total[4][kDigits], red[kDigits / 32];
@@ -350,11 +389,18 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_move(const __grid_constan
   {
     const int digit = tid & (kDigits - 1), q = tid / kDigits;
     uint32_t low = 0, all = 0;
+    if constexpr (SCANNED) {
+      if (q == 0) {
+        low = p.count[static_cast<size_t>(blockIdx.x) * kDigits + digit];
+        all = p.count[static_cast<size_t>(p.tiles) * kDigits + digit];
+      }
+    } else {
 #pragma unroll 8
-    for (int t = q; t < p.tiles; t += 4) {
-      const uint32_t c = p.count[static_cast<size_t>(t) * kDigits + digit];
-      all += c;
-      low += t < static_cast<int>(blockIdx.x) ? c : 0;
+      for (int t = q; t < p.tiles; t += 4) {
+        const uint32_t c = p.count[static_cast<size_t>(t) * kDigits + digit];
+        all += c;
+        low += t < static_cast<int>(blockIdx.x) ? c : 0;
+      }
     }
     lower[q][digit] = low;
     total[q][digit] = all;
@@ -701,12 +747,16 @@ int tiles_of(int rows) {
   const long long tile = static_cast<long long>(tile_items(rows)) * kSortThreads;
   return static_cast<int>((rows + tile - 1) / tile);
 }
+size_t count_bytes(int rows) {  // a row of counts a tile, and one of sums
+  const int tiles = tiles_of(rows);
+  return up256(static_cast<size_t>(tiles + (tiles >= kScanTiles)) * kDigits * 4);
+}
 
 }  // namespace
 
 size_t embed_grad_bytes(int rows, int C) {
   const size_t words = up256(static_cast<size_t>(rows) * 4);
-  const size_t sort = rows <= kSortMax ? 2 * words : 4 * words + up256(static_cast<size_t>(tiles_of(rows)) * kDigits * 4);
+  const size_t sort = rows <= kSortMax ? 2 * words : 4 * words + count_bytes(rows);
   const size_t strips = (C + strip_of(C, false) - 1) / strip_of(C, false);  // bf16 has half as many
   const size_t counts = rows <= kSortAlone ? up256(blocks_of(rows) * strips * 4) : 0;
   return sort + counts + static_cast<size_t>(2) * blocks_of(rows) * C * 4;
@@ -779,7 +829,8 @@ cudaError_t launch_embed_grad(EmbedGradArgs a, void* ws, bool bf16, cudaStream_t
     p.items = tile_items(n);
     uint32_t* key1 = take(words);
     uint32_t* pos1 = take(words);
-    p.count = take(up256(static_cast<size_t>(p.tiles) * kDigits * 4));
+    p.count = take(count_bytes(n));
+    const bool scan = p.tiles >= kScanTiles;
     int passes = 1;
     while (passes < 4 && (static_cast<uint32_t>(a.V) >> (8 * passes)) != 0) ++passes;
     // the last pass ends in a.key, a.pos
@@ -789,7 +840,11 @@ cudaError_t launch_embed_grad(EmbedGradArgs a, void* ws, bool bf16, cudaStream_t
       p.key = last ? a.key : key1;
       p.pos = last ? a.pos : pos1;
       e = launch_ex(k_sort_count, dim3(p.tiles), dim3(kSortThreads), 0, st, 1, pdl_enabled(), p);
-      if (e == cudaSuccess) e = launch_ex(k_sort_move, dim3(p.tiles), dim3(kSortThreads), 0, st, 1, pdl_enabled(), p);
+      if (e == cudaSuccess && scan)
+        e = launch_ex(k_sort_scan, dim3(kDigits / 32), dim3(kSortThreads), 0, st, 1, pdl_enabled(), p);
+      if (e == cudaSuccess)
+        e = launch_ex(scan ? k_sort_move<true> : k_sort_move<false>, dim3(p.tiles), dim3(kSortThreads), 0, st, 1,
+                      pdl_enabled(), p);
       p.tokens = nullptr;
       p.key0 = p.key;
       p.pos0 = p.pos;

@@ -164,3 +164,58 @@ def test_long_lists_of_many_tensors(torch, count, in_place, scale):
         assert bool(((o.double() - want).abs() <= want.abs() * (36 * U + 1.01 * h)).all())
     if not in_place:
         assert all(torch.equal(a, b) for a, b in zip(g, keep))
+
+
+# ---------------------------------------------------------------------------
+# more positions than the tiles of a few launches
+# ---------------------------------------------------------------------------
+def call_ms(torch, f, calls):
+    """Time of a call among `calls`, the best of three runs."""
+    f()
+    best = float("inf")
+    for _ in range(3):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        for _ in range(calls):
+            f()
+        b.record()
+        b.synchronize()
+        best = min(best, a.elapsed_time(b) / calls)
+    return best
+
+
+def test_a_table_gradient_takes_time_in_proportion_to_its_positions(torch):
+    """2^29 positions in 32768 tiles against 2^23 in 512."""
+    api = _api()
+    V, C = 1000, 8
+    gen = torch.Generator("cuda").manual_seed(1)
+    per = []
+    for rows in (1 << 23, 1 << 29):
+        tok = torch.randint(0, V, (rows,), generator=gen, device="cuda", dtype=torch.int32)
+        gy = torch.ones(rows, C, device="cuda", dtype=torch.bfloat16)
+        gt, ws = nan_like(torch, (V, C), torch.float32), api.embed_grad_workspace(rows, V, C, "cuda")
+        per.append(call_ms(torch, lambda: api.embed_grad(gy, tok, gt, ws), 2) / rows)
+        assert torch.equal(gt, torch.bincount(tok, minlength=V).float()[:, None].expand(V, C))
+    assert per[1] <= 1.5 * per[0]
+
+
+@pytest.mark.parametrize("rows", [199 * 1024, 199 * 1024 + 1, 304 * 1024, 199 * 2048 + 1, 304 * 16384 + 5])
+def test_table_gradients_of_as_many_tiles_as_are_scanned(torch, rows):
+    """199 and 200 tiles of 1024 positions, 304 of them, 200 of 2048, and more than 304 of 16384."""
+    api, V, C = _api(), 70001, 4
+    gen = torch.Generator("cuda").manual_seed(rows)
+    tok = torch.randint(-3, V, (rows,), generator=gen, device="cuda")
+    gy = torch.randint(-8, 9, (rows, C), generator=gen, device="cuda").float()
+    ws = api.embed_grad_workspace(rows, V, C, "cuda").fill_(0xff)
+    gt = nan_like(torch, (V, C), torch.float32)
+    api.embed_grad(gy, tok, gt, ws)
+    # small whole numbers: their sums are exact in any order
+    want = torch.zeros(V + 1, C, device="cuda", dtype=torch.float64)
+    want.index_add_(0, torch.where(tok < 0, V, tok), gy.double())
+    assert torch.equal(gt, want[:V].float())
+    again = nan_like(torch, (V, C), torch.float32)
+    g2 = torch.randn(rows, C, generator=gen, device="cuda")
+    api.embed_grad(g2, tok, gt, ws)
+    api.embed_grad(g2, tok, again, ws.fill_(0xff))
+    assert torch.equal(gt, again)
+    assert api.device_status() == 0
