@@ -550,7 +550,7 @@ size_t instant_embed_grad_workspace_bytes(int rows, int V, int C);
  * A row of minus infinities has stats, logp and top_logp of minus infinity and entropy
  * 0.  A NaN or plus infinity makes a row's results NaN.
  * Limits: 0 <= top <= min(V, INSTANT_TOP_MAX), rows <= 2^30, V <= ld <= 2^24; scale
- * finite and positive.  Rows may start anywhere (ld of any size).
+ * between 2^-120 and 2^120.  Rows may start anywhere (ld of any size).
  */
 instant_status instant_token_logprobs(const void* x, const void* tokens, int token_bytes, float* logp,
                                       float* stats, float* entropy, long long* top_ids, float* top_logp,
@@ -566,6 +566,7 @@ instant_status instant_token_logprobs(const void* x, const void* tokens, int tok
  *   g_entropy, entropy [rows], or both NULL
  *   gx [rows, ld] dtype dt, zero in the columns from V on; may be x
  * Rows without a token have no part in g_logp; a row of minus infinities has gradient 0.
+ * Limits as in instant_token_logprobs.
  */
 instant_status instant_token_logprobs_grad(const void* x, const void* tokens, int token_bytes,
                                            const float* stats, const float* g_logp,

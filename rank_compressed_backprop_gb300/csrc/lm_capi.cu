@@ -23,6 +23,9 @@ constexpr int kMaxRows = 1 << 30, kMaxV = 1 << 24;
 bool embed_shape_ok(int rows, int V, int C) {
   return rows >= 1 && rows <= kMaxRows && V >= 1 && V <= kMaxV && C >= 1 && C <= INSTANT_EMBED_MAX_C;
 }
+// within 2^-120 .. 2^120: the scale times log2 e is finite, and a difference of two logits that passes the
+// range of fp32 has a weight of 0 (beyond 2^128 2^-120 log2 e its exponent is -369)
+bool logits_scale_ok(float scale) { return scale >= 0x1p-120f && scale <= 0x1p120f; }
 bool logits_shape_ok(int rows, int V, int ld) {
   return rows >= 1 && rows <= kMaxRows && V >= 1 && V <= ld && ld <= kMaxV;
 }
@@ -156,7 +159,7 @@ instant_status instant_token_logprobs(const void* x, const void* tokens, int tok
                                       int top, float scale, instant_dtype dt, void* stream) {
   if (!dtype_ok(dt) || !tokens_ok(token_bytes)) return INSTANT_ERR_DTYPE;
   if (!x || !(logp || stats || entropy || top_ids || top_logp) || (logp && !tokens) ||
-      !(std::isfinite(scale) && scale > 0.f))
+      !logits_scale_ok(scale))
     return INSTANT_ERR_ARG;
   if ((top == 0) != !(top_ids || top_logp)) return INSTANT_ERR_ARG;
   if (!logits_shape_ok(rows, V, ld) || top < 0 || top > INSTANT_TOP_MAX || top > V) return INSTANT_ERR_SHAPE;
@@ -186,7 +189,7 @@ instant_status instant_token_logprobs_grad(const void* x, const void* tokens, in
                                            void* stream) {
   if (!dtype_ok(dt) || !tokens_ok(token_bytes)) return INSTANT_ERR_DTYPE;
   if (!x || !stats || !gx || !(g_logp || g_entropy) || (g_logp && !tokens) || (!g_entropy != !entropy) ||
-      !(std::isfinite(scale) && scale > 0.f))
+      !logits_scale_ok(scale))
     return INSTANT_ERR_ARG;
   if (!logits_shape_ok(rows, V, ld)) return INSTANT_ERR_SHAPE;
   if (!aligned(x, 16) || !aligned(tokens, token_bytes) || !aligned(stats, 8) || !aligned(g_logp, 4) ||

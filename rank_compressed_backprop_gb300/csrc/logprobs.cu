@@ -190,6 +190,11 @@ struct Part {
   }
 };
 
+// scale (x - m) - log S; halves, as the difference may pass the range of fp32 where the product does not
+__device__ __forceinline__ float log_prob(float x, float m, float scale, float logs) {
+  return fmaf(2.f * scale, 0.5f * x - 0.5f * m, -logs);
+}
+
 // the part of a row that one CTA reads: 16-byte vectors, and for the first CTA of
 // the row the elements before the first boundary and after the last
 template <typename T>
@@ -712,7 +717,7 @@ __global__ void __launch_bounds__(NT, CTAS) k_logprobs(const __grid_constant__ L
   const bool none = p.m == -inf_f();
   const float logs = p.log_sum(c);
   if (lane == 0) {
-    if (a.logp) a.logp[row] = token < 0 ? 0.f : none ? -inf_f() : fmaf(a.scale, xt - p.m, -logs);
+    if (a.logp) a.logp[row] = token < 0 ? 0.f : none ? -inf_f() : log_prob(xt, p.m, a.scale, logs);
     if (a.stats) reinterpret_cast<float2*>(a.stats)[row] = make_float2(p.m, logs);
     if (ENT) a.entropy[row] = none ? 0.f : fmaf(-kLn2, p.a / p.s, logf(p.s));
   }
@@ -720,7 +725,7 @@ __global__ void __launch_bounds__(NT, CTAS) k_logprobs(const __grid_constant__ L
     const uint32_t id = key_index(top.best[lane]);
     const size_t o = static_cast<size_t>(row) * a.top + lane;
     if (a.top_ids) a.top_ids[o] = id;
-    if (a.top_logp) a.top_logp[o] = none ? -inf_f() : fmaf(a.scale, key_value(top.best[lane]) - p.m, -logs);
+    if (a.top_logp) a.top_logp[o] = none ? -inf_f() : log_prob(key_value(top.best[lane]), p.m, a.scale, logs);
   }
 }
 

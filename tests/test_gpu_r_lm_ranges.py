@@ -103,6 +103,23 @@ def test_finite_masks_in_short_rows(torch, dtype, V):
     check_logprobs_grad(torch, x, V, tok, 1.0, dtype, "logp")
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", [2.0 ** -120, 2.0 ** -119.5, 2.0 ** -60, 0.25, 1.0, 2.0 ** 60, 2.0 ** 120])
+def test_logits_over_the_whole_range_at_the_smallest_and_largest_scales(torch, dtype, scale):
+    """Differences of logits beyond the type's range, whose product with the scale is within it."""
+    g = rng(3)
+    for rows, V in ((6, 7), (6, 2600), (330, 300)):
+        x = g.standard_normal((rows, V)) * 2.5
+        x[:, ::3] = g.choice([-3.38e38, -1e38, 1e38], (rows, len(x[0, ::3])))
+        x[::2, 1] = 3e38
+        x[1::3] = g.standard_normal((len(x[1::3]), V))
+        x = stored(x, dtype)
+        tok = np.zeros(rows, int)
+        check_logprobs(torch, x, V, tok, scale, 2, dtype)
+        if scale <= 1:             # beyond, the gradient itself passes the range
+            check_logprobs_grad(torch, x, V, tok, scale, dtype, "both")
+
+
 # ---------------------------------------------------------------------------
 # the norm's range
 # ---------------------------------------------------------------------------

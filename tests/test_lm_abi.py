@@ -73,6 +73,12 @@ def test_token_logprobs_refusals(L):
     assert L.instant_launch_count() == n0
 
 
+def test_scales_that_no_logits_are_multiplied_by(L):
+    for scale in (2.0 ** -121, 2.0 ** 121, 3e38, 1e-45, -2.0):
+        assert L.instant_token_logprobs(F, F, 8, F, F, F, F, F, 4, 100, 104, 5, scale, 1, None) == ARG
+        assert L.instant_token_logprobs_grad(F, F, 4, F, F, F, F, F, 4, 100, 104, scale, 1, None) == ARG
+
+
 def test_grad_clip_refusals(L):
     from rank_compressed_backprop_gb300._lib import GradItem
 
