@@ -236,3 +236,35 @@ def test_table_gradients_of_as_many_tiles_as_are_scanned(torch, rows):
     api.embed_grad(g2, tok, again, ws.fill_(0xff))
     assert torch.equal(gt, again)
     assert api.device_status() == 0
+
+
+# ---------------------------------------------------------------------------
+# the largest tables and widths
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype,rows,V,C", [("bf16", 300, 1 << 24, 8), ("f32", 5000, 1 << 24, 3), ("f32", 40000, 1 << 24, 4),
+                                            ("bf16", 300, 9, 65536), ("bf16", 3000, 9, 65536), ("f32", 300, 9, 65535),
+                                            ("f32", 2100, 9, 65535), ("f32", 33000, 5, 4097)])
+def test_the_largest_tables_and_widths(torch, dtype, rows, V, C):
+    """A table of 2^24 rows takes a fourth pass of the sort; its last rows, its first and none."""
+    api = _api()
+    gen = torch.Generator("cuda").manual_seed(rows + C)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    tok = torch.randint(0, V, (rows,), generator=gen, device="cuda")
+    tok[::3] = V - 1 - torch.arange(len(tok[::3]), device="cuda") % min(V, 11)
+    tok[::7] = 0
+    tok[::13] = -1
+    gy = torch.randint(-8, 9, (rows, C), generator=gen, device="cuda").to(dt)
+    ws = api.embed_grad_workspace(rows, V, C, "cuda").fill_(0xff)
+    gt = nan_like(torch, (V, C), torch.float32)
+    api.embed_grad(gy, tok, gt, ws)
+    # whole numbers below 2^24: their sums are exact in any order
+    want = torch.zeros(V, C, device="cuda").index_add_(0, tok.clamp(min=0), gy.float() * (tok >= 0)[:, None])
+    assert torch.equal(gt, want)
+    api.embed_grad(gy, tok, gt, ws, scale=-1.0, accumulate=True)
+    assert int(gt.count_nonzero()) == 0
+    y = nan_like(torch, (rows, C), dt)
+    table = torch.zeros(V, C, device="cuda", dtype=dt)
+    table[tok.clamp(min=0)] = gy                       # some position's row for each token
+    api.embed(tok, table, y)
+    assert torch.equal(y, torch.where((tok >= 0)[:, None], table[tok.clamp(min=0)], 0))
+    assert api.device_status() == 0
