@@ -441,7 +441,7 @@ struct LogprobArgs {
   long long* top_ids;           // [rows, top] or null
   float* top_logp;              // [rows, top] or null
   int wide, rows, V, ld, top;
-  float scale;
+  float scale, near;            // near: set by the launch
 };
 struct LogprobGradArgs {
   const void *x, *tokens;
@@ -450,7 +450,7 @@ struct LogprobGradArgs {
   int wide, rows, V, ld;
   float scale;
 };
-cudaError_t launch_logprobs(const LogprobArgs& a, bool bf16, cudaStream_t st);
+cudaError_t launch_logprobs(LogprobArgs a, bool bf16, cudaStream_t st);
 cudaError_t launch_logprobs_grad(const LogprobGradArgs& a, bool bf16, cudaStream_t st);
 
 struct ClipItem {

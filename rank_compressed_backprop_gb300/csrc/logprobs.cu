@@ -154,39 +154,41 @@ __device__ __forceinline__ uint32_t key_index(uint64_t key) { return ~static_cas
 // Running maximum and sums of a part of a row.  An exponent is taken as w = x c - mc with
 // c = scale log2 e and mc = m c rounded, one FMA; rest = m c - mc, by which the rounding
 // shifts all of them, is put right in the row's log S.  That is so while |m c| is at most
-// kNear, where the rest is below 2^-5; from 2^31 on 2^rest itself would leave the range of
+// 2^20, where the rest is below 2^-5; from 2^31 on 2^rest itself would leave the range of
 // fp32.  Larger maxima (a row masked whole by some -1e10, one of the type's lowest values)
 // and very large or small scales take w as (x - m) c instead.
+struct Scale {
+  float c, near;  // near: the largest |m| of the first form
+};
 struct Part {
-  static constexpr float kNear = 1048576.f;  // 2^20
   float m, s, a;  // max, sum 2^w, sum w 2^w
-  __device__ __forceinline__ static bool careful(float m, float c) {
-    return !(fabsf(m) * c <= kNear && c >= 1e-30f && c <= 10.f);
+  __device__ __forceinline__ static bool careful(float m, const Scale& b) { return !(fabsf(m) <= b.near); }
+  __device__ __forceinline__ static float ref(float m, const Scale& b) { return __fmul_rn(m, b.c); }  // mc, in no FMA
+  __device__ __forceinline__ static float rest(float m, const Scale& b) {
+    return careful(m, b) ? 0.f : fmaf(m, b.c, -ref(m, b));
   }
-  __device__ __forceinline__ static float ref(float m, float c) { return __fmul_rn(m, c); }  // mc, in no FMA
-  __device__ __forceinline__ static float rest(float m, float c) { return careful(m, c) ? 0.f : fmaf(m, c, -ref(m, c)); }
   // Moves the sums to another maximum (at least m, or a NaN), from the one form of an exponent
   // to the other where that changes.  s is finite, at most the number of its elements and 2^(2^-5).
   template <bool ENT>
-  __device__ __forceinline__ void move(float m1, float c) {
-    float t = ref(m, c) - ref(m1, c);
-    if (__builtin_expect(careful(m, c) || careful(m1, c), 0)) t = fmaf(m - m1, c, rest(m1, c) - rest(m, c));
+  __device__ __forceinline__ void move(float m1, const Scale& b) {
+    float t = ref(m, b) - ref(m1, b);
+    if (careful(m, b) || careful(m1, b)) t = fmaf(m - m1, b.c, rest(m1, b) - rest(m, b));
     const float f = m == -inf_f() ? 0.f : ex2_approx(t);
     if (ENT) a = f == 0.f ? 0.f : f * fmaf(t, s, a);  // t may be huge where f is 0
     s = f * s;
     m = m1;
   }
   template <bool ENT>
-  __device__ __forceinline__ void join(Part o, float c) {
+  __device__ __forceinline__ void join(Part o, const Scale& b) {
     const float m1 = max_nan(m, o.m);
-    if (!(m1 == m)) move<ENT>(m1, c);
-    if (!(m1 == o.m)) o.move<ENT>(m1, c);
+    if (!(m1 == m)) move<ENT>(m1, b);
+    if (!(m1 == o.m)) o.move<ENT>(m1, b);
     s += o.s;
     a += o.a;
   }
   // log S from s: S = s 2^-rest
-  __device__ __forceinline__ float log_sum(float c) const {
-    return m == -inf_f() ? m : fmaf(-kLn2, rest(m, c), logf(s));
+  __device__ __forceinline__ float log_sum(const Scale& b) const {
+    return m == -inf_f() ? m : fmaf(-kLn2, rest(m, b), logf(s));
   }
 };
 
@@ -502,6 +504,7 @@ __global__ void __launch_bounds__(NT, CTAS) k_logprobs(const __grid_constant__ L
   const T* x = static_cast<const T*>(a.x) + static_cast<size_t>(row) * a.ld;
   const Slice<T> sl(x, a.V, rank, shares);
   const float c = a.scale * kLog2e;
+  const Scale b{c, a.near};
   const bool first = rank == 0;
 
   long long token = -1;
@@ -529,11 +532,11 @@ __global__ void __launch_bounds__(NT, CTAS) k_logprobs(const __grid_constant__ L
     if (!(mb <= p.m)) {
       p.s = s2.x + s2.y;
       p.a = a2.x + a2.y;
-      p.move<ENT>(max_nan(mb, p.m), c);
+      p.move<ENT>(max_nan(mb, p.m), b);
       s2 = make_float2(p.s, 0.f);
       a2 = make_float2(p.a, 0.f);
-      mc = Part::ref(p.m, c);
-      careful = Part::careful(p.m, c);
+      mc = Part::ref(p.m, b);
+      careful = Part::careful(p.m, b);
     }
     if (!careful) {
 #pragma unroll
@@ -650,15 +653,15 @@ __global__ void __launch_bounds__(NT, CTAS) k_logprobs(const __grid_constant__ L
   if (edge) {
     Part e;
     e.m = xe;
-    const float w = Part::careful(e.m, c) ? e.m - e.m : Part::rest(e.m, c);  // NaN for an infinity
+    const float w = Part::careful(e.m, b) ? e.m - e.m : Part::rest(e.m, b);  // NaN for an infinity
     e.s = e.m == -inf_f() ? 0.f : ex2_approx(w);
     e.a = e.m == -inf_f() ? 0.f : w * e.s;
-    p.join<ENT>(e, c);
+    p.join<ENT>(e, b);
   }
   // over the warp, then over the CTA
   auto warp_join = [&](Part& q) {
     const float m1 = warp_max(q.m);
-    if (!(m1 == q.m)) q.move<ENT>(m1, c);
+    if (!(m1 == q.m)) q.move<ENT>(m1, b);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       q.s += __shfl_xor_sync(0xffffffffu, q.s, o);
@@ -715,7 +718,7 @@ __global__ void __launch_bounds__(NT, CTAS) k_logprobs(const __grid_constant__ L
   if (warp != 0) return;
   if (TOP && shares == 1) p = part;
   const bool none = p.m == -inf_f();
-  const float logs = p.log_sum(c);
+  const float logs = p.log_sum(b);
   if (lane == 0) {
     if (a.logp) a.logp[row] = token < 0 ? 0.f : none ? -inf_f() : log_prob(xt, p.m, a.scale, logs);
     if (a.stats) reinterpret_cast<float2*>(a.stats)[row] = make_float2(p.m, logs);
@@ -821,6 +824,9 @@ __global__ void __launch_bounds__(kThreads) k_logprobs_grad(const __grid_constan
   for (int i = a.V + tid; i < a.ld; i += kThreads) gx[i] = f_to_elem<T>(0.f);
 }
 
+// Scale::near, below 0 where no maximum is near
+float near_of(float c) { return c >= 1e-30f && c <= 10.f ? 1048576.f / c : -1.f; }
+
 // CTAs of a row: enough for `per_sm` CTAs an SM, with a vector or more for every thread
 int row_shares(int rows, int vecs, int threads, int per_sm, int most) {
   int n = 1;
@@ -832,7 +838,8 @@ int row_shares(int rows, int vecs, int threads, int per_sm, int most) {
 
 }  // namespace
 
-cudaError_t launch_logprobs(const LogprobArgs& a, bool bf16, cudaStream_t st) {
+cudaError_t launch_logprobs(LogprobArgs a, bool bf16, cudaStream_t st) {
+  a.near = near_of(a.scale * kLog2e);
   const int vecs = a.V / (bf16 ? 8 : 4);
   // Small CTAs hide one another's row ends, large ones are sooner done with a row when rows
   // are few.  us by shape, bf16, without / with five alternatives and entropy: 8192 x 6000
