@@ -584,7 +584,8 @@ instant_status instant_token_logprobs_grad(const void* x, const void* tokens, in
  *   norm   [2] fp32: N and f
  *   ws     device scratch of instant_grad_clip_workspace_bytes(count) bytes, 16-byte
  *          aligned; contents are overwritten
- * An N that is not finite in fp32 clips nothing (f = 1), and the caller sees it.  The
+ * An N that is not finite in fp32 clips nothing (f = 1), and the caller sees it; an f
+ * below 2^-126 has the fewer bits of a subnormal number.  The
  * sums are taken in a fixed order: squares of values between 2^-50 and 2^40 in fp32 over
  * at most 65 and in two fp32 words (some 48 bits) from there on, others in 64 bits.  With
  * every out its g and scale f = 1 nothing is written.

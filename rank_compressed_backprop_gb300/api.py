@@ -954,8 +954,8 @@ def _ptrs(tensors):
 
 def _clip_ptrs(grads, outs):
     """The pointers of both lists if all tensors are right for :class:`GradClip` and none shares
-    memory with another, else None: seen list by list (a GradClip of 400 gradients is made in 217 us
-    in place and 463 with other outputs, with a look at one tensor after the other in some 850)."""
+    memory with another, else None: seen list by list (a GradClip of 400 gradients is made in 240 us
+    in place and 470 with other outputs, with a look at one tensor after the other in some 850)."""
     try:
         dev, dts, nbytes = grads[0].get_device(), [g.dtype for g in grads], [g.nbytes for g in grads]
         at = to = all_at = _ptrs(grads)
@@ -1012,8 +1012,9 @@ def _refuse_clip(grads, outs):
 class GradClip:
     """The gradients of a model as one list: a call takes their common norm and clips
     them by it, in place or into ``outs`` (of the same shapes and dtypes).  The argument
-    block and the workspace are made once, so the tensors given here must stay alive and
-    in place; a call belongs to one stream at a time."""
+    block and the workspace are made once (of 400 gradients in 240 us, with other outputs
+    in 470), so the tensors given here must stay alive and in place; a call belongs to one
+    stream at a time."""
 
     def __init__(self, grads, outs=None):
         grads = list(grads)
@@ -1052,7 +1053,8 @@ class GradClip:
 
 def grad_clip(grads, max_norm: float, norm: torch.Tensor, *, outs=None, scale: float = 1.0,
               stream=None) -> torch.Tensor:
-    """One call of a :class:`GradClip` that is not kept."""
+    """One call of a :class:`GradClip` that is not kept; a program whose gradients stay in place
+    keeps one, as making it takes longer than the call."""
     with _on_stream(stream):  # the workspace comes from the pool of the stream that uses it
         clip = GradClip(grads, outs)
     return clip(max_norm, norm, scale=scale, stream=stream)

@@ -4,8 +4,10 @@
 //   gT_v (+)= scale sum of g_i over the i with t_i = v.
 // A token below zero is no token: its row of y is zero and it has no gradient.
 //
-// Both are bound by HBM.  The gradient's sums are taken in fp32 in the order of i, the
-// same bits on every call: the positions are sorted by token (stably), and
+// Both are bound by HBM.  The gradient's sums are taken in fp32 in a fixed order, the same
+// bits on every call: the positions are sorted by token (stably), eight neighbours of them are
+// added in order, then a CTA's eights in order; of a token that lies in many CTAs eight warps
+// add every eighth CTA's share, and their sums are added in order.
 //   k_embed_sort  up to kSortMax positions in one cluster, in shared memory; more go through
 //                 k_sort_count, k_sort_scan (of many) and k_sort_move, eight bits of the
 //                 token at a time
