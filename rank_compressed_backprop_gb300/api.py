@@ -868,7 +868,7 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None, logp: torc
                    top_logp: torch.Tensor | None = None, stream=None):
     """Log probabilities of the rows' tokens under ``softmax(scale * logits[:, :vocab])``:
     logits ``[rows, ld]``, tokens ``[rows]`` int32 or int64 (negative: none, its logp is
-    0), logp ``[rows]`` fp32.  Optional outputs: stats ``[rows, 2]`` (for
+    0), logp ``[rows]`` fp32; scale within 2^-120 .. 2^120.  Optional outputs: stats ``[rows, 2]`` (for
     :func:`token_logprobs_grad`) and entropy ``[rows]`` fp32, top_ids ``[rows, k]`` int64
     and top_logp ``[rows, k]`` fp32 of the k <= 32 likeliest tokens, ties by lower index.
     Returns logp."""
